@@ -8,6 +8,11 @@ The three entry points mirror ``include/gdn.h``:
             cu_seqlens=None) -> (dq, dk, dv, dbeta, dlog_alpha, ds0)
   decode_step(q, k, v, beta, log_alpha, state) -> o   (state updated in place)
 
+Beside them: linear attention with a constant decay per head
+(linear_attn_fwd, linear_attn_bwd, linear_attn_decode_step) and the group
+norm of a block's output with an activation or gate (group_norm_fwd,
+group_norm_bwd).
+
 Tensors are torch CUDA tensors (HIP device memory); torch is used only to
 allocate outputs / workspaces and to name the current stream.  The gate mode
 follows ``log_alpha``: None = no decay (delta rule), one value per
@@ -28,7 +33,9 @@ __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "chunk_fwd_conv", "gdn2_chunk_fwd",
            "gdn2_decode_step",
            "chunk_bwd", "decode_step", "decode_step_product",
            "chunk_fwd_product", "tree_verify",
-           "tree_commit", "FwdPlan", "GdnError",
+           "tree_commit", "linear_attn_fwd", "linear_attn_bwd",
+           "linear_attn_decode_step", "group_norm_fwd", "group_norm_bwd",
+           "FwdPlan", "GdnError",
            "abi_version", "stage_times"]
 
 _DT = {torch.float32: _lib.GDN_F32, torch.bfloat16: _lib.GDN_BF16}
@@ -544,3 +551,204 @@ def decode_step(q, k, v, beta, log_alpha, state):
                              _stream(q.device))
     _lib.check(st, "gdn_decode_step")
     return o
+
+
+# ------------------------------------------- linear attention, group norm ---
+
+class _On:
+    """Makes ``device`` current for a launch, where it is not already."""
+
+    def __init__(self, device):
+        self._guard = (None if device.index == torch.cuda.current_device()
+                       else torch.cuda.device(device))
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _want(t, name, shape, dtype, device):
+    """Checks an argument tensor; None passes."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _bytes(fn, p, *args):
+    need = ctypes.c_size_t(0)
+    _lib.check(fn(ctypes.byref(p), *args, ctypes.byref(need)), fn.__name__)
+    return need.value
+
+
+def _workspace(ws, need, device):
+    """The caller's workspace where it is large enough, else a new one."""
+    if ws is not None and ws.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    if ws is None or ws.numel() * ws.element_size() < need:
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    return ws, ws.numel() * ws.element_size()
+
+
+def _linattn_problem(q, k, v, log_decay, cu_seqlens, seg_chunks, lead):
+    """The problem of a linear-attention call; `lead`: dimensions in front of
+    the heads (batch and time, or the sequences of a decode step)."""
+    if q.dim() != lead + 2 or v.dim() != lead + 2:
+        raise ValueError(f"q and v must have {lead + 2} dimensions")
+    if not q.is_cuda:
+        raise ValueError("libgdn takes GPU tensors")
+    hq, dk = q.shape[lead:]
+    H, dv = v.shape[lead:]
+    _want(k, "k", q.shape, q.dtype, q.device)
+    _want(v, "v", (*q.shape[:lead], H, dv), q.dtype, q.device)
+    _want(log_decay, "log_decay", (H,), torch.float32, q.device)
+    _check_cu(cu_seqlens, q)
+    if cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2):
+        raise ValueError("cu_seqlens must hold the bounds of at least one sequence")
+    p = _lib.GdnProblem()
+    p.B, p.T, p.H, p.dk, p.dv, p.chunk = q.shape[0], (q.shape[1] if lead == 2 else 1), H, dk, dv, 0
+    p.nseq = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+    p.cu_seqlens = _ptr(cu_seqlens)
+    p.io_dtype = _dtype_code(q)
+    p.gate_dtype = _lib.GDN_F32
+    p.gate = _lib.GDN_GATE_NONE
+    p.seg_chunks = int(seg_chunks)
+    nseq = q.shape[0] if cu_seqlens is None else p.nseq
+    return p, hq, (nseq, H, dk, dv)
+
+
+def linear_attn_fwd(q, k, v, log_decay=None, s0=None, cu_seqlens=None,
+                    output_final_state: bool = True,
+                    workspace: Optional[torch.Tensor] = None, seg_chunks: int = 0,
+                    o=None, s_final=None):
+    """Linear attention with a constant decay per head over whole sequences
+    (gdn_linear_attn_fwd): S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,
+    o_t = S_t^T q_t.  q, k [B,T,Hq,dk] with Hq dividing H (v head h reads q, k
+    head h // (H // Hq)); v [B,T,H,dv]; log_decay [H] fp32 or None (no decay);
+    s0 [nseq,H,dk,dv] fp32 or None; cu_seqlens packs sequences (B = 1).
+    o / s_final: optional preallocated outputs.  Returns (o, s_final or None)."""
+    lib = _lib.load()
+    p, hq, states = _linattn_problem(q, k, v, log_decay, cu_seqlens, seg_chunks, 2)
+    _want(s0, "s0", states, torch.float32, q.device)
+    o = _out(o, v.shape, q.dtype, q.device)
+    sf = _out(s_final, states, torch.float32, q.device) if output_final_state else None
+    ws, nbytes = _workspace(workspace, _bytes(lib.gdn_linear_attn_fwd_workspace, p, hq), q.device)
+    with _On(q.device):
+        st = lib.gdn_linear_attn_fwd(ctypes.byref(p), hq, _ptr(q), _ptr(k), _ptr(v),
+                                     _ptr(log_decay), _ptr(s0), _ptr(o), _ptr(sf), _ptr(ws),
+                                     nbytes, _stream(q.device))
+    _lib.check(st, "gdn_linear_attn_fwd")
+    return o, sf
+
+
+def linear_attn_bwd(q, k, v, log_decay, s0, d_o, ds_final=None, cu_seqlens=None,
+                    need_ds0: bool = True, workspace: Optional[torch.Tensor] = None,
+                    seg_chunks: int = 0, out=None):
+    """Backward of :func:`linear_attn_fwd` (gdn_linear_attn_bwd): gradients of
+    <d_o, o> + <ds_final, s_final>.  out: optional preallocated (dq, dk, dv,
+    ds0), entries may be None.  Returns (dq, dk, dv, ds0 or None)."""
+    lib = _lib.load()
+    p, hq, states = _linattn_problem(q, k, v, log_decay, cu_seqlens, seg_chunks, 2)
+    _want(s0, "s0", states, torch.float32, q.device)
+    _want(d_o, "d_o", v.shape, v.dtype, q.device)
+    _want(ds_final, "ds_final", states, torch.float32, q.device)
+    out = (None,) * 4 if out is None else tuple(out)
+    dq = _out(out[0], q.shape, q.dtype, q.device)
+    dk = _out(out[1], k.shape, k.dtype, q.device)
+    dv = _out(out[2], v.shape, v.dtype, q.device)
+    ds0 = _out(out[3], states, torch.float32, q.device) if need_ds0 else None
+    ws, nbytes = _workspace(workspace, _bytes(lib.gdn_linear_attn_bwd_workspace, p, hq), q.device)
+    with _On(q.device):
+        st = lib.gdn_linear_attn_bwd(ctypes.byref(p), hq, _ptr(q), _ptr(k), _ptr(v),
+                                     _ptr(log_decay), _ptr(s0), _ptr(d_o), _ptr(ds_final),
+                                     _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ds0), _ptr(ws), nbytes,
+                                     _stream(q.device))
+    _lib.check(st, "gdn_linear_attn_bwd")
+    return dq, dk, dv, ds0
+
+
+def linear_attn_decode_step(q, k, v, log_decay, state, o=None):
+    """One token per sequence of :func:`linear_attn_fwd`'s rule
+    (gdn_linear_attn_decode_step); ``state`` [N,H,dk,dv] fp32 is updated in
+    place.  q, k [N,Hq,dk]; v [N,H,dv]; log_decay [H] fp32 or None.
+    Returns o [N,H,dv]."""
+    lib = _lib.load()
+    p, hq, states = _linattn_problem(q, k, v, log_decay, None, 0, 1)
+    if state is None:
+        raise ValueError("state must be given")
+    _want(state, "state", states, torch.float32, q.device)
+    o = _out(o, v.shape, q.dtype, q.device)
+    with _On(q.device):
+        st = lib.gdn_linear_attn_decode_step(ctypes.byref(p), hq, _ptr(q), _ptr(k), _ptr(v),
+                                             _ptr(log_decay), _ptr(state), _ptr(o),
+                                             _stream(q.device))
+    _lib.check(st, "gdn_linear_attn_decode_step")
+    return o
+
+
+_ACTS = {"none": _lib.GDN_ACT_NONE, "silu": _lib.GDN_ACT_SILU, "sigmoid": _lib.GDN_ACT_SIGMOID}
+
+
+def _norm_problem(x, weight, bias, gate, act):
+    """(problem, act code, shared weights) of a group-norm call."""
+    if x.dim() != 4:
+        raise ValueError("x must be [B, T, H, d]")
+    if not x.is_cuda:
+        raise ValueError("libgdn takes GPU tensors")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    B, T, H, d = x.shape
+    _want(gate, "gate", x.shape, x.dtype, x.device)
+    one = next((t for t in (weight, bias) if t is not None), None)
+    shared = one is not None and one.dim() == 1
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        _want(t, name, (d,) if shared else (H, d), torch.float32, x.device)
+    p = _lib.GdnProblem()
+    p.B, p.T, p.H, p.dk, p.dv = B, T, H, d, d
+    p.io_dtype = _dtype_code(x)
+    return p, _ACTS[act], int(shared)
+
+
+def group_norm_fwd(x, weight=None, bias=None, gate=None, act: str = "silu", eps: float = 1e-5,
+                   center: bool = True, y=None):
+    """Group norm of a causal block's output (gdn_group_norm_fwd): each
+    token's d channels of each head are normalised (center False: the RMS
+    form), scaled and shifted; then act(n), or n * act(gate) with a gate.
+    x, gate [B,T,H,d]; weight, bias [H,d] or [d] (one set for all heads), fp32
+    or None.  act: "none", "silu" or "sigmoid".  y: optional preallocated
+    output (may be x or gate itself).  Returns y."""
+    lib = _lib.load()
+    p, code, shared = _norm_problem(x, weight, bias, gate, act)
+    y = _out(y, x.shape, x.dtype, x.device)
+    with _On(x.device):
+        st = lib.gdn_group_norm_fwd(ctypes.byref(p), x.shape[-1], code, int(center), shared, eps,
+                                    _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y),
+                                    _stream(x.device))
+    _lib.check(st, "gdn_group_norm_fwd")
+    return y
+
+
+def group_norm_bwd(x, dy, weight=None, bias=None, gate=None, act: str = "silu",
+                   eps: float = 1e-5, center: bool = True,
+                   workspace: Optional[torch.Tensor] = None):
+    """Backward of :func:`group_norm_fwd` (gdn_group_norm_bwd).  Returns
+    (dx, dgate, dweight, dbias); the last three are None where their input
+    is."""
+    lib = _lib.load()
+    p, code, shared = _norm_problem(x, weight, bias, gate, act)
+    _want(dy, "dy", x.shape, x.dtype, x.device)
+    dx = torch.empty_like(x)
+    dz, dw, db = (None if t is None else torch.empty_like(t) for t in (gate, weight, bias))
+    ws, nbytes = _workspace(workspace, _bytes(lib.gdn_group_norm_bwd_workspace, p, x.shape[-1]),
+                            x.device)
+    with _On(x.device):
+        st = lib.gdn_group_norm_bwd(ctypes.byref(p), x.shape[-1], code, int(center), shared, eps,
+                                    _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(dy),
+                                    _ptr(dx), _ptr(dz), _ptr(dw), _ptr(db), _ptr(ws), nbytes,
+                                    _stream(x.device))
+    _lib.check(st, "gdn_group_norm_bwd")
+    return dx, dz, dw, db

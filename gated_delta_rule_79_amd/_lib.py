@@ -21,6 +21,7 @@ GDN_ERR_SCRATCH = 8
 NOALLOC_SCRATCH_BYTES = 256 << 20  # GDN_NOALLOC_SCRATCH_BYTES
 GDN_F32, GDN_BF16 = 0, 1
 GDN_GATE_NONE, GDN_GATE_SCALAR, GDN_GATE_CHANNEL = 0, 1, 2
+GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_SIGMOID = 0, 1, 2
 
 EXPORTED = (
     "gdn_abi_version", "gdn_status_str", "gdn_chunk_fwd_workspace",
@@ -33,6 +34,10 @@ EXPORTED = (
     "gdn2_chunk_fwd", "gdn2_decode_step", "gdn_chunk_fwd_qknorm_workspace",
     "gdn_chunk_fwd_conv_workspace", "gdn_chunk_fwd_conv", "gdn_prologue_fwd",
     "gdn_prologue_bwd_workspace", "gdn_prologue_bwd",
+    "gdn_linear_attn_fwd_workspace", "gdn_linear_attn_fwd",
+    "gdn_linear_attn_bwd_workspace", "gdn_linear_attn_bwd",
+    "gdn_linear_attn_decode_step", "gdn_group_norm_fwd",
+    "gdn_group_norm_bwd_workspace", "gdn_group_norm_bwd",
 )
 STAGE_COUNT = 12
 STAGES = ("chunk_map", "fwd_prep", "fwd_scan", "decode", "bwd_states",
@@ -126,6 +131,23 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.gdn_prologue_bwd.argtypes = [pp, i32, i32, i32] + [vp] * 6 + [sz, vp]
     lib.gdn_tree_commit.restype = i32
     lib.gdn_tree_commit.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.gdn_linear_attn_fwd_workspace.restype = i32
+    lib.gdn_linear_attn_fwd_workspace.argtypes = [pp, i32, ctypes.POINTER(sz)]
+    lib.gdn_linear_attn_fwd.restype = i32
+    lib.gdn_linear_attn_fwd.argtypes = [pp, i32] + [vp] * 8 + [sz, vp]
+    lib.gdn_linear_attn_bwd_workspace.restype = i32
+    lib.gdn_linear_attn_bwd_workspace.argtypes = [pp, i32, ctypes.POINTER(sz)]
+    lib.gdn_linear_attn_bwd.restype = i32
+    lib.gdn_linear_attn_bwd.argtypes = [pp, i32] + [vp] * 12 + [sz, vp]
+    lib.gdn_linear_attn_decode_step.restype = i32
+    lib.gdn_linear_attn_decode_step.argtypes = [pp, i32] + [vp] * 7
+    f32 = ctypes.c_float
+    lib.gdn_group_norm_fwd.restype = i32
+    lib.gdn_group_norm_fwd.argtypes = [pp, i32, i32, i32, i32, f32] + [vp] * 6
+    lib.gdn_group_norm_bwd_workspace.restype = i32
+    lib.gdn_group_norm_bwd_workspace.argtypes = [pp, i32, ctypes.POINTER(sz)]
+    lib.gdn_group_norm_bwd.restype = i32
+    lib.gdn_group_norm_bwd.argtypes = [pp, i32, i32, i32, i32, f32] + [vp] * 10 + [sz, vp]
     if path is None:
         _LIB = lib
     return lib

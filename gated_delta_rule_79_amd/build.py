@@ -35,7 +35,7 @@ SAN = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined
        "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-fno-sanitize-recover=all"]
 
 SOURCES = ["gdn_api.hip", "gdn_decode.hip", "gdn_fwd.hip", "gdn_bwd.hip", "gdn_tree.hip",
-           "gdn_prologue.hip"]
+           "gdn_prologue.hip", "gdn_linattn.hip", "gdn_groupnorm.hip"]
 ARCH = "gfx950"
 
 CFLAGS = [

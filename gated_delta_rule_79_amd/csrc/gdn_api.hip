@@ -976,4 +976,269 @@ gdn_status gdn_decode_step_product(const gdn_problem* p, int32_t nh, const void*
   }
 }
 
+// ------------------------------------------------------- linear attention ---
+
+}  // extern "C"
+
+namespace {
+
+// Checks of the linear-attention entry points; decode: one token of p->B
+// sequences, the packing ignored.
+gdn_status check_linattn(const gdn_problem* p, int32_t hq, bool decode, gdn::LinAttn* out) {
+  if (p == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+  if (!dtype_ok(p->io_dtype)) return GDN_FAIL(GDN_ERR_DTYPE);
+  if (p->gate != GDN_GATE_NONE) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  if (p->B < 1 || p->H < 1) return GDN_FAIL(GDN_ERR_SHAPE);
+  if (hq < 1 || hq > p->H || p->H % hq != 0) return GDN_FAIL(GDN_ERR_SHAPE);
+  if (!dk_ok(p->dk) || !dv_ok(p->dv)) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  const int64_t esize = p->io_dtype == GDN_BF16 ? 2 : 4;
+  // a chunk's rows are addressed with 32-bit byte offsets
+  if (p->H * esize * std::max(p->dk, p->dv) >= (int64_t(1) << 25))
+    return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  out->B = p->B;
+  out->T = decode ? 1 : p->T;
+  out->H = p->H;
+  out->dk = p->dk;
+  out->dv = p->dv;
+  out->hq = hq;
+  out->varlen = !decode && p->nseq > 0;
+  out->nseq = out->varlen ? p->nseq : p->B;
+  out->cu_seqlens = out->varlen ? p->cu_seqlens : nullptr;
+  out->io = p->io_dtype;
+  out->seg_req = decode ? 0 : p->seg_chunks;
+  if (decode) {
+    const int64_t blocks = static_cast<int64_t>(p->B) * p->H * ((p->dv + 63) / 64);
+    return blocks <= (int64_t(1) << 31) - 1 ? GDN_OK : GDN_FAIL(GDN_ERR_SHAPE);
+  }
+  if (p->T < 0 || p->nseq < 0) return GDN_FAIL(GDN_ERR_SHAPE);
+  if (p->nseq > 0) {
+    if (p->B != 1) return GDN_FAIL(GDN_ERR_SHAPE);
+    if (p->cu_seqlens == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+    if ((reinterpret_cast<uintptr_t>(p->cu_seqlens) & 3u) != 0) return GDN_FAIL(GDN_ERR_ALIGN);
+  } else if (p->cu_seqlens != nullptr) {
+    return GDN_FAIL(GDN_ERR_SHAPE);
+  }
+  if (p->T > (1 << 30) ||
+      static_cast<int64_t>(p->B) * p->T * p->H * 256 > (int64_t(1) << 46) ||
+      !gdn::linattn_grid_ok(*out))
+    return GDN_FAIL(GDN_ERR_SHAPE);
+  return GDN_OK;
+}
+
+// Pointers of q, k, v and a [tokens, H, dv] tensor (o or d_o).
+gdn_status check_linattn_rows(const gdn::LinAttn& p, const void* q, const void* k, const void* v,
+                              const void* o, const float* log_decay) {
+  const int64_t tok = static_cast<int64_t>(p.B) * p.T;
+  GDN_TRY(need(q, tok * p.hq * p.dk));
+  GDN_TRY(need(k, tok * p.hq * p.dk));
+  GDN_TRY(need(v, tok * p.H * p.dv));
+  GDN_TRY(need(o, tok * p.H * p.dv));
+  return opt(log_decay);
+}
+
+gdn_status launched(const gdn::LinAttn& p, hipError_t e) {
+  if (log_on()) {
+    fprintf(stderr, "gdn: %s: B=%d T=%d H=%d hq=%d dk=%d dv=%d io=%s nseq=%d%s -> %s\n", t_entry,
+            p.B, p.T, p.H, p.hq, p.dk, p.dv, dtype_name(p.io), p.nseq,
+            p.varlen ? " (varlen)" : "", hipGetErrorName(e));
+  }
+  return e == hipSuccess ? GDN_OK : GDN_FAIL(GDN_ERR_HIP);
+}
+
+gdn_status check_group_norm(const gdn_problem* p, int32_t d, int32_t act, float eps,
+                            gdn::GroupNorm* out) {
+  if (p == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+  if (!dtype_ok(p->io_dtype)) return GDN_FAIL(GDN_ERR_DTYPE);
+  if (p->B < 1 || p->T < 0 || p->H < 1 || p->H > 65535) return GDN_FAIL(GDN_ERR_SHAPE);
+  if (d != p->dk && d != p->dv) return GDN_FAIL(GDN_ERR_SHAPE);
+  if (!dv_ok(d)) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  if (act < GDN_ACT_NONE || act > GDN_ACT_SIGMOID) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  if (!std::isfinite(eps) || !(eps > 0.0f)) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  const int64_t tok = static_cast<int64_t>(p->B) * p->T;
+  if (tok > (int64_t(1) << 38) / p->H) return GDN_FAIL(GDN_ERR_SHAPE);
+  out->tokens = tok;
+  out->H = p->H;
+  out->d = d;
+  out->io = p->io_dtype;
+  out->act = act;
+  out->center = false;
+  out->shared = false;
+  out->eps = eps;
+  return GDN_OK;
+}
+
+gdn_status launched(const gdn::GroupNorm& p, hipError_t e) {
+  if (log_on()) {
+    fprintf(stderr, "gdn: %s: tokens=%lld H=%d d=%d io=%s act=%d%s%s -> %s\n", t_entry,
+            static_cast<long long>(p.tokens), p.H, p.d, dtype_name(p.io), p.act,
+            p.center ? " center" : "", p.shared ? " shared" : "", hipGetErrorName(e));
+  }
+  return e == hipSuccess ? GDN_OK : GDN_FAIL(GDN_ERR_HIP);
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_linear_attn_fwd_workspace(const gdn_problem* p, int32_t hq, size_t* bytes) {
+  GDN_ENTRY();
+  try {
+    if (bytes == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+    gdn::LinAttn pp;
+    GDN_TRY(check_linattn(p, hq, false, &pp));
+    *bytes = gdn::linattn_fwd_workspace_bytes(pp);
+    return GDN_OK;
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_linear_attn_fwd(const gdn_problem* p, int32_t hq, const void* q, const void* k,
+                               const void* v, const float* log_decay, const float* s0, void* o,
+                               float* s_final, void* ws, size_t ws_bytes, void* stream) {
+  GDN_ENTRY();
+  try {
+    gdn::LinAttn pp;
+    GDN_TRY(check_linattn(p, hq, false, &pp));
+    GDN_TRY(check_linattn_rows(pp, q, k, v, o, log_decay));
+    GDN_TRY(opt(s0));
+    GDN_TRY(opt(s_final));
+    const size_t need_ws = gdn::linattn_fwd_workspace_bytes(pp);
+    if (need_ws > 0 && (ws == nullptr || ws_bytes < need_ws)) return GDN_FAIL(GDN_ERR_WORKSPACE);
+    GDN_TRY(opt(ws));
+    if (g_fail_launch.load()) return launched(pp, hipErrorLaunchFailure);  // test hook
+    return launched(pp, gdn::launch_linattn_fwd(pp, q, k, v, log_decay, s0, o, s_final, ws,
+                                                static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_linear_attn_bwd_workspace(const gdn_problem* p, int32_t hq, size_t* bytes) {
+  GDN_ENTRY();
+  try {
+    if (bytes == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+    gdn::LinAttn pp;
+    GDN_TRY(check_linattn(p, hq, false, &pp));
+    *bytes = gdn::linattn_bwd_workspace_bytes(pp);
+    return GDN_OK;
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_linear_attn_bwd(const gdn_problem* p, int32_t hq, const void* q, const void* k,
+                               const void* v, const float* log_decay, const float* s0,
+                               const void* d_o, const float* ds_final, void* dq, void* dk,
+                               void* dv, float* ds0, void* ws, size_t ws_bytes, void* stream) {
+  GDN_ENTRY();
+  try {
+    gdn::LinAttn pp;
+    GDN_TRY(check_linattn(p, hq, false, &pp));
+    GDN_TRY(check_linattn_rows(pp, q, k, v, d_o, log_decay));
+    const int64_t tok = static_cast<int64_t>(pp.B) * pp.T;
+    GDN_TRY(need(dq, tok * pp.hq * pp.dk));
+    GDN_TRY(need(dk, tok * pp.hq * pp.dk));
+    GDN_TRY(need(dv, tok * pp.H * pp.dv));
+    GDN_TRY(opt(s0));
+    GDN_TRY(opt(ds_final));
+    GDN_TRY(opt(ds0));
+    const size_t need_ws = gdn::linattn_bwd_workspace_bytes(pp);
+    if (need_ws > 0 && (ws == nullptr || ws_bytes < need_ws)) return GDN_FAIL(GDN_ERR_WORKSPACE);
+    GDN_TRY(opt(ws));
+    if (g_fail_launch.load()) return launched(pp, hipErrorLaunchFailure);  // test hook
+    return launched(pp, gdn::launch_linattn_bwd(pp, q, k, v, log_decay, s0, d_o, ds_final, dq, dk,
+                                                dv, ds0, ws, static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_linear_attn_decode_step(const gdn_problem* p, int32_t hq, const void* q,
+                                       const void* k, const void* v, const float* log_decay,
+                                       float* state, void* o, void* stream) {
+  GDN_ENTRY();
+  try {
+    gdn::LinAttn pp;
+    GDN_TRY(check_linattn(p, hq, true, &pp));
+    GDN_TRY(check_linattn_rows(pp, q, k, v, o, log_decay));
+    GDN_TRY(need(state, static_cast<int64_t>(pp.B) * pp.H));
+    if (g_fail_launch.load()) return launched(pp, hipErrorLaunchFailure);  // test hook
+    return launched(pp, gdn::launch_linattn_decode(pp, q, k, v, log_decay, state, o,
+                                                   static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+// -------------------------------------------------------------- group norm ---
+
+gdn_status gdn_group_norm_fwd(const gdn_problem* p, int32_t d, int32_t act, int32_t center,
+                              int32_t shared, float eps, const void* x, const void* z,
+                              const float* w, const float* b, void* y, void* stream) {
+  GDN_ENTRY();
+  try {
+    gdn::GroupNorm pp;
+    GDN_TRY(check_group_norm(p, d, act, eps, &pp));
+    pp.center = center != 0;
+    pp.shared = shared != 0;
+    const int64_t n = pp.tokens * pp.H * d;
+    GDN_TRY(need(x, n));
+    GDN_TRY(opt(z));
+    GDN_TRY(opt(w));
+    GDN_TRY(opt(b));
+    GDN_TRY(need(y, n));
+    if (g_fail_launch.load()) return launched(pp, hipErrorLaunchFailure);  // test hook
+    return launched(pp, gdn::launch_group_norm_fwd(pp, x, z, w, b, y,
+                                                   static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_group_norm_bwd_workspace(const gdn_problem* p, int32_t d, size_t* bytes) {
+  GDN_ENTRY();
+  try {
+    if (bytes == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+    gdn::GroupNorm pp;
+    GDN_TRY(check_group_norm(p, d, GDN_ACT_NONE, 1.0f, &pp));
+    *bytes = gdn::group_norm_bwd_workspace_bytes(pp);
+    return GDN_OK;
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_group_norm_bwd(const gdn_problem* p, int32_t d, int32_t act, int32_t center,
+                              int32_t shared, float eps, const void* x, const void* z,
+                              const float* w, const float* b, const void* dy, void* dx,
+                              void* dz, float* dw, float* db, void* ws, size_t ws_bytes,
+                              void* stream) {
+  GDN_ENTRY();
+  try {
+    gdn::GroupNorm pp;
+    GDN_TRY(check_group_norm(p, d, act, eps, &pp));
+    pp.center = center != 0;
+    pp.shared = shared != 0;
+    const int64_t n = pp.tokens * pp.H * d;
+    GDN_TRY(need(x, n));
+    GDN_TRY(opt(z));
+    GDN_TRY(opt(w));
+    GDN_TRY(opt(b));
+    GDN_TRY(need(dy, n));
+    GDN_TRY(need(dx, n));
+    if (z != nullptr) GDN_TRY(need(dz, n));
+    GDN_TRY(opt(dw));
+    GDN_TRY(opt(db));
+    if (ws == nullptr || ws_bytes < gdn::group_norm_bwd_workspace_bytes(pp))
+      return GDN_FAIL(GDN_ERR_WORKSPACE);
+    GDN_TRY(opt(ws));
+    if (g_fail_launch.load()) return launched(pp, hipErrorLaunchFailure);  // test hook
+    return launched(pp, gdn::launch_group_norm_bwd(pp, x, z, w, b, dy, dx, dz, dw, db, ws,
+                                                   static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
 }  // extern "C"

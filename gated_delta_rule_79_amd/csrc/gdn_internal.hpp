@@ -109,4 +109,44 @@ hipError_t launch_bwd(const Problem& p, const void* q, const void* k,
                       void* dq, void* dk, void* dv, float* dbeta, float* dla,
                       float* ds0, void* ws, hipStream_t s);
 
+// Linear attention with a constant decay per head (gdn_linattn.hip).
+struct LinAttn {
+  int B, T, H, dk, dv;
+  int hq;                     // q / k heads, shared by H / hq v heads each
+  int nseq;                   // number of independent sequences (B or packed)
+  bool varlen;
+  const int32_t* cu_seqlens;  // device
+  int io;                     // gdn_dtype
+  int seg_req;                // gdn_problem::seg_chunks
+};
+bool linattn_grid_ok(const LinAttn& p);  // whether the launches fit the grid
+size_t linattn_fwd_workspace_bytes(const LinAttn& p);
+hipError_t launch_linattn_fwd(const LinAttn& p, const void* q, const void* k, const void* v,
+                              const float* la, const float* s0, void* o, float* s_final,
+                              void* ws, hipStream_t s);
+size_t linattn_bwd_workspace_bytes(const LinAttn& p);
+hipError_t launch_linattn_bwd(const LinAttn& p, const void* q, const void* k, const void* v,
+                              const float* la, const float* s0, const void* d_o,
+                              const float* ds_final, void* dq, void* dk, void* dv, float* ds0,
+                              void* ws, hipStream_t s);
+hipError_t launch_linattn_decode(const LinAttn& p, const void* q, const void* k, const void* v,
+                                 const float* la, float* state, void* o, hipStream_t s);
+
+// Group norm of a causal block's output (gdn_groupnorm.hip).
+struct GroupNorm {
+  int64_t tokens;
+  int H, d;      // groups and channels of each
+  int io;        // gdn_dtype of x, z, y and their gradients
+  int act;       // gdn_act
+  bool center;   // subtract the mean
+  bool shared;   // weight and bias are [d], one set for all groups
+  float eps;
+};
+hipError_t launch_group_norm_fwd(const GroupNorm& p, const void* x, const void* z, const float* w,
+                                 const float* b, void* y, hipStream_t s);
+size_t group_norm_bwd_workspace_bytes(const GroupNorm& p);
+hipError_t launch_group_norm_bwd(const GroupNorm& p, const void* x, const void* z, const float* w,
+                                 const float* b, const void* dy, void* dx, void* dz, float* dw,
+                                 float* db, void* ws, hipStream_t s);
+
 }  // namespace gdn

@@ -410,6 +410,92 @@ gdn_status gdn_decode_step_product(const gdn_problem* p, int32_t nh, const void*
                                    const void* log_alpha, float* state, void* o,
                                    void* stream);
 
+/* Linear attention with a constant decay per head: the recurrence without
+ * the erase step,
+ *   S_t = a_h S_{t-1} + k_t v_t^T  (S: [dk, dv]),   o_t = S_t^T q_t,
+ * a_h = exp(log_decay[h]).  The fixed decays of a hybrid or ablation model's
+ * linear layers, next to the gated delta layers; a gate that differs from
+ * token to token is gdn_chunk_fwd's.  Chunked for whole sequences (no
+ * triangular system: one masked q k^T product and a state per chunk).
+ *   p         : B, T, H, dk, dv, nseq, cu_seqlens, io_dtype and seg_chunks as
+ *               in the chunked calls; gate must be GDN_GATE_NONE; chunk and
+ *               gate_dtype are ignored (chunks take 64 tokens in bf16, 32 in
+ *               fp32, and seg_chunks counts those).
+ *   hq        : heads of q and k; v head h reads q / k head h / (H / hq).
+ *               hq in 1 .. H dividing H, else GDN_ERR_SHAPE.
+ *   q, k      : [B, T, hq, dk];  v, o : [B, T, H, dv], io_dtype.
+ *   log_decay : [H] fp32, 16-byte aligned, or NULL for a = 1 (plain causal
+ *               linear attention).  Normally <= 0; -inf is a = 0.
+ *   s0, s_final : [nseq, H, dk, dv] fp32 or NULL, as in gdn_chunk_fwd.
+ *   ws        : at least gdn_linear_attn_fwd_workspace bytes.
+ * Products of bf16 operands are summed in fp32; the state is carried (and
+ * s_final written) to fp32 accuracy in either type; only the copy of the
+ * state, and of q k^T, that multiplies bf16 rows is rounded to bf16.  Rows
+ * of packed tensors behind cu_seqlens[nseq] are neither read nor written.
+ * A NaN or infinity in a token reaches the outputs of its own chunk and of
+ * all later tokens of its sequence, never another sequence.  Deterministic.
+ * Errors as gdn_chunk_fwd; GDN_ERR_UNSUPPORTED for another gate or for rows
+ * of 2^25 bytes or more (all heads of one token). */
+gdn_status gdn_linear_attn_fwd_workspace(const gdn_problem* p, int32_t hq, size_t* bytes);
+gdn_status gdn_linear_attn_fwd(const gdn_problem* p, int32_t hq, const void* q, const void* k,
+                               const void* v, const float* log_decay, const float* s0, void* o,
+                               float* s_final, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward of gdn_linear_attn_fwd: gradients of <dO, o> + <ds_final,
+ * S_final> with respect to q, k, v and s0 (log_decay is a constant of the
+ * head and gets none).  Gradients of a q or k head shared by several v heads
+ * are summed over them in fp32, in head order.
+ *   d_o [B, T, H, dv]; ds_final fp32 or NULL (zeros); dq, dk [B, T, hq, dk]
+ *   and dv [B, T, H, dv] in io_dtype; ds0 [nseq, H, dk, dv] fp32 or NULL.
+ * Deterministic (no floating-point atomics).  Errors as the forward. */
+gdn_status gdn_linear_attn_bwd_workspace(const gdn_problem* p, int32_t hq, size_t* bytes);
+gdn_status gdn_linear_attn_bwd(const gdn_problem* p, int32_t hq, const void* q, const void* k,
+                               const void* v, const float* log_decay, const float* s0,
+                               const void* d_o, const float* ds_final, void* dq, void* dk,
+                               void* dv, float* ds0, void* ws, size_t ws_bytes, void* stream);
+
+/* One token per sequence of the same rule (B = N sequences), state updated
+ * in place:  M <- a_h M + k v^T,  o = M^T q; each state element is read once
+ * and written once.  q, k [N, hq, dk]; v, o [N, H, dv]; state
+ * [N, H, dk, dv] fp32.  T, chunk, nseq, cu_seqlens and seg_chunks of the
+ * problem are ignored. */
+gdn_status gdn_linear_attn_decode_step(const gdn_problem* p, int32_t hq, const void* q,
+                                       const void* k, const void* v, const float* log_decay,
+                                       float* state, void* o, void* stream);
+
+/* Group norm of a causal block's output, channels last, with an activation:
+ * the output stage of the linear-attention and gated-delta blocks.  x is
+ * [B, T, H, d]; a group is one token's d channels of one head (statistics
+ * never cross tokens, so a token's output does not depend on later ones):
+ *   c = x - mean(x)  (center != 0; else c = x, the RMS form),
+ *   n = c / sqrt(mean(c^2) + eps) * w + b,
+ *   y = act(n), or with a gate  y = n * act(z).
+ *   p      : B, T, H, dk, dv and io_dtype are used (the rest is ignored; a
+ *            packed batch's rows are all normalised).
+ *   d      : the channels of a group, the problem's dk or dv (else
+ *            GDN_ERR_SHAPE): a multiple of 16 up to 256.
+ *   act    : gdn_act.     eps : finite and > 0 (else GDN_ERR_UNSUPPORTED).
+ *   shared : 0: w, b are [H, d]; else [d], one set for every head.
+ *   x, z, y: io_dtype; z NULL = no gate.   w, b : fp32, each may be NULL
+ *            (ones, zeros).
+ * fp32 arithmetic, the variance taken around the mean.  y may be x or z
+ * itself (each element is read before it is written, by one thread). */
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_SIGMOID = 2 } gdn_act;
+gdn_status gdn_group_norm_fwd(const gdn_problem* p, int32_t d, int32_t act, int32_t center,
+                              int32_t shared, float eps, const void* x, const void* z,
+                              const float* w, const float* b, void* y, void* stream);
+
+/* Backward of gdn_group_norm_fwd: dx and (with a gate) dz in io_dtype, dw
+ * and db in fp32 (shapes of w, b; each may be NULL to skip it, also where w
+ * or b itself is NULL).  Sums over tokens run in a fixed order
+ * (deterministic).  Workspace: gdn_group_norm_bwd_workspace bytes. */
+gdn_status gdn_group_norm_bwd_workspace(const gdn_problem* p, int32_t d, size_t* bytes);
+gdn_status gdn_group_norm_bwd(const gdn_problem* p, int32_t d, int32_t act, int32_t center,
+                              int32_t shared, float eps, const void* x, const void* z,
+                              const float* w, const float* b, const void* dy, void* dx,
+                              void* dz, float* dw, float* db, void* ws, size_t ws_bytes,
+                              void* stream);
+
 /* Stage timing, for benchmarks and profiling.  While enabled, every kernel
  * the library enqueues is bracketed by a pair of HIP events recorded on the
  * same stream.  gdn_profile_read waits for the recorded events, writes the

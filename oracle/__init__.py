@@ -52,3 +52,10 @@ from .gdn_oracle import (  # noqa: F401
     conv_prologue_bwd,
     gdn_fwd_conv,
 )
+from .linattn_oracle import (  # noqa: F401
+    linattn_fwd,
+    linattn_bwd,
+    linattn_decode,
+    group_norm_fwd,
+    group_norm_bwd,
+)
