@@ -34,9 +34,6 @@ namespace gdn {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
-
 // Tokens per chunk: the LDS tiles of x, y (up to 256 wide) and z fit one
 // workgroup in either type.
 template <typename IO> constexpr int walk_chunk() { return opstore<IO>::bytes == 2 ? 64 : 32; }
@@ -130,6 +127,21 @@ __device__ inline Segment find_segment(const Cut& c, int slot) {
 // a^n for a whole n >= 0, in 64 bits: a walk multiplies thousands of these.
 __device__ inline double decay_pow(double log_a, int n) { return n == 0 ? 1.0 : exp(log_a * n); }
 
+// a^n in 32 bits: the exponent is reduced in 64, so that the hardware's
+// exponential (one unit in the last place) sees a fraction of [0, 1).
+__device__ inline float decay_pow32(double log_a, int n) {
+  const double x = log_a * n * 1.4426950408889634;
+  const double w = floor(x);
+  const float r = ldexpf(__builtin_amdgcn_exp2f(static_cast<float>(x - w)),
+                         static_cast<int>(fmin(fmax(w, -1000.0), 1000.0)));
+  return n == 0 ? 1.0f : x < -1000.0 ? 0.0f : r;
+}
+
+// A uniform element of a read-only array by a scalar load.
+__device__ inline float ld_scalar(const float* p, int i) {
+  return ((const __attribute__((address_space(4))) float*)(p))[i];
+}
+
 // ------------------------------------------------------- LDS tile reads ---
 // Operand fragments from row-major LDS tiles.  `p` is a lane's own base; all
 // further offsets are constants, which the reads take as immediates.
@@ -162,13 +174,15 @@ __device__ inline opvec<IO> lds_perm8(const char* p) {
 // STRIDE elements apart).  16-bit tiles use the transposing LDS read:
 // sixteen lanes name the 8-byte pieces of four rows of 16 columns, and lane
 // i receives column i of the four rows.  col_base: a lane's base for it.
-template <typename IO, int STRIDE>
+// Column i of the 16 is element GAP (i / 4) + i % 4 from the base; rows
+// 4 g .. 4 g + 3 (and 16 further down) start SKEW g elements in.
+template <typename IO, int STRIDE, int GAP, int SKEW>
 __device__ inline const char* col_base(const char* t, int lane) {
-  const int g = lane >> 4;
+  const int g = lane >> 4, l16 = lane & 15;
   if constexpr (opstore<IO>::bytes == 2)
-    return t + ((4 * g + ((lane & 15) >> 2)) * STRIDE + 4 * (lane & 3)) * 2;
+    return t + ((4 * g + (l16 >> 2)) * STRIDE + SKEW * g + GAP * (lane & 3)) * 2;
   else
-    return t + (4 * g * STRIDE + (lane & 15)) * 4;
+    return t + (4 * g * STRIDE + GAP * (l16 >> 2) + (l16 & 3)) * 4;
 }
 template <typename IO, int STRIDE>
 __device__ inline opvec<IO> lds_col8(const char* p) {
@@ -187,24 +201,40 @@ __device__ inline opvec<IO> lds_col8(const char* p) {
   }
 }
 
-// x = parts[0] + parts[1] + parts[2] in the operand type: bf16 operands
-// leave 2^-9, 2^-18, 2^-27 of x behind; fp32 operands are x itself.
+// A column of 8 weighted values as operand parts, x = p[0] + p[1] + p[2]:
+// bf16 parts leave 2^-9, 2^-18, 2^-27 of x behind; fp32 operands are x itself.
 template <typename IO> struct Parts;
 template <> struct Parts<f32_t> {
-  static constexpr int n = 1;
+  static constexpr int most = 1;
   floatx8 p[1];
-  __device__ inline void set(int e, float x) { p[0][e] = x; }
+  template <int N> __device__ inline void set(const floatx8& z, const float* w) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[0][e] = z[e] * w[e];
+  }
 };
 template <> struct Parts<bf16_t> {
-  static constexpr int n = 3;
+  static constexpr int most = 3;
   bf16x8 p[3];
-  __device__ inline void set(int e, float x) {
-    const __bf16 hi = (__bf16)x;
-    const float r = x - (float)hi;
-    const __bf16 mid = (__bf16)r;
-    p[0][e] = hi;
-    p[1][e] = mid;
-    p[2][e] = (__bf16)(r - (float)mid);
+  template <int N> __device__ inline void set(const bf16x8& z, const float* w) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    u32x4 out[3];
+    const u32x4 in = __builtin_bit_cast(u32x4, z);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float a = __uint_as_float(in[e] << 16) * w[2 * e];
+      float b = __uint_as_float(in[e] & 0xffff0000u) * w[2 * e + 1];
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const uint32_t r = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+        out[u][e] = r;
+        if (u + 1 < N) {
+          a -= __uint_as_float(r << 16);
+          b -= __uint_as_float(r & 0xffff0000u);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) p[u] = __builtin_bit_cast(bf16x8, out[u]);
   }
 };
 
@@ -227,16 +257,20 @@ struct Walk {
   float* behind;
 };
 
-// Tiles of a workgroup: R up to 32 NKB, slabs of NP columns.  A wave owns 16
-// columns; with narrow slabs SETS groups of W waves share the output rows (OUT)
-// or the state's rows.
+// Tiles of a workgroup: R up to 32 NKB, slabs of NP columns.  A wave owns CT
+// 16-column tiles; with narrow slabs SETS groups of W waves share the output
+// rows (OUT) or the state's rows.
 template <typename IO, int NKB, int NP, bool OUT>
 struct WalkTiles {
   static constexpr int C = walk_chunk<IO>();
   static constexpr int ob = opstore<IO>::bytes;
   static constexpr int RP = 32 * NKB, NR = 2 * NKB, NI = C / 16, NKC = C / 32;
-  static constexpr int W = NP / 16;  // waves that cover the slab
-  static constexpr int SETS = std::min(kWaves / W, OUT ? NI : NR);
+  // two column tiles a wave halve the operand reads; a state of over 128
+  // rows leaves no registers for them and takes eight waves instead of four
+  static constexpr int CT = NP > 64 && NKB <= 4 ? 2 : 1;
+  static constexpr int waves = NP > 64 && (NKB > 4 || !OUT) ? 8 : 4, threads = 64 * waves;
+  static constexpr int W = NP / (16 * CT);
+  static constexpr int SETS = std::min(waves / W, OUT ? NI : NR);
   static constexpr int IPS = OUT ? NI / SETS : 0;   // output row tiles of a wave
   static constexpr int RPS = OUT ? NR : NR / SETS;  // state row tiles of a wave
   // LDS: row strides (elements) that spread 16 rows read 16 bytes at a time
@@ -245,32 +279,40 @@ struct WalkTiles {
                        sz = NP + (ob == 2 ? 16 : 4);
   static constexpr int off_y = OUT ? C * sx * ob : 0, off_z = off_y + C * sy * ob,
                        off_p = off_z + C * sz * ob, off_d = off_p + (OUT ? C * C * ob : 0),
-                       off_w = off_d + (C + 4) * 4, bytes = off_w + (C + 4) * 8;
+                       off_w = off_d + (32 + C + 4) * 4, bytes = off_w + C * 4;
+  // y rows shift by 8 bytes every four rows (in the row's padding): 16 rows
+  // read 8 bytes at a time then meet all banks, as the transposing reads do
+  static constexpr int skew = ob == 2 ? 4 : 0;
   // 16-byte pieces of a row, rows per turn of the workgroup, turns
   static constexpr int px = RP * ob / 16, pz = NP * ob / 16;
-  static constexpr int stepx = kThreads / px, stepz = kThreads / pz;
-  static constexpr int nx = (C + stepx - 1) / stepx, nz = (C + stepz - 1) / stepz;
+  static constexpr int nx = (C * px + threads - 1) / threads,
+                       nz = (C * pz + threads - 1) / threads;
 };
 
 // One segment of one head and column slab.  The state sits in accumulator
 // registers.  Per chunk: rows of x, y, z arrive in LDS from registers that
 // were loaded during the previous chunk; x y^T on the matrix cores, decayed
 // and rounded once into operand fragments in LDS; out^T = M^T x^T (from the
-// state's registers, re-packed as an operand), scaled in fp32, plus
-// z^T (x y^T)^T; the state update between the two.
+// state's registers, re-packed as an operand), scaled in fp32; the state
+// update; plus z^T (x y^T)^T, stored at the start of the next chunk, where
+// the loads being waited for are older than the stores.
 // The update's weights go onto z in fp32, and the product is split into
 // bf16 parts, so the carried state keeps the fp32 accuracy of its storage.
+// Operand reads run one step ahead of the products that take them
+// (scheduling barriers hold them there).
 template <typename IO, int NKB, int NP, bool OUT, bool REV>
-__global__ __launch_bounds__(kThreads) void linattn_walk_kernel(Walk a) {
+__global__ __launch_bounds__((WalkTiles<IO, NKB, NP, OUT>::threads), 2)
+void linattn_walk_kernel(Walk a) {
   using L = WalkTiles<IO, NKB, NP, OUT>;
-  constexpr int C = L::C, NI = L::NI, NKC = L::NKC, ob = L::ob, off = REV ? 0 : 1;
+  constexpr int C = L::C, NI = L::NI, NKC = L::NKC, CT = L::CT, ob = L::ob, off = REV ? 0 : 1;
+  constexpr int kThreads = L::threads;
   __shared__ __align__(16) char lds[L::bytes];
   char* const tx = lds;
   char* const ty = lds + L::off_y;
   char* const tz = lds + L::off_z;
   char* const tp = lds + L::off_p;
-  float* const dec = reinterpret_cast<float*>(lds + L::off_d);    // a^0 .. a^C
-  double* const dec64 = reinterpret_cast<double*>(lds + L::off_w);
+  float* const dec = reinterpret_cast<float*>(lds + L::off_d) + 32;  // a^0 .. a^C, 0 below
+  float* const wgt = reinterpret_cast<float*>(lds + L::off_w);       // update weights of rows
 
   const int nslab = (a.N + NP - 1) / NP;
   const int id = xcd_swizzle(blockIdx.x, gridDim.x);
@@ -286,37 +328,13 @@ __global__ __launch_bounds__(kThreads) void linattn_walk_kernel(Walk a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, l16 = lane & 15;
 
-  const double log_a = a.log_decay == nullptr ? 0.0 : static_cast<double>(a.log_decay[h]);
-  for (int n = tid; n <= C; n += kThreads) {
-    const double d = decay_pow(log_a, n);
-    dec[n] = static_cast<float>(d);
-    dec64[n] = d;
-  }
-
   // this wave's columns and set; state rows r0 .., output row tiles set, set + SETS ..
   const int n0 = slab * NP;
-  const int set = L::SETS == 1 ? 0 : wave / L::W, col = (wave % L::W) * 16;  // column in the slab
+  // (two tiles interleave by fours, so that a lane's outputs are 8 adjacent columns)
+  const int set = L::SETS == 1 ? 0 : wave / L::W, col = (wave % L::W) * CT * 16;
+  const int n_lane = n0 + col + (CT == 2 ? 8 * (l16 >> 2) + (l16 & 3) : l16);
   const bool active = set < L::SETS && n0 + col < a.N;
   const int r0 = OUT ? 0 : set * L::RPS * 16;
-
-  // the state in front
-  floatx4 S[L::RPS];
-  const float* ent = a.enter == nullptr
-                         ? nullptr
-                         : a.enter + (static_cast<int64_t>(slot) * a.H + h) * a.R * a.N;
-#pragma unroll
-  for (int rt = 0; rt < L::RPS; ++rt) {
-    S[rt] = floatx4{0.f, 0.f, 0.f, 0.f};
-    const int r = rt * 16 + 4 * g, n = n0 + col + l16;
-    if (OUT && ent != nullptr && active && r < a.R) {
-      if (a.turned) {
-        S[rt] = *reinterpret_cast<const floatx4*>(ent + n * a.R + r);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[rt][e] = ent[(r + e) * a.N + n];
-      }
-    }
-  }
 
   // Rows of the next chunk, loaded ahead into registers as 16-byte pieces.
   // Row r of the walk is token t0 + r, backwards t0 + len - 1 - r: counted
@@ -356,13 +374,15 @@ __global__ __launch_bounds__(kThreads) void linattn_walk_kernel(Walk a) {
                      rs, in && row + u * step < len ? at : kOob,
                      (REV ? NT - 1 - u : u) * step * stride, 0));
   };
-  auto load_chunk = [&](int c) __attribute__((always_inline)) {
+  // bit 0 of `which`: x, 1: y, 2: z
+  auto load_chunk = [&](int c, auto which) __attribute__((always_inline)) {
+    constexpr int w = decltype(which)::value;
     int64_t t0;
     int len;
     chunk_of(c, &t0, &len);
-    if constexpr (OUT) load_rows(a.x, a.hx, a.R, 0, PX(), NX(), t0, len, rx);
-    load_rows(a.y, a.hy, a.R, 0, PX(), NX(), t0, len, ry);
-    load_rows(a.z, a.hz, a.N, n0, PZ(), NZ(), t0, len, rz);
+    if constexpr (OUT && (w & 1) != 0) load_rows(a.x, a.hx, a.R, 0, PX(), NX(), t0, len, rx);
+    if constexpr ((w & 2) != 0) load_rows(a.y, a.hy, a.R, 0, PX(), NX(), t0, len, ry);
+    if constexpr ((w & 4) != 0) load_rows(a.z, a.hz, a.N, n0, PZ(), NZ(), t0, len, rz);
   };
   auto put_rows = [&](char* t, auto stride, auto per_row, auto turns, const uint4* r)
       __attribute__((always_inline)) {
@@ -375,116 +395,316 @@ __global__ __launch_bounds__(kThreads) void linattn_walk_kernel(Walk a) {
       for (int u = 0; u < NT; ++u) *reinterpret_cast<uint4*>(p + u * step * ST * ob) = r[u];
     }
   };
+  // x rows with the columns of each 32-block in the permuted K order, so that
+  // a fragment that matches the state's registers is one 16-byte read
+  auto put_x = [&]() __attribute__((always_inline)) {
+    constexpr int step = kThreads / L::px;
+    const int row = tid / L::px, q = tid % L::px;
+    char* p = tx + row * L::sx * ob;
+    if (C % step == 0 || row < C) {
+      if constexpr (ob == 2) {
+        p += (q / 4 * 32 + 16 * (q & 1) + 4 * ((q >> 1) & 1)) * 2;
+#pragma unroll
+        for (int u = 0; u < L::nx; ++u) {
+          *reinterpret_cast<uint2*>(p + u * step * L::sx * 2) = make_uint2(rx[u].x, rx[u].y);
+          *reinterpret_cast<uint2*>(p + u * step * L::sx * 2 + 16) = make_uint2(rx[u].z, rx[u].w);
+        }
+      } else {
+        p += (q / 8 * 32 + 8 * (q & 3) + 4 * ((q >> 2) & 1)) * 4;
+#pragma unroll
+        for (int u = 0; u < L::nx; ++u) *reinterpret_cast<uint4*>(p + u * step * L::sx * 4) = rx[u];
+      }
+    }
+  };
+  auto put_y = [&]() __attribute__((always_inline)) {
+    if constexpr (L::skew == 0) {
+      put_rows(ty, std::integral_constant<int, L::sy>(), PX(), NX(), ry);
+    } else {
+      constexpr int step = kThreads / L::px;
+      // a thread's rows share their shift, or (8 apart) take two in turn
+      static_assert(L::nx == 1 || step % 16 == 0 || step == 8, "");
+      constexpr int odd = step == 8 ? 2 * L::skew : 0;
+      const int row = tid / L::px;
+      char* p = ty + (row * L::sy + L::skew * ((row >> 2) & 3)) * 2 + (tid % L::px) * 16;
+      if (C % step == 0 || row < C) {
+#pragma unroll
+        for (int u = 0; u < L::nx; ++u) {
+          char* const q = p + (u * step * L::sy + (u & 1) * odd) * 2;
+          *reinterpret_cast<uint2*>(q) = make_uint2(ry[u].x, ry[u].y);
+          *reinterpret_cast<uint2*>(q + 8) = make_uint2(ry[u].z, ry[u].w);
+        }
+      }
+    }
+  };
+  if (nch > 0) load_chunk(0, std::integral_constant<int, 7>());
+
+  // The state in front, all loads in flight at once (rows and columns past
+  // the state's, and a state that is not there, read zeros from no memory).
+  floatx4 S[L::RPS][CT];
+  if constexpr (OUT) {
+    const uint32_t bytes = a.enter == nullptr ? 0 : static_cast<uint32_t>(a.R) * a.N * 4;
+    const __amdgpu_buffer_rsrc_t rs =
+        make_rsrc(a.enter + (a.enter == nullptr
+                                 ? 0
+                                 : (static_cast<int64_t>(slot) * a.H + h) * a.R * a.N),
+                  bytes);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const int n = n_lane + 4 * ct;
+      const bool in = active && n < a.N;
+      if (a.turned) {
+        const uint32_t at = in ? (n * a.R + 4 * g) * 4 : kOob;
+#pragma unroll
+        for (int rt = 0; rt < L::RPS; ++rt)
+          S[rt][ct] = __builtin_bit_cast(
+              floatx4, __builtin_amdgcn_raw_buffer_load_b128(
+                           rs, at, rt * 16 < a.R ? rt * 64 : 0x40000000, 0));
+      } else {
+        const uint32_t at = in ? (4 * g * a.N + n) * 4 : kOob;
+#pragma unroll
+        for (int rt = 0; rt < L::RPS; ++rt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            S[rt][ct][e] = __uint_as_float(
+                __builtin_amdgcn_raw_buffer_load_b32(rs, at, (rt * 16 + e) * a.N * 4, 0));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int rt = 0; rt < L::RPS; ++rt)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) S[rt][ct] = floatx4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // powers of the decay, while the loads are on their way
+  const double log_a =
+      a.log_decay == nullptr ? 0.0 : static_cast<double>(ld_scalar(a.log_decay, h));
+  for (int n = tid; n <= C + 32; n += kThreads)
+    dec[n - 32] = n < 32 ? 0.f : decay_pow32(log_a, n - 32);
+  // A chunk's decay of the state, full chunks' and the segment's last one's:
+  // M a^n as M + M (a^n - 1) near 1, so that thousands of chunks keep it.
+  auto fade_of = [&](int n, float* mul, float* add) __attribute__((always_inline)) {
+    const double d = decay_pow(log_a, n);
+    const bool slow = d >= 0.5;
+    *mul = __uint_as_float(__builtin_amdgcn_readfirstlane(
+        __float_as_uint(static_cast<float>(slow ? d - 1.0 : d))));
+    *add = __uint_as_float(__builtin_amdgcn_readfirstlane(slow ? 0x3f800000u : 0u));
+  };
+  float mul_full, add_full, mul_tail, add_tail;
+  fade_of(C, &mul_full, &add_full);
+  fade_of(seg.len % C, &mul_tail, &add_tail);
 
   // lane bases of the operand reads and of the stores
   const char* const x_run = tx + (l16 * L::sx + 8 * g) * ob;
-  const char* const x_perm = tx + ((set * 16 + l16) * L::sx + 4 * g) * ob;
-  const char* const y_run = ty + (l16 * L::sy + 8 * g) * ob;
-  const char* const y_col = col_base<IO, L::sy>(ty, lane) + r0 * ob;
-  const char* const z_col = col_base<IO, L::sz>(tz, lane) + col * ob;
+  const char* const x_out = x_run + set * 16 * L::sx * ob;
+  const char* const y_perm = ty + (l16 * L::sy + L::skew * (l16 >> 2) + 4 * g) * ob;
+  const char* const y_col = col_base<IO, L::sy, 4, L::skew>(ty, lane) + r0 * ob;
+  const char* const z_col = col_base<IO, L::sz, 4 * CT, 0>(tz, lane) + col * ob;
+  const float* const d_lane = dec + (l16 - 4 * g);
   const char* const p_run = tp + (set * NKC * 64 + lane) * 8 * ob;
   const int os = a.out_f32 ? 4 : ob;  // bytes per output element
   const uint32_t ostride = static_cast<uint32_t>(a.H) * a.N * os;
-  const uint32_t o_lane = (REV ? 15 - l16 : l16) * ostride + (n0 + col + 4 * g) * os;
+  const uint32_t o_lane = (REV ? 15 - l16 : l16) * ostride + (n0 + col + 4 * CT * g) * os;
 
-  if (nch > 0) load_chunk(0);
+  floatx4 acc[OUT ? L::IPS : 1][CT];
+  // output rows of chunk c, from acc
+  auto store_out = [&](int c) __attribute__((always_inline)) {
+    int64_t t0;
+    int len;
+    chunk_of(c, &t0, &len);
+    // uniform base of the chunk's rows (backwards: of a full chunk's)
+    char* const orow = static_cast<char*>(a.out) +
+                       ((REV ? t0 + len - C : t0) * a.H + h) * static_cast<int64_t>(a.N) * os;
+#pragma unroll
+    for (int u = 0; u < L::IPS; ++u) {
+      const int it = set + u * L::SETS;
+      char* const p =
+          orow + static_cast<int64_t>((REV ? NI - 1 - it : it) * 16) * ostride + o_lane;
+      if (it * 16 + l16 < len && n0 + col + 4 * CT * g < a.N) {
+        if (ob == 4 || a.out_f32) {
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) *reinterpret_cast<floatx4*>(p + ct * 16) = acc[u][ct];
+        } else if constexpr (CT == 2) {
+          *reinterpret_cast<opvec<IO>*>(p) = pack2<IO>(acc[u][0], acc[u][1]);
+        } else {
+          *reinterpret_cast<typename acc4<IO>::type*>(p) = from_f4<IO>(acc[u][0]);
+        }
+      }
+    }
+  };
 
+  // Two stacked tiles of x y^T, transposed (column i, rows j): row tiles
+  // 2 jp and 2 jp + 1 of y against tile `it` of x, one operand fragment.
+  auto pair = [&](int it, int jp) __attribute__((always_inline)) {
+    floatx4 p0 = {0.f, 0.f, 0.f, 0.f}, p1 = p0;
+    const char* const xp = x_run + it * 16 * L::sx * ob;
+    const char* const yp = y_perm + jp * 32 * L::sy * ob;
+#pragma unroll
+    for (int kb = 0; kb < NKB; ++kb) {
+      const opvec<IO> xf = lds_run8<IO>(xp + kb * 32 * ob);
+      p0 = mma32(lds_perm8<IO>(yp + kb * 32 * ob), xf, p0);
+      p1 = mma32(lds_perm8<IO>(yp + (16 * L::sy + kb * 32) * ob), xf, p1);
+    }
+    // decays a^(i - j), zero above the diagonal (the table's lower end)
+    const float* const d = d_lane + (it * 16 - jp * 32);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      p0[e] *= d[-e];
+      p1[e] *= d[-16 - e];
+    }
+    *reinterpret_cast<opvec<IO>*>(tp + ((it * NKC + jp) * 64 + lane) * 8 * ob) =
+        pack2<IO>(p0, p1);
+  };
+
+  // M <- a^n M + sum_j y_j (w_j z_j)^T
+  auto update = [&](int n, auto parts) __attribute__((always_inline)) {
+    constexpr int NPART = decltype(parts)::value;
+    const float mul = n == C ? mul_full : mul_tail, add = n == C ? add_full : add_tail;
+    auto fade = [&](int rt) __attribute__((always_inline)) {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          S[rt][ct][e] = __builtin_fmaf(S[rt][ct][e], mul, add * S[rt][ct][e]);
+    };
+    constexpr int GR = std::min(2, L::RPS);  // state row tiles a step
+    constexpr int PER = L::RPS / GR;         // steps a 32-row block
+    opvec<IO> yf[2][GR], zf[CT];
+    auto read_z = [&](int kb) __attribute__((always_inline)) {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+        zf[ct] = lds_col8<IO, L::sz>(z_col + (kb * 32 * L::sz + ct * 4) * ob);
+    };
+    auto read_y = [&](int step) __attribute__((always_inline)) {
+#pragma unroll
+      for (int u = 0; u < GR; ++u)
+        yf[step & 1][u] = lds_col8<IO, L::sy>(
+            y_col + (step / PER * 32 * L::sy + ((step % PER) * GR + u) * 16) * ob);
+    };
+    read_z(0);
+    read_y(0);
+#pragma unroll
+    for (int u = 0; u < GR; ++u) fade(u);
+    Parts<IO> wz[CT];
+#pragma unroll
+    for (int step = 0; step < NKC * PER; ++step) {
+      const int kb = step / PER, rt = (step % PER) * GR;
+      if (step + 1 < NKC * PER) read_y(step + 1);
+      if (rt == 0) {
+        float w[8];
+        const floatx4 lo = *reinterpret_cast<const floatx4*>(wgt + kb * 32 + 4 * g);
+        const floatx4 hi = *reinterpret_cast<const floatx4*>(wgt + kb * 32 + 16 + 4 * g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = lo[e], w[4 + e] = hi[e];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) wz[ct].template set<NPART>(zf[ct], w);
+        if (kb + 1 < NKC) read_z(kb + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < NPART; ++u)
+#pragma unroll
+        for (int v = 0; v < GR; ++v)
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+            S[rt + v][ct] = mma32(yf[step & 1][v], wz[ct].p[u], S[rt + v][ct]);
+      // the next rows' decay, between the products
+      if (kb == 0 && step + 1 < PER) {
+#pragma unroll
+        for (int u = 0; u < GR; ++u) fade(rt + GR + u);
+      }
+    }
+  };
+
+  int wlen = -1;  // chunk length that wgt is for
   for (int c = 0; c < nch; ++c) {
     int64_t t0;
     int len;
     chunk_of(c, &t0, &len);
     __syncthreads();  // the previous chunk's tiles have been read
-    if constexpr (OUT)
-      put_rows(tx, std::integral_constant<int, L::sx>(), PX(), NX(), rx);
-    put_rows(ty, std::integral_constant<int, L::sy>(), PX(), NX(), ry);
+    if constexpr (OUT) put_x();
+    put_y();
     put_rows(tz, std::integral_constant<int, L::sz>(), PZ(), NZ(), rz);
+    if (len != wlen) {
+      wlen = len;
+      if (tid < C) wgt[tid] = tid < len ? dec[len - off - tid] : 0.f;
+    }
+    if constexpr (OUT)
+      if (active && c > 0) store_out(c - 1);
     __syncthreads();
-    if (c + 1 < nch) load_chunk(c + 1);
+    // the next chunk's rows, a third at a time: a burst would stall the waves
+    // behind the memory pipe
+    if (c + 1 < nch) load_chunk(c + 1, std::integral_constant<int, OUT ? 1 : 6>());
 
     if constexpr (OUT) {
-      // x y^T tiles with i >= j, transposed (column i, rows j): a fragment
-      // block takes two stacked j tiles; above the diagonal zeros
-      for (int job = wave; job < NI * (NI + 2) / 2; job += kWaves) {
-        int it = 0, first = 0;
-#pragma unroll
-        for (int i = 1; i < NI; ++i)
-          if (job >= first + 2 * ((it >> 1) + 1)) first += 2 * ((it >> 1) + 1), it = i;
-        const int jt = job - first;
-        floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-        if (jt <= it) {
-          const char* const yp = y_run + jt * 16 * L::sy * ob;
-          const char* const xp = x_run + it * 16 * L::sx * ob;
-#pragma unroll
-          for (int kb = 0; kb < NKB; ++kb)
-            acc = mma32(lds_run8<IO>(yp + kb * 32 * ob), lds_run8<IO>(xp + kb * 32 * ob), acc);
-        }
-        const int d = (it - jt) * 16 + l16 - 4 * g;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = d - e >= 0 ? acc[e] * dec[max(0, d - e)] : 0.f;
-        *reinterpret_cast<typename acc4<IO>::type*>(
-            tp + (((it * NKC + (jt >> 1)) * 64 + lane) * 8 + (jt & 1) * 4) * ob) =
-            from_f4<IO>(acc);
+      if constexpr (NI == 2) {
+        if (wave < 2) pair(wave, 0);
+      } else if constexpr (L::waves == 4) {
+        pair(wave < 2 ? 3 : 4 - wave, wave == 1 ? 1 : 0);
+        if (wave >= 2) pair(wave == 2 ? 0 : 2, wave - 2);
+      } else {
+        if (wave < 6) pair(wave < 2 ? wave : wave < 4 ? 2 : 3, wave < 2 ? 0 : wave & 1);
       }
+      if (c + 1 < nch) load_chunk(c + 1, std::integral_constant<int, 2>());
     }
 
-    opvec<IO> zf[NKC];
-    floatx4 acc[OUT ? L::IPS : 1];
     if (active) {
-#pragma unroll
-      for (int kb = 0; kb < NKC; ++kb)
-        zf[kb] = lds_col8<IO, L::sz>(z_col + kb * 32 * L::sz * ob);
       if constexpr (OUT) {
         // M^T x^T, the state rounded once to the operand type
+        opvec<IO> xf[2][L::IPS];
+        auto read_x = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
-        for (int it = 0; it < L::IPS; ++it) acc[it] = floatx4{0.f, 0.f, 0.f, 0.f};
+          for (int it = 0; it < L::IPS; ++it)
+            xf[kb & 1][it] = lds_run8<IO>(x_out + (it * L::SETS * 16 * L::sx + kb * 32) * ob);
+        };
+        read_x(0);
+#pragma unroll
+        for (int it = 0; it < L::IPS; ++it)
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) acc[it][ct] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < NKB; ++kb) {
-          const opvec<IO> m = pack2<IO>(S[2 * kb], S[2 * kb + 1]);
+          if (kb + 1 < NKB) read_x(kb + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          opvec<IO> m[CT];
 #pragma unroll
-          for (int it = 0; it < L::IPS; ++it) {
-            const opvec<IO> xf =
-                lds_perm8<IO>(x_perm + (it * L::SETS * 16 * L::sx + kb * 32) * ob);
-            acc[it] = mma32(m, xf, acc[it]);
-          }
+          for (int ct = 0; ct < CT; ++ct) m[ct] = pack2<IO>(S[2 * kb][ct], S[2 * kb + 1][ct]);
+#pragma unroll
+          for (int it = 0; it < L::IPS; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+              acc[it][ct] = mma32(m[ct], xf[kb & 1][it], acc[it][ct]);
         }
 #pragma unroll
-        for (int it = 0; it < L::IPS; ++it) acc[it] *= dec[(set + it * L::SETS) * 16 + l16 + off];
+        for (int it = 0; it < L::IPS; ++it) {
+          const float s = dec[(set + it * L::SETS) * 16 + l16 + off];
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) acc[it][ct] *= s;
+        }
       }
-      // the state behind the chunk, where another chunk or the caller wants it
-      if (!OUT || c + 1 < nch || (last && a.behind != nullptr)) {
-        const double dl = dec64[len];
-        const float dh = static_cast<float>(dl), dr = static_cast<float>(dl - dh);
-#pragma unroll
-        for (int rt = 0; rt < L::RPS; ++rt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            S[rt][e] = __builtin_fmaf(S[rt][e], dh, S[rt][e] * dr);
-#pragma unroll
-        for (int kb = 0; kb < NKC; ++kb) {
-          Parts<IO> wz;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            wz.set(e, (float)zf[kb][e] * dec[max(0, len - off - (kb * 32 + perm_k(g, e)))]);
-#pragma unroll
-          for (int rt = 0; rt < L::RPS; ++rt) {
-            const opvec<IO> yf =
-                lds_col8<IO, L::sy>(y_col + (kb * 32 * L::sy + rt * 16) * ob);
-#pragma unroll
-            for (int u = 0; u < Parts<IO>::n; ++u) S[rt] = mma32(yf, wz.p[u], S[rt]);
-            // a state of over 128 rows leaves no registers for reads far ahead
-            if constexpr (NKB > 4)
-              if (rt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-          }
-        }
+    }
+    if constexpr (OUT)
+      if (c + 1 < nch) load_chunk(c + 1, std::integral_constant<int, 4>());
+    if (active) {
+      // The state behind the chunk, where another chunk or the caller wants
+      // it.  What a caller or another workgroup gets takes all parts; a state
+      // that only multiplies bf16 rows keeps 2^-18 with two.
+      if (!OUT || (last && a.behind != nullptr)) {
+        update(len, std::integral_constant<int, Parts<IO>::most>());
+      } else if (c + 1 < nch) {
+        update(len, std::integral_constant<int, std::min(2, Parts<IO>::most)>());
       }
     }
 
     if constexpr (OUT) {
+      opvec<IO> zf[NKC][CT];
+#pragma unroll
+      for (int kb = 0; kb < NKC; ++kb)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          zf[kb][ct] = lds_col8<IO, L::sz>(z_col + (kb * 32 * L::sz + ct * 4) * ob);
       __syncthreads();  // x y^T is in LDS
       if (active) {
-        // uniform base of the chunk's rows (backwards: of a full chunk's)
-        char* const orow = static_cast<char*>(a.out) +
-                           ((REV ? t0 + len - C : t0) * a.H + h) * static_cast<int64_t>(a.N) * os;
 #pragma unroll
         for (int u = 0; u < L::IPS; ++u) {
           const int it = set + u * L::SETS;
@@ -492,34 +712,34 @@ __global__ __launch_bounds__(kThreads) void linattn_walk_kernel(Walk a) {
           for (int kb = 0; kb < NKC; ++kb) {
             if (kb > it / 2) continue;
             const opvec<IO> pf = lds_run8<IO>(p_run + (u * L::SETS * NKC + kb) * 512 * ob);
-            acc[u] = mma32(zf[kb], pf, acc[u]);
-          }
-          char* const orow_it =
-              orow + static_cast<int64_t>((REV ? C / 16 - 1 - it : it) * 16) * ostride;
-          if (it * 16 + l16 < len) {
-            char* const p = orow_it + o_lane;
-            if (ob == 4 || a.out_f32)
-              *reinterpret_cast<floatx4*>(p) = acc[u];
-            else
-              *reinterpret_cast<typename acc4<IO>::type*>(p) = from_f4<IO>(acc[u]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) acc[u][ct] = mma32(zf[kb][ct], pf, acc[u][ct]);
           }
         }
       }
     }
   }
+  if constexpr (OUT)
+    if (active && nch > 0) store_out(nch - 1);
 
+  // (the lane's place is worked out again: kept, it costs the loop registers)
+  int again = lane;
+  asm volatile("" : "+v"(again));
   float* bh = a.behind;
   if (bh != nullptr && active && (OUT ? last && set == 0 : true)) {
     const int64_t at = OUT ? static_cast<int64_t>(seg.seq) * a.H + h
                            : static_cast<int64_t>(slot) * a.H + h;
     bh += at * a.R * a.N;
 #pragma unroll
-    for (int rt = 0; rt < L::RPS; ++rt) {
-      const int r = r0 + rt * 16 + 4 * g, n = n0 + col + l16;
-      if (r >= a.R) continue;
+    for (int rt = 0; rt < L::RPS; ++rt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) bh[(r + e) * a.N + n] = S[rt][e];
-    }
+      for (int ct = 0; ct < CT; ++ct) {
+        const int r = r0 + rt * 16 + 4 * (again >> 4), 
+                  n = n0 + col + (CT == 2 ? 8 * ((again & 15) >> 2) + (again & 3) + 4 * ct : again & 15);
+        if (r >= a.R || n >= a.N) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bh[(r + e) * a.N + n] = S[rt][ct][e];
+      }
   }
 }
 
@@ -718,7 +938,8 @@ template <typename IO, int NKB, int NP, bool OUT, bool REV>
 void launch_walk_t(const Walk& w, int64_t slots, hipStream_t s) {
   const int64_t nslab = (w.N + NP - 1) / NP;
   hipLaunchKernelGGL((linattn_walk_kernel<IO, NKB, NP, OUT, REV>),
-                     dim3(static_cast<unsigned>(slots * w.H * nslab)), dim3(kThreads), 0, s, w);
+                     dim3(static_cast<unsigned>(slots * w.H * nslab)),
+                     dim3(WalkTiles<IO, NKB, NP, OUT>::threads), 0, s, w);
 }
 
 template <typename IO, int NKB, bool OUT, bool REV>
