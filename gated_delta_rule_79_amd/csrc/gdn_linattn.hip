@@ -252,6 +252,9 @@ struct Walk {
   // matrices, nullptr = zeros; `turned`: M is that matrix transposed
   const float* enter;
   int turned;
+  // enter (OUT) and behind (not OUT) in register order instead: per 16 CT
+  // columns and 16 rows, CT tiles of 64 lanes' four rows
+  int image;
   // state behind the walk: of each (sequence, head), by its last segment in
   // walk order (OUT); of each (slot, head) but those (not OUT)
   float* behind;
@@ -268,7 +271,7 @@ struct WalkTiles {
   // two column tiles a wave halve the operand reads; a state of over 128
   // rows leaves no registers for them and takes eight waves instead of four
   static constexpr int CT = NP > 64 && NKB <= 4 ? 2 : 1;
-  static constexpr int waves = NP > 64 && (NKB > 4 || !OUT) ? 8 : 4, threads = 64 * waves;
+  static constexpr int waves = NP > 64 && NKB > 4 ? 8 : 4, threads = 64 * waves;
   static constexpr int W = NP / (16 * CT);
   static constexpr int SETS = std::min(waves / W, OUT ? NI : NR);
   static constexpr int IPS = OUT ? NI / SETS : 0;   // output row tiles of a wave
@@ -301,7 +304,7 @@ struct WalkTiles {
 // Operand reads run one step ahead of the products that take them
 // (scheduling barriers hold them there).
 template <typename IO, int NKB, int NP, bool OUT, bool REV>
-__global__ __launch_bounds__((WalkTiles<IO, NKB, NP, OUT>::threads), 2)
+__global__ __launch_bounds__((WalkTiles<IO, NKB, NP, OUT>::threads), OUT ? 2 : 3)
 void linattn_walk_kernel(Walk a) {
   using L = WalkTiles<IO, NKB, NP, OUT>;
   constexpr int C = L::C, NI = L::NI, NKC = L::NKC, CT = L::CT, ob = L::ob, off = REV ? 0 : 1;
@@ -315,10 +318,18 @@ void linattn_walk_kernel(Walk a) {
   float* const wgt = reinterpret_cast<float*>(lds + L::off_w);       // update weights of rows
 
   const int nslab = (a.N + NP - 1) / NP;
-  const int id = xcd_swizzle(blockIdx.x, gridDim.x);
-  const int slab = id % nslab;
-  const int h = (id / nslab) % a.H;
-  const int slot = id / (nslab * a.H);
+  // Consecutive workgroups go round the 8 XCDs.  Items (segment, head) follow
+  // each other that way, so that unused slots and short segments fall on all
+  // of them alike; the slabs of one item, which read the same x and y rows,
+  // are 8 workgroups apart and so share an L2.
+  const int full = gridDim.x / (8 * nslab) * 8;  // items in whole groups of 8
+  const int id = blockIdx.x;
+  int slab = (id >> 3) % nslab, item = (id / (8 * nslab)) * 8 + (id & 7);
+  if (id >= full * nslab) {
+    slab = (id - full * nslab) % nslab;
+    item = full + (id - full * nslab) / nslab;
+  }
+  const int h = item % a.H, slot = item / a.H;
   const Segment seg = find_segment(a.cut, slot);
   if (seg.seq < 0) return;
   const bool last = REV ? seg.j == 0 : seg.j == seg.n - 1;  // in walk order
@@ -335,6 +346,10 @@ void linattn_walk_kernel(Walk a) {
   const int n_lane = n0 + col + (CT == 2 ? 8 * (l16 >> 2) + (l16 & 3) : l16);
   const bool active = set < L::SETS && n0 + col < a.N;
   const int r0 = OUT ? 0 : set * L::RPS * 16;
+
+  // this wave's place in a state in register order
+  const uint32_t image_elems = (a.N + 16 * CT - 1) / (16 * CT) * 16 * CT * a.R;
+  const uint32_t image_at = (n0 + col) * a.R * 4 + lane * 16;
 
   // Rows of the next chunk, loaded ahead into registers as 16-byte pieces.
   // Row r of the walk is token t0 + r, backwards t0 + len - 1 - r: counted
@@ -442,17 +457,24 @@ void linattn_walk_kernel(Walk a) {
   // the state's, and a state that is not there, read zeros from no memory).
   floatx4 S[L::RPS][CT];
   if constexpr (OUT) {
-    const uint32_t bytes = a.enter == nullptr ? 0 : static_cast<uint32_t>(a.R) * a.N * 4;
+    const uint32_t elems = a.image ? image_elems : a.R * a.N;
     const __amdgpu_buffer_rsrc_t rs =
         make_rsrc(a.enter + (a.enter == nullptr
                                  ? 0
-                                 : (static_cast<int64_t>(slot) * a.H + h) * a.R * a.N),
-                  bytes);
+                                 : (static_cast<int64_t>(slot) * a.H + h) * elems),
+                  a.enter == nullptr ? 0 : elems * 4);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       const int n = n_lane + 4 * ct;
       const bool in = active && n < a.N;
-      if (a.turned) {
+      if (a.image) {
+        const uint32_t at = active ? image_at + ct * 1024 : kOob;
+#pragma unroll
+        for (int rt = 0; rt < L::RPS; ++rt)
+          S[rt][ct] = __builtin_bit_cast(
+              floatx4, __builtin_amdgcn_raw_buffer_load_b128(
+                           rs, at, rt * 16 < a.R ? rt * CT * 1024 : 0x40000000, 0));
+      } else if (a.turned) {
         const uint32_t at = in ? (n * a.R + 4 * g) * 4 : kOob;
 #pragma unroll
         for (int rt = 0; rt < L::RPS; ++rt)
@@ -567,7 +589,7 @@ void linattn_walk_kernel(Walk a) {
         for (int e = 0; e < 4; ++e)
           S[rt][ct][e] = __builtin_fmaf(S[rt][ct][e], mul, add * S[rt][ct][e]);
     };
-    constexpr int GR = std::min(2, L::RPS);  // state row tiles a step
+    constexpr int GR = OUT ? std::min(2, L::RPS) : 1;  // state row tiles a step
     constexpr int PER = L::RPS / GR;         // steps a 32-row block
     opvec<IO> yf[2][GR], zf[CT];
     auto read_z = [&](int kb) __attribute__((always_inline)) {
@@ -729,11 +751,17 @@ void linattn_walk_kernel(Walk a) {
   if (bh != nullptr && active && (OUT ? last && set == 0 : true)) {
     const int64_t at = OUT ? static_cast<int64_t>(seg.seq) * a.H + h
                            : static_cast<int64_t>(slot) * a.H + h;
-    bh += at * a.R * a.N;
+    bh += at * (!OUT && a.image ? image_elems : a.R * a.N);
 #pragma unroll
     for (int rt = 0; rt < L::RPS; ++rt)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
+        if (!OUT && a.image) {
+          if (r0 + rt * 16 < a.R)
+            *reinterpret_cast<floatx4*>(bh + (n0 + col) * a.R + ((r0 / 16 + rt) * CT + ct) * 256 +
+                                        again * 4) = S[rt][ct];
+          continue;
+        }
         const int r = r0 + rt * 16 + 4 * (again >> 4), 
                   n = n0 + col + (CT == 2 ? 8 * ((again & 15) >> 2) + (again & 3) + 4 * ct : again & 15);
         if (r >= a.R || n >= a.N) continue;
@@ -748,10 +776,14 @@ void linattn_walk_kernel(Walk a) {
 // segment's own contribution (all but the last in walk order) and becomes
 // the state entering it,  E' = a^len E + own.  A thread carries four state
 // elements through the sequence's segments; loads run ahead of the chain.
+// image: buf holds the states in register order (Walk::image, with CT column
+// tiles a block); init is a [dk, dv] matrix.
 template <bool REV>
-__global__ __launch_bounds__(256) void linattn_combine_kernel(Cut cut, int H, int elems,
-                                                              const float* log_decay,
+__global__ __launch_bounds__(256) void linattn_combine_kernel(Cut cut, int H, int R, int N,
+                                                              int image, const float* log_decay,
                                                               const float* init, float* buf) {
+  const int CT = N > 64 ? 2 : 1;
+  const int elems = image ? (N + 16 * CT - 1) / (16 * CT) * 16 * CT * R : R * N;
   const int nblk = (elems / 4 + 255) / 256;
   const int blk = blockIdx.x % nblk;
   const int h = (blockIdx.x / nblk) % H;
@@ -776,25 +808,40 @@ __global__ __launch_bounds__(256) void linattn_combine_kernel(Cut cut, int H, in
   }
   const int e4 = blk * 256 + threadIdx.x;
   if (e4 >= elems / 4) return;
-  const double log_a = log_decay == nullptr ? 0.0 : static_cast<double>(log_decay[h]);
-  const double ds = decay_pow(log_a, cut.span);
-  const double dt = decay_pow(log_a, len - (n - 1) * cut.span);  // the last segment's
-
-  floatx4 E = {0.f, 0.f, 0.f, 0.f};
-  if (init != nullptr)
-    E = *reinterpret_cast<const floatx4*>(init + (static_cast<int64_t>(seq) * H + h) * elems +
-                                          4 * e4);
   auto at = [&](int w) {  // w: index in walk order
     const int j = REV ? n - 1 - w : w;
     return reinterpret_cast<floatx4*>(
         buf + (static_cast<int64_t>(first + j) * H + h) * elems + 4 * e4);
   };
-  constexpr int kAhead = 8;
-  for (int w0 = 0; w0 < n; w0 += kAhead) {
-    floatx4 own[kAhead];
+  constexpr int kAhead = 16;
+  floatx4 own[kAhead];
+  auto load = [&](int w0) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
       if (w0 + u < n - 1) own[u] = *at(w0 + u);
+  };
+  load(0);
+
+  floatx4 E = {0.f, 0.f, 0.f, 0.f};
+  if (init != nullptr) {
+    init += (static_cast<int64_t>(seq) * H + h) * R * N;
+    if (image) {
+      const int lane = e4 & 63, tile = e4 >> 6, l16 = lane & 15;
+      const int ct = tile % CT, rt = tile / CT % (R / 16), cb = tile / (CT * (R / 16));
+      const int col = cb * 16 * CT + (CT == 2 ? 8 * (l16 >> 2) + (l16 & 3) + 4 * ct : l16);
+      if (col < N) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) E[e] = init[(rt * 16 + 4 * (lane >> 4) + e) * N + col];
+      }
+    } else {
+      E = *reinterpret_cast<const floatx4*>(init + 4 * e4);
+    }
+  }
+  const double log_a = log_decay == nullptr ? 0.0 : static_cast<double>(ld_scalar(log_decay, h));
+  const double ds = decay_pow(log_a, cut.span);
+  const double dt = REV ? decay_pow(log_a, len - (n - 1) * cut.span) : ds;  // the last segment's
+  for (int w0 = 0; w0 < n; w0 += kAhead) {
+    if (w0 > 0) load(w0);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (w0 + u >= n) break;
@@ -907,16 +954,29 @@ Plan plan_walk(const LinAttn& p) {
   const int C = p.io == GDN_BF16 ? 64 : 32;
   Plan r;
   const int64_t nch = (static_cast<int64_t>(p.T) + C - 1) / C;  // of one dense sequence, or all
-  const int64_t slabs = (p.dv + 127) / 128;
+  const int64_t chains = static_cast<int64_t>(p.nseq) * p.H * ((p.dv + 127) / 128);
+  const int64_t units = p.varlen ? nch * (chains / p.nseq) : nch * chains;  // chunks to walk
   int64_t L = nch;  // chunks per segment
   if (p.seg_req > 0) {
     L = std::min<int64_t>(nch, p.seg_req);
-  } else if (p.seg_req == 0) {
-    // workgroups when nothing is split: one chain of chunks each
-    const int64_t total = nch * (p.varlen ? 1 : p.nseq) * p.H * slabs;
-    const int64_t fill = (total + 255) / 256;
-    L = std::max<int64_t>(fill, 2);
-    if (!p.varlen && static_cast<int64_t>(p.nseq) * p.H * slabs >= 256) L = nch;
+  } else if (p.seg_req == 0 && nch > 6) {
+    // (six chunks or fewer are walked faster than two more launches take)
+    if (p.varlen) {
+      // Segments for two workgroups a CU (512), in whole rounds: each chain
+      // ends in a segment that is half full on average, which may take up
+      // to a quarter of a round (65k tokens in 7 sequences: 37 chunks 390 us,
+      // 12: 441; 32k in 24: 10 to 12 chunks 232, 26: 251)
+      const int64_t all = std::max<int64_t>(512, (2 * chains + 511) / 512 * 512);
+      const int64_t room = all - chains / 2;
+      L = (units + room - 1) / room;
+    } else {
+      // One workgroup a CU while walks are short, since every further segment
+      // costs four passes over its state (T4096 H16: 4 chunks 51 us, 2: 60;
+      // T16384 H8: 8 chunks 79, 4: 91); two where they are long.
+      const int64_t target = units < 48 * 256 ? 256 : 512;
+      const int64_t per_seq = std::max<int64_t>(1, target / chains);
+      L = (nch + per_seq - 1) / per_seq;
+    }
     L = std::min(L, nch);
   }
   L = std::max<int64_t>(L, 1);
@@ -980,22 +1040,25 @@ hipError_t launch_walk(const LinAttn& p, const Walk& w, int64_t slots, bool out,
   return hipGetLastError();
 }
 
-hipError_t launch_combine(const LinAttn& p, const Cut& cut, bool rev, const float* la,
+// Elements of a state in register order: whole column blocks.
+int image_elems(const LinAttn& p) { return p.dk * (p.dv > 64 ? (p.dv + 31) / 32 * 32 : p.dv); }
+
+hipError_t launch_combine(const LinAttn& p, const Cut& cut, bool rev, bool image, const float* la,
                           const float* init, float* buf, hipStream_t s) {
   StageScope scope(GDN_STAGE_FWD_COMBINE, s);
-  const int elems = p.dk * p.dv;
+  const int elems = image ? image_elems(p) : p.dk * p.dv;
   const int64_t grid = static_cast<int64_t>(p.nseq) * p.H * ((elems / 4 + 255) / 256);
   if (rev)
     hipLaunchKernelGGL(linattn_combine_kernel<true>, dim3(static_cast<unsigned>(grid)), dim3(256),
-                       0, s, cut, p.H, elems, la, init, buf);
+                       0, s, cut, p.H, p.dk, p.dv, image ? 1 : 0, la, init, buf);
   else
     hipLaunchKernelGGL(linattn_combine_kernel<false>, dim3(static_cast<unsigned>(grid)),
-                       dim3(256), 0, s, cut, p.H, elems, la, init, buf);
+                       dim3(256), 0, s, cut, p.H, p.dk, p.dv, image ? 1 : 0, la, init, buf);
   return hipGetLastError();
 }
 
 // States in front of every segment into `buf`: own contributions, chained.
-hipError_t enter_states(const LinAttn& p, const Plan& pl, bool rev, const void* y, const void* z,
+hipError_t enter_states(const LinAttn& p, const Plan& pl, bool rev, bool image, const void* y, const void* z,
                         int hy, int hz, const float* la, const float* init, float* buf,
                         hipStream_t s) {
   Walk w{};
@@ -1010,13 +1073,14 @@ hipError_t enter_states(const LinAttn& p, const Plan& pl, bool rev, const void* 
   w.N = p.dv;
   w.log_decay = la;
   w.behind = buf;
+  w.image = image ? 1 : 0;
   hipError_t e = launch_walk(p, w, pl.slots, false, rev, GDN_STAGE_FWD_TRANS, s);
   if (e != hipSuccess) return e;
-  return launch_combine(p, w.cut, rev, la, init, buf, s);
+  return launch_combine(p, w.cut, rev, image, la, init, buf, s);
 }
 
 size_t state_bytes(const LinAttn& p, const Plan& pl) {
-  return pl.split ? al256(static_cast<size_t>(pl.slots) * p.H * p.dk * p.dv * 4) : 0;
+  return pl.split ? al256(static_cast<size_t>(pl.slots) * p.H * image_elems(p) * 4) : 0;
 }
 
 size_t part_bytes(const LinAttn& p) {
@@ -1040,7 +1104,7 @@ void launch_decode_dk(const LinAttn& p, const void* q, const void* k, const void
 bool linattn_grid_ok(const LinAttn& p) {
   const Plan pl = plan_walk(p);
   const int64_t most = (int64_t(1) << 31) - 1;
-  const int64_t blocks = (static_cast<int64_t>(p.dk) * p.dv / 4 + 255) / 256;
+  const int64_t blocks = (static_cast<int64_t>(image_elems(p)) / 4 + 255) / 256;
   return pl.slots * p.H * 2 <= most && static_cast<int64_t>(p.nseq) * p.H * blocks <= most;
 }
 
@@ -1055,9 +1119,10 @@ hipError_t launch_linattn_fwd(const LinAttn& p, const void* q, const void* k, co
   w.enter = s0;
   if (pl.split) {
     float* buf = static_cast<float*>(ws);
-    const hipError_t e = enter_states(p, pl, false, k, v, p.hq, p.H, la, s0, buf, s);
+    const hipError_t e = enter_states(p, pl, false, true, k, v, p.hq, p.H, la, s0, buf, s);
     if (e != hipSuccess) return e;
     w.enter = buf;
+    w.image = 1;
   }
   w.x = q;
   w.y = k;
@@ -1089,9 +1154,9 @@ hipError_t launch_linattn_bwd(const LinAttn& p, const void* q, const void* k, co
     at += state_bytes(p, pl);
     float* bb = reinterpret_cast<float*>(at);
     at += state_bytes(p, pl);
-    e = enter_states(p, pl, false, k, v, p.hq, p.H, la, s0, bf, s);
+    e = enter_states(p, pl, false, false, k, v, p.hq, p.H, la, s0, bf, s);
     if (e != hipSuccess) return e;
-    e = enter_states(p, pl, true, q, d_o, p.hq, p.H, la, ds_final, bb, s);
+    e = enter_states(p, pl, true, false, q, d_o, p.hq, p.H, la, ds_final, bb, s);
     if (e != hipSuccess) return e;
     front = bf;
     back = bb;
