@@ -555,27 +555,24 @@ def decode_step(q, k, v, beta, log_alpha, state):
 
 # ------------------------------------------- linear attention, group norm ---
 
-class _On:
-    """Makes ``device`` current for a launch, where it is not already."""
-
-    def __init__(self, device):
-        self._guard = (None if device.index == torch.cuda.current_device()
-                       else torch.cuda.device(device))
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+def _launch(fn, device, *args):
+    """fn(*args, stream) on ``device``'s current stream, with the device made
+    current where it is not, and the status checked."""
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream)
+    if st != _lib.GDN_OK:
+        _lib.check(st, fn.__name__)
 
 
 def _want(t, name, shape, dtype, device):
     """Checks an argument tensor; None passes."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
@@ -609,16 +606,11 @@ def _linattn_problem(q, k, v, log_decay, cu_seqlens, seg_chunks, lead):
     _check_cu(cu_seqlens, q)
     if cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2):
         raise ValueError("cu_seqlens must hold the bounds of at least one sequence")
-    p = _lib.GdnProblem()
-    p.B, p.T, p.H, p.dk, p.dv, p.chunk = q.shape[0], (q.shape[1] if lead == 2 else 1), H, dk, dv, 0
-    p.nseq = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
-    p.cu_seqlens = _ptr(cu_seqlens)
-    p.io_dtype = _dtype_code(q)
-    p.gate_dtype = _lib.GDN_F32
-    p.gate = _lib.GDN_GATE_NONE
-    p.seg_chunks = int(seg_chunks)
-    nseq = q.shape[0] if cu_seqlens is None else p.nseq
-    return p, hq, (nseq, H, dk, dv)
+    packed = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+    p = _lib.GdnProblem(q.shape[0], q.shape[1] if lead == 2 else 1, H, dk, dv, 0, packed,
+                        _ptr(cu_seqlens), _dtype_code(q), _lib.GDN_F32, _lib.GDN_GATE_NONE,
+                        int(seg_chunks))
+    return p, hq, (packed or q.shape[0], H, dk, dv)
 
 
 def linear_attn_fwd(q, k, v, log_decay=None, s0=None, cu_seqlens=None,
@@ -637,11 +629,8 @@ def linear_attn_fwd(q, k, v, log_decay=None, s0=None, cu_seqlens=None,
     o = _out(o, v.shape, q.dtype, q.device)
     sf = _out(s_final, states, torch.float32, q.device) if output_final_state else None
     ws, nbytes = _workspace(workspace, _bytes(lib.gdn_linear_attn_fwd_workspace, p, hq), q.device)
-    with _On(q.device):
-        st = lib.gdn_linear_attn_fwd(ctypes.byref(p), hq, _ptr(q), _ptr(k), _ptr(v),
-                                     _ptr(log_decay), _ptr(s0), _ptr(o), _ptr(sf), _ptr(ws),
-                                     nbytes, _stream(q.device))
-    _lib.check(st, "gdn_linear_attn_fwd")
+    _launch(lib.gdn_linear_attn_fwd, q.device, ctypes.byref(p), hq, _ptr(q), _ptr(k), _ptr(v),
+            _ptr(log_decay), _ptr(s0), _ptr(o), _ptr(sf), _ptr(ws), nbytes)
     return o, sf
 
 
@@ -662,12 +651,9 @@ def linear_attn_bwd(q, k, v, log_decay, s0, d_o, ds_final=None, cu_seqlens=None,
     dv = _out(out[2], v.shape, v.dtype, q.device)
     ds0 = _out(out[3], states, torch.float32, q.device) if need_ds0 else None
     ws, nbytes = _workspace(workspace, _bytes(lib.gdn_linear_attn_bwd_workspace, p, hq), q.device)
-    with _On(q.device):
-        st = lib.gdn_linear_attn_bwd(ctypes.byref(p), hq, _ptr(q), _ptr(k), _ptr(v),
-                                     _ptr(log_decay), _ptr(s0), _ptr(d_o), _ptr(ds_final),
-                                     _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ds0), _ptr(ws), nbytes,
-                                     _stream(q.device))
-    _lib.check(st, "gdn_linear_attn_bwd")
+    _launch(lib.gdn_linear_attn_bwd, q.device, ctypes.byref(p), hq, _ptr(q), _ptr(k), _ptr(v),
+            _ptr(log_decay), _ptr(s0), _ptr(d_o), _ptr(ds_final), _ptr(dq), _ptr(dk), _ptr(dv),
+            _ptr(ds0), _ptr(ws), nbytes)
     return dq, dk, dv, ds0
 
 
@@ -682,11 +668,8 @@ def linear_attn_decode_step(q, k, v, log_decay, state, o=None):
         raise ValueError("state must be given")
     _want(state, "state", states, torch.float32, q.device)
     o = _out(o, v.shape, q.dtype, q.device)
-    with _On(q.device):
-        st = lib.gdn_linear_attn_decode_step(ctypes.byref(p), hq, _ptr(q), _ptr(k), _ptr(v),
-                                             _ptr(log_decay), _ptr(state), _ptr(o),
-                                             _stream(q.device))
-    _lib.check(st, "gdn_linear_attn_decode_step")
+    _launch(lib.gdn_linear_attn_decode_step, q.device, ctypes.byref(p), hq, _ptr(q), _ptr(k),
+            _ptr(v), _ptr(log_decay), _ptr(state), _ptr(o))
     return o
 
 
@@ -707,9 +690,7 @@ def _norm_problem(x, weight, bias, gate, act):
     shared = one is not None and one.dim() == 1
     for t, name in ((weight, "weight"), (bias, "bias")):
         _want(t, name, (d,) if shared else (H, d), torch.float32, x.device)
-    p = _lib.GdnProblem()
-    p.B, p.T, p.H, p.dk, p.dv = B, T, H, d, d
-    p.io_dtype = _dtype_code(x)
+    p = _lib.GdnProblem(B, T, H, d, d, 0, 0, None, _dtype_code(x))
     return p, _ACTS[act], int(shared)
 
 
@@ -724,11 +705,8 @@ def group_norm_fwd(x, weight=None, bias=None, gate=None, act: str = "silu", eps:
     lib = _lib.load()
     p, code, shared = _norm_problem(x, weight, bias, gate, act)
     y = _out(y, x.shape, x.dtype, x.device)
-    with _On(x.device):
-        st = lib.gdn_group_norm_fwd(ctypes.byref(p), x.shape[-1], code, int(center), shared, eps,
-                                    _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y),
-                                    _stream(x.device))
-    _lib.check(st, "gdn_group_norm_fwd")
+    _launch(lib.gdn_group_norm_fwd, x.device, ctypes.byref(p), p.dv, code, int(center), shared,
+            eps, _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y))
     return y
 
 
@@ -745,10 +723,7 @@ def group_norm_bwd(x, dy, weight=None, bias=None, gate=None, act: str = "silu",
     dz, dw, db = (None if t is None else torch.empty_like(t) for t in (gate, weight, bias))
     ws, nbytes = _workspace(workspace, _bytes(lib.gdn_group_norm_bwd_workspace, p, x.shape[-1]),
                             x.device)
-    with _On(x.device):
-        st = lib.gdn_group_norm_bwd(ctypes.byref(p), x.shape[-1], code, int(center), shared, eps,
-                                    _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(dy),
-                                    _ptr(dx), _ptr(dz), _ptr(dw), _ptr(db), _ptr(ws), nbytes,
-                                    _stream(x.device))
-    _lib.check(st, "gdn_group_norm_bwd")
+    _launch(lib.gdn_group_norm_bwd, x.device, ctypes.byref(p), p.dv, code, int(center), shared,
+            eps, _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(dy), _ptr(dx), _ptr(dz),
+            _ptr(dw), _ptr(db), _ptr(ws), nbytes)
     return dx, dz, dw, db

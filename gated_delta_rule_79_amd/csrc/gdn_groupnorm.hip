@@ -114,7 +114,8 @@ struct Args {
   const void *x, *z, *dy;
   const float *w, *b;
   void *y, *dx, *dz;
-  float *pw, *pb;   // partial dw, db [stride rows][d]
+  int q;            // rows of partial dw, db a block leaves
+  float *pw, *pb;   // partial dw, db [blocks * q][d]
 };
 
 template <typename IO, int LPR, int ACT, bool GATE, bool BWD>
@@ -182,33 +183,55 @@ __global__ __launch_bounds__(kThreads) void group_norm_kernel(Args a) {
     }
   }
   if constexpr (BWD) {
-    if (live && a.pw != nullptr) store8<f32_t>(a.pw, first * a.d + piece * 8, sw);
-    if (live && a.pb != nullptr) store8<f32_t>(a.pb, first * a.d + piece * 8, sb);
+    // the block's shares of dw, db: rows of the same weights added in order
+    constexpr int PER = kThreads / LPR;
+    __shared__ float t[kThreads * 8];
+    auto leave = [&](float* part, const float* v) {
+      if (part == nullptr) return;
+      __syncthreads();
+      store8<f32_t>(t, threadIdx.x * 8, v);
+      __syncthreads();
+      for (int o = threadIdx.x; o < a.q * a.d; o += kThreads) {
+        const int r = o / a.d, c = o - r * a.d;
+        float s = t[r * LPR * 8 + c];
+        for (int k = r + a.q; k < PER; k += a.q) s += t[k * LPR * 8 + c];
+        part[static_cast<int64_t>(blockIdx.x) * a.q * a.d + o] = s;
+      }
+    };
+    leave(a.pw, sw);
+    leave(a.pb, sb);
   }
 }
 
 // Sums of the partial dw, db rows of each group (row index mod `period`), in
-// a fixed order: out[g, c] = sum_k part[(g + k period), c].  Sixteen columns
-// of one group a workgroup, 16 runs of rows added up in LDS.
-__global__ __launch_bounds__(256) void group_norm_sum_kernel(const float* pw, const float* pb,
-                                                             int64_t rows, int period, int d,
-                                                             float* ow, float* ob) {
+// a fixed order: out[g, c] = sum_k part[g + k period, c].  Sixteen columns of
+// one group a workgroup, 64 runs of rows added up in LDS.
+constexpr int kRuns = 64;
+__global__ __launch_bounds__(16 * kRuns) void group_norm_sum_kernel(const float* pw,
+                                                                    const float* pb, int64_t rows,
+                                                                    int period, int d, float* ow,
+                                                                    float* ob) {
   const float* part = blockIdx.z == 0 ? pw : pb;
   float* out = blockIdx.z == 0 ? ow : ob;
   if (part == nullptr) return;
-  const int c = blockIdx.x * 16 + (threadIdx.x & 15), run = threadIdx.x >> 4;
-  const int g = blockIdx.y;
-  float s = 0.f;
-  for (int64_t k = g + static_cast<int64_t>(run) * period; k < rows; k += 16 * period)
-    s += part[k * d + c];
-  __shared__ float t[16][17];
-  t[run][threadIdx.x & 15] = s;
-  __syncthreads();
-  if (run == 0) {
+  const int lc = threadIdx.x & 15, run = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + lc, g = blockIdx.y;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};  // four rows at a time in flight
+  const int64_t step = static_cast<int64_t>(kRuns) * period;
+  for (int64_t k = g + static_cast<int64_t>(run) * period; k < rows; k += 4 * step) {
 #pragma unroll
-    for (int j = 1; j < 16; ++j) s += t[j][threadIdx.x & 15];
-    out[static_cast<int64_t>(g) * d + c] = s;
+    for (int u = 0; u < 4; ++u)
+      if (k + u * step < rows) s[u] += part[(k + u * step) * d + c];
   }
+  __shared__ float t[kRuns][17];
+  t[run][lc] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+#pragma unroll
+  for (int n = kRuns / 2; n >= 1; n >>= 1) {
+    if (run < n) t[run][lc] += t[run + n][lc];
+    __syncthreads();
+  }
+  if (run == 0) out[static_cast<int64_t>(g) * d + c] = t[0][lc];
 }
 
 int lanes_per_row(int d) {
@@ -225,6 +248,13 @@ int64_t norm_blocks(const GroupNorm& p, int64_t most) {
   const int64_t unit = p.H / std::gcd(p.H, per);  // blocks in a whole number of tokens
   const int64_t want = std::min<int64_t>((rows + per - 1) / per, most);
   return std::max<int64_t>(1, (want + unit - 1) / unit) * unit;
+}
+
+// Rows of partial dw, db a block leaves: one when all groups share their
+// weights, one for each head where its rows are whole tokens, else all.
+int partial_rows(const GroupNorm& p) {
+  const int per = kThreads / lanes_per_row(p.d);
+  return p.shared ? 1 : per % p.H == 0 ? p.H : per;
 }
 
 constexpr int64_t kFwdBlocks = 2048, kBwdBlocks = 1024;
@@ -269,6 +299,7 @@ Args make_args(const GroupNorm& p, int64_t blocks, const void* x, const void* z,
   a.center = p.center ? 1 : 0;
   a.eps = p.eps;
   a.wstride = p.shared ? 0 : p.d;
+  a.q = partial_rows(p);
   a.x = x;
   a.z = z;
   a.w = w;
@@ -292,10 +323,9 @@ hipError_t launch_group_norm_fwd(const GroupNorm& p, const void* x, const void* 
   return hipGetLastError();
 }
 
-// Partial dw and db: one row of d values per row of the grid.
+// Partial dw and db (for weights of each group: a shared set needs less).
 size_t group_norm_bwd_workspace_bytes(const GroupNorm& p) {
-  const int64_t rows = norm_blocks(p, kBwdBlocks) * (kThreads / lanes_per_row(p.d));
-  return 2 * static_cast<size_t>(rows) * p.d * 4;
+  return 2 * static_cast<size_t>(norm_blocks(p, kBwdBlocks) * partial_rows(p)) * p.d * 4;
 }
 
 hipError_t launch_group_norm_bwd(const GroupNorm& p, const void* x, const void* z, const float* w,
@@ -307,7 +337,8 @@ hipError_t launch_group_norm_bwd(const GroupNorm& p, const void* x, const void* 
   a.dx = dx;
   a.dz = dz;
   if (dw != nullptr) a.pw = static_cast<float*>(ws);
-  if (db != nullptr) a.pb = static_cast<float*>(ws) + a.stride * p.d;
+  const int64_t rows = blocks * a.q;
+  if (db != nullptr) a.pb = static_cast<float*>(ws) + rows * p.d;
   StageScope scope(GDN_STAGE_OTHER, s);
   if (p.io == GDN_BF16)
     launch_io<bf16_t, true>(p, a, blocks, s);
@@ -316,8 +347,8 @@ hipError_t launch_group_norm_bwd(const GroupNorm& p, const void* x, const void* 
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (dw == nullptr && db == nullptr)) return e;
   const int period = p.shared ? 1 : p.H;
-  hipLaunchKernelGGL(group_norm_sum_kernel, dim3(p.d / 16, period, 2), dim3(256), 0, s, a.pw, a.pb,
-                     a.stride, period, p.d, dw, db);
+  hipLaunchKernelGGL(group_norm_sum_kernel, dim3(p.d / 16, period, 2), dim3(16 * kRuns), 0, s,
+                     a.pw, a.pb, rows, period, p.d, dw, db);
   return hipGetLastError();
 }
 
