@@ -586,8 +586,10 @@ def _workspace(ws, need, device):
     """The caller's workspace where it is large enough, else a new one."""
     if ws is not None and ws.device != device:
         raise ValueError(f"workspace must be on {device}")
+    if need == 0:
+        return None, 0
     if ws is None or ws.numel() * ws.element_size() < need:
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
     return ws, ws.numel() * ws.element_size()
 
 

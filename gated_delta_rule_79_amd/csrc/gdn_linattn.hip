@@ -15,11 +15,11 @@
 //   dk: (v, do, q),             M = dS^T            from the last token back
 //   dv: (k, q, do),             M = dS              from the last token back
 //
-// so one kernel serves all four (REV: rows taken from the end; the entering
+// so one kernel serves all four (rev: rows taken from the end; the entering
 // state then reaches the first walked token undecayed, and the state handed
 // on is multiplied by a once more).
 //
-// Chunk form over C tokens (i, j: rows in walk order, off = 1, REV: 0):
+// Chunk form over C tokens (i, j: rows in walk order, off = 1, rev: 0):
 //   out_i = a^{i+off} M_in^T x_i + sum_{j<=i} a^{i-j} (x_i . y_j) z_j
 //   M_out = a^len M_in + sum_j a^{len-off-j} y_j z_j^T
 // Every power of a has a non-negative exponent, so no factor overflows for
@@ -201,13 +201,14 @@ __device__ inline opvec<IO> lds_col8(const char* p) {
   }
 }
 
-// A column of 8 weighted values as operand parts, x = p[0] + p[1] + p[2]:
-// bf16 parts leave 2^-9, 2^-18, 2^-27 of x behind; fp32 operands are x itself.
+// A column of 8 weighted values as operand parts.  bf16: N parts after
+// SKIP earlier ones; k parts leave 2^(-9 k) of the value behind.  fp32
+// operands are the value itself.
 template <typename IO> struct Parts;
 template <> struct Parts<f32_t> {
   static constexpr int most = 1;
   floatx8 p[1];
-  template <int N> __device__ inline void set(const floatx8& z, const float* w) {
+  template <int N, int SKIP> __device__ inline void set(const floatx8& z, const float* w) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[0][e] = z[e] * w[e];
   }
@@ -215,22 +216,27 @@ template <> struct Parts<f32_t> {
 template <> struct Parts<bf16_t> {
   static constexpr int most = 3;
   bf16x8 p[3];
-  template <int N> __device__ inline void set(const bf16x8& z, const float* w) {
+  template <int N, int SKIP> __device__ inline void set(const bf16x8& z, const float* w) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    u32x4 out[3];
+    u32x4 out[N];
     const u32x4 in = __builtin_bit_cast(u32x4, z);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float a = __uint_as_float(in[e] << 16) * w[2 * e];
       float b = __uint_as_float(in[e] & 0xffff0000u) * w[2 * e + 1];
+      auto round = [&]() __attribute__((always_inline)) {
+        return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+      };
+      auto rest = [&](uint32_t r) __attribute__((always_inline)) {
+        a -= __uint_as_float(r << 16);
+        b -= __uint_as_float(r & 0xffff0000u);
+      };
+#pragma unroll
+      for (int u = 0; u < SKIP; ++u) rest(round());
 #pragma unroll
       for (int u = 0; u < N; ++u) {
-        const uint32_t r = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
-        out[u][e] = r;
-        if (u + 1 < N) {
-          a -= __uint_as_float(r << 16);
-          b -= __uint_as_float(r & 0xffff0000u);
-        }
+        out[u][e] = round();
+        if (u + 1 < N) rest(out[u][e]);
       }
     }
 #pragma unroll
@@ -242,6 +248,7 @@ template <> struct Parts<bf16_t> {
 
 struct Walk {
   Cut cut;
+  int rev;                // from the last token back
   const void *x, *y, *z;  // [tokens, hx, R], [tokens, hy, R], [tokens, hz, N]
   int hx, hy, hz;         // heads of each; head h of H reads h / (H / hx) ...
   int H, R, N;
@@ -255,9 +262,11 @@ struct Walk {
   // enter (OUT) and behind (not OUT) in register order instead: per 16 CT
   // columns and 16 rows, CT tiles of 64 lanes' four rows
   int image;
-  // state behind the walk: of each (sequence, head), by its last segment in
-  // walk order (OUT); of each (slot, head) but those (not OUT)
+  // state behind the walk: of each (sequence, head), where a segment is the
+  // whole sequence (OUT); of each (slot, head), the last ones in walk order
+  // only if `ends` (not OUT)
   float* behind;
+  int ends;
 };
 
 // Tiles of a workgroup: R up to 32 NKB, slabs of NP columns.  A wave owns CT
@@ -296,20 +305,25 @@ struct WalkTiles {
 // registers.  Per chunk: rows of x, y, z arrive in LDS from registers that
 // were loaded during the previous chunk; x y^T on the matrix cores, decayed
 // and rounded once into operand fragments in LDS; out^T = M^T x^T (from the
-// state's registers, re-packed as an operand), scaled in fp32; the state
-// update; plus z^T (x y^T)^T, stored at the start of the next chunk, where
-// the loads being waited for are older than the stores.
+// state's registers, re-packed as an operand), scaled in fp32, plus
+// z^T (x y^T)^T, stored at once; the state update last, while the stores
+// drain.
 // The update's weights go onto z in fp32, and the product is split into
 // bf16 parts, so the carried state keeps the fp32 accuracy of its storage.
 // Operand reads run one step ahead of the products that take them
 // (scheduling barriers hold them there).
-template <typename IO, int NKB, int NP, bool OUT, bool REV>
-__global__ __launch_bounds__((WalkTiles<IO, NKB, NP, OUT>::threads), OUT ? 2 : 3)
-void linattn_walk_kernel(Walk a) {
+// One launch takes up to three walks of the same tiles (a backward's), so
+// that short ones share the machine.
+struct Walks {
+  Walk w[3];
+  int n;
+};
+
+template <typename IO, int NKB, int NP, bool OUT, bool rev>
+__device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int slot, char* lds) {
   using L = WalkTiles<IO, NKB, NP, OUT>;
-  constexpr int C = L::C, NI = L::NI, NKC = L::NKC, CT = L::CT, ob = L::ob, off = REV ? 0 : 1;
+  constexpr int C = L::C, NI = L::NI, NKC = L::NKC, CT = L::CT, ob = L::ob, off = rev ? 0 : 1;
   constexpr int kThreads = L::threads;
-  __shared__ __align__(16) char lds[L::bytes];
   char* const tx = lds;
   char* const ty = lds + L::off_y;
   char* const tz = lds + L::off_z;
@@ -317,23 +331,10 @@ void linattn_walk_kernel(Walk a) {
   float* const dec = reinterpret_cast<float*>(lds + L::off_d) + 32;  // a^0 .. a^C, 0 below
   float* const wgt = reinterpret_cast<float*>(lds + L::off_w);       // update weights of rows
 
-  const int nslab = (a.N + NP - 1) / NP;
-  // Consecutive workgroups go round the 8 XCDs.  Items (segment, head) follow
-  // each other that way, so that unused slots and short segments fall on all
-  // of them alike; the slabs of one item, which read the same x and y rows,
-  // are 8 workgroups apart and so share an L2.
-  const int full = gridDim.x / (8 * nslab) * 8;  // items in whole groups of 8
-  const int id = blockIdx.x;
-  int slab = (id >> 3) % nslab, item = (id / (8 * nslab)) * 8 + (id & 7);
-  if (id >= full * nslab) {
-    slab = (id - full * nslab) % nslab;
-    item = full + (id - full * nslab) / nslab;
-  }
-  const int h = item % a.H, slot = item / a.H;
   const Segment seg = find_segment(a.cut, slot);
   if (seg.seq < 0) return;
-  const bool last = REV ? seg.j == 0 : seg.j == seg.n - 1;  // in walk order
-  if (!OUT && last) return;
+  const bool last = rev ? seg.j == 0 : seg.j == seg.n - 1;  // in walk order
+  if (!OUT && last && !a.ends) return;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -352,9 +353,10 @@ void linattn_walk_kernel(Walk a) {
   const uint32_t image_at = (n0 + col) * a.R * 4 + lane * 16;
 
   // Rows of the next chunk, loaded ahead into registers as 16-byte pieces.
-  // Row r of the walk is token t0 + r, backwards t0 + len - 1 - r: counted
-  // from the row that would be a full chunk's last, so that a lane's offsets
-  // do not depend on the chunk.  Rows past len and columns past the width
+  // Row r of the walk is token t0 + r, backwards t0 + len - 1 - r.  Tokens are
+  // loaded in order, backwards from the one that would be a full chunk's
+  // first, so that a lane's offsets do not depend on the chunk, and turned
+  // round on their way into LDS.  Rows past len and columns past the width
   // read zeros from no memory.
   using PX = std::integral_constant<int, L::px>;
   using PZ = std::integral_constant<int, L::pz>;
@@ -363,31 +365,46 @@ void linattn_walk_kernel(Walk a) {
   const int nch = (seg.len + C - 1) / C;
   uint4 rx[OUT ? L::nx : 1], ry[L::nx], rz[L::nz];
   auto chunk_of = [&](int c, int64_t* t0, int* len) __attribute__((always_inline)) {
-    const int w = REV ? nch - 1 - c : c;
+    const int w = rev ? nch - 1 - c : c;
     *t0 = seg.tok0 + static_cast<int64_t>(w) * C;
     *len = min(C, seg.len - w * C);
+  };
+  // a thread's row among the `step` rows of a turn, as a token
+  auto turned_row = [&](int row, int step) __attribute__((always_inline)) {
+    return rev ? std::min(step, C) - 1 - row : row;
+  };
+  // calls put(register, turn in LDS) for a thread's pieces
+  auto each_turn = [&](auto turns, auto put) __attribute__((always_inline)) {
+    constexpr int NT = decltype(turns)::value;
+    if (rev) {
+#pragma unroll
+      for (int u = 0; u < NT; ++u) put(u, NT - 1 - u);
+    } else {
+#pragma unroll
+      for (int u = 0; u < NT; ++u) put(u, u);
+    }
   };
   auto load_rows = [&](const void* base, int heads, int width, int col0, auto per_row, auto turns,
                        int64_t t0, int len, uint4* r) __attribute__((always_inline)) {
     constexpr int PR = decltype(per_row)::value, NT = decltype(turns)::value;
     constexpr int step = kThreads / PR;
     const uint32_t stride = static_cast<uint32_t>(heads) * width * ob;
-    const int64_t row0 = REV ? t0 + len - C : t0;
+    const int64_t row0 = rev ? t0 + len - C : t0;
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(
         static_cast<const char*>(base) +
             (row0 * heads + h / (a.H / heads)) * static_cast<int64_t>(width) * ob + col0 * ob,
         kOob);
-    const int row = tid / PR, c16 = (tid % PR) * 16;
+    const int row = turned_row(tid / PR, step), c16 = (tid % PR) * 16;
     const bool in = c16 < (width - col0) * ob;
     // one offset a lane, the turns' rows in the scalar offset
-    const uint32_t at =
-        static_cast<uint32_t>(REV ? C - 1 - row - (NT - 1) * step : row) * stride + c16;
+    const uint32_t at = static_cast<uint32_t>(row) * stride + c16;
+    const uint32_t from = row - (rev ? C - len : 0);
 #pragma unroll
     for (int u = 0; u < NT; ++u)
       r[u] = __builtin_bit_cast(
           uint4, __builtin_amdgcn_raw_buffer_load_b128(
-                     rs, in && row + u * step < len ? at : kOob,
-                     (REV ? NT - 1 - u : u) * step * stride, 0));
+                     rs, in && from + u * step < static_cast<uint32_t>(len) ? at : kOob,
+                     u * step * stride, 0));
   };
   // bit 0 of `which`: x, 1: y, 2: z
   auto load_chunk = [&](int c, auto which) __attribute__((always_inline)) {
@@ -405,10 +422,10 @@ void linattn_walk_kernel(Walk a) {
                   NT = decltype(turns)::value, step = kThreads / PR;
     const int row = tid / PR;
     char* p = t + row * ST * ob + (tid % PR) * 16;
-    if (C % step == 0 || row < C) {
-#pragma unroll
-      for (int u = 0; u < NT; ++u) *reinterpret_cast<uint4*>(p + u * step * ST * ob) = r[u];
-    }
+    if (C % step == 0 || row < C)
+      each_turn(turns, [&](int u, int t) __attribute__((always_inline)) {
+        *reinterpret_cast<uint4*>(p + t * step * ST * ob) = r[u];
+      });
   };
   // x rows with the columns of each 32-block in the permuted K order, so that
   // a fragment that matches the state's registers is one 16-byte read
@@ -419,15 +436,15 @@ void linattn_walk_kernel(Walk a) {
     if (C % step == 0 || row < C) {
       if constexpr (ob == 2) {
         p += (q / 4 * 32 + 16 * (q & 1) + 4 * ((q >> 1) & 1)) * 2;
-#pragma unroll
-        for (int u = 0; u < L::nx; ++u) {
-          *reinterpret_cast<uint2*>(p + u * step * L::sx * 2) = make_uint2(rx[u].x, rx[u].y);
-          *reinterpret_cast<uint2*>(p + u * step * L::sx * 2 + 16) = make_uint2(rx[u].z, rx[u].w);
-        }
+        each_turn(NX(), [&](int u, int t) __attribute__((always_inline)) {
+          *reinterpret_cast<uint2*>(p + t * step * L::sx * 2) = make_uint2(rx[u].x, rx[u].y);
+          *reinterpret_cast<uint2*>(p + t * step * L::sx * 2 + 16) = make_uint2(rx[u].z, rx[u].w);
+        });
       } else {
         p += (q / 8 * 32 + 8 * (q & 3) + 4 * ((q >> 2) & 1)) * 4;
-#pragma unroll
-        for (int u = 0; u < L::nx; ++u) *reinterpret_cast<uint4*>(p + u * step * L::sx * 4) = rx[u];
+        each_turn(NX(), [&](int u, int t) __attribute__((always_inline)) {
+          *reinterpret_cast<uint4*>(p + t * step * L::sx * 4) = rx[u];
+        });
       }
     }
   };
@@ -442,12 +459,11 @@ void linattn_walk_kernel(Walk a) {
       const int row = tid / L::px;
       char* p = ty + (row * L::sy + L::skew * ((row >> 2) & 3)) * 2 + (tid % L::px) * 16;
       if (C % step == 0 || row < C) {
-#pragma unroll
-        for (int u = 0; u < L::nx; ++u) {
-          char* const q = p + (u * step * L::sy + (u & 1) * odd) * 2;
+        each_turn(NX(), [&](int u, int t) __attribute__((always_inline)) {
+          char* const q = p + (t * step * L::sy + (t & 1) * odd) * 2;
           *reinterpret_cast<uint2*>(q) = make_uint2(ry[u].x, ry[u].y);
           *reinterpret_cast<uint2*>(q + 8) = make_uint2(ry[u].z, ry[u].w);
-        }
+        });
       }
     }
   };
@@ -526,34 +542,7 @@ void linattn_walk_kernel(Walk a) {
   const char* const p_run = tp + (set * NKC * 64 + lane) * 8 * ob;
   const int os = a.out_f32 ? 4 : ob;  // bytes per output element
   const uint32_t ostride = static_cast<uint32_t>(a.H) * a.N * os;
-  const uint32_t o_lane = (REV ? 15 - l16 : l16) * ostride + (n0 + col + 4 * CT * g) * os;
-
-  floatx4 acc[OUT ? L::IPS : 1][CT];
-  // output rows of chunk c, from acc
-  auto store_out = [&](int c) __attribute__((always_inline)) {
-    int64_t t0;
-    int len;
-    chunk_of(c, &t0, &len);
-    // uniform base of the chunk's rows (backwards: of a full chunk's)
-    char* const orow = static_cast<char*>(a.out) +
-                       ((REV ? t0 + len - C : t0) * a.H + h) * static_cast<int64_t>(a.N) * os;
-#pragma unroll
-    for (int u = 0; u < L::IPS; ++u) {
-      const int it = set + u * L::SETS;
-      char* const p =
-          orow + static_cast<int64_t>((REV ? NI - 1 - it : it) * 16) * ostride + o_lane;
-      if (it * 16 + l16 < len && n0 + col + 4 * CT * g < a.N) {
-        if (ob == 4 || a.out_f32) {
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) *reinterpret_cast<floatx4*>(p + ct * 16) = acc[u][ct];
-        } else if constexpr (CT == 2) {
-          *reinterpret_cast<opvec<IO>*>(p) = pack2<IO>(acc[u][0], acc[u][1]);
-        } else {
-          *reinterpret_cast<typename acc4<IO>::type*>(p) = from_f4<IO>(acc[u][0]);
-        }
-      }
-    }
-  };
+  const uint32_t o_lane = (rev ? 15 - l16 : l16) * ostride + (n0 + col + 4 * CT * g) * os;
 
   // Two stacked tiles of x y^T, transposed (column i, rows j): row tiles
   // 2 jp and 2 jp + 1 of y against tile `it` of x, one operand fragment.
@@ -578,9 +567,11 @@ void linattn_walk_kernel(Walk a) {
         pack2<IO>(p0, p1);
   };
 
-  // M <- a^n M + sum_j y_j (w_j z_j)^T
-  auto update = [&](int n, auto parts) __attribute__((always_inline)) {
-    constexpr int NPART = decltype(parts)::value;
+  // M <- a^n M + sum_j y_j (w_j z_j)^T, the weighted rows in NPART operand
+  // parts (pass 0), or M += their next NPART parts (pass 1)
+  constexpr int NPART = OUT ? std::min(2, Parts<IO>::most) : Parts<IO>::most;
+  auto update = [&](int n, auto which) __attribute__((always_inline)) {
+    constexpr int pass = decltype(which)::value;
     const float mul = n == C ? mul_full : mul_tail, add = n == C ? add_full : add_tail;
     auto fade = [&](int rt) __attribute__((always_inline)) {
 #pragma unroll
@@ -590,7 +581,7 @@ void linattn_walk_kernel(Walk a) {
           S[rt][ct][e] = __builtin_fmaf(S[rt][ct][e], mul, add * S[rt][ct][e]);
     };
     constexpr int GR = OUT ? std::min(2, L::RPS) : 1;  // state row tiles a step
-    constexpr int PER = L::RPS / GR;         // steps a 32-row block
+    constexpr int PER = L::RPS / GR;                   // steps a 32-row block
     opvec<IO> yf[2][GR], zf[CT];
     auto read_z = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
@@ -605,8 +596,10 @@ void linattn_walk_kernel(Walk a) {
     };
     read_z(0);
     read_y(0);
+    if constexpr (pass == 0) {
 #pragma unroll
-    for (int u = 0; u < GR; ++u) fade(u);
+      for (int u = 0; u < GR; ++u) fade(u);
+    }
     Parts<IO> wz[CT];
 #pragma unroll
     for (int step = 0; step < NKC * PER; ++step) {
@@ -619,7 +612,7 @@ void linattn_walk_kernel(Walk a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = lo[e], w[4 + e] = hi[e];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) wz[ct].template set<NPART>(zf[ct], w);
+        for (int ct = 0; ct < CT; ++ct) wz[ct].template set<NPART, pass * NPART>(zf[ct], w);
         if (kb + 1 < NKC) read_z(kb + 1);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -631,7 +624,7 @@ void linattn_walk_kernel(Walk a) {
           for (int ct = 0; ct < CT; ++ct)
             S[rt + v][ct] = mma32(yf[step & 1][v], wz[ct].p[u], S[rt + v][ct]);
       // the next rows' decay, between the products
-      if (kb == 0 && step + 1 < PER) {
+      if (pass == 0 && kb == 0 && step + 1 < PER) {
 #pragma unroll
         for (int u = 0; u < GR; ++u) fade(rt + GR + u);
       }
@@ -643,6 +636,34 @@ void linattn_walk_kernel(Walk a) {
     int64_t t0;
     int len;
     chunk_of(c, &t0, &len);
+    floatx4 acc[OUT ? L::IPS : 1][CT];
+    // the chunk's output rows, from acc
+    auto store_out = [&]() __attribute__((always_inline)) {
+      // uniform base of the chunk's rows (backwards: of a full chunk's)
+      using global = __attribute__((address_space(1))) char;
+      global* const orow = (global*)(a.out) +
+                         ((rev ? t0 + len - C : t0) * a.H + h) * static_cast<int64_t>(a.N) * os;
+      global* p = orow + static_cast<int64_t>((rev ? NI - 1 - set : set) * 16) * ostride;
+      const int64_t next = static_cast<int64_t>(rev ? -16 * L::SETS : 16 * L::SETS) * ostride;
+#pragma unroll
+      for (int u = 0; u < L::IPS; ++u, p += next) {
+        const int it = set + u * L::SETS;
+        if (it * 16 + l16 < len && n0 + col + 4 * CT * g < a.N) {
+          if (ob == 4 || a.out_f32) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+              *(__attribute__((address_space(1))) floatx4*)(p + o_lane + ct * 16) = acc[u][ct];
+          } else if constexpr (CT == 2) {
+            *(__attribute__((address_space(1))) opvec<IO>*)(p + o_lane) =
+                pack2<IO>(acc[u][0], acc[u][1]);
+          } else {
+            *(__attribute__((address_space(1))) typename acc4<IO>::type*)(p + o_lane) =
+                from_f4<IO>(acc[u][0]);
+          }
+        }
+      }
+    };
+
     __syncthreads();  // the previous chunk's tiles have been read
     if constexpr (OUT) put_x();
     put_y();
@@ -651,11 +672,9 @@ void linattn_walk_kernel(Walk a) {
       wlen = len;
       if (tid < C) wgt[tid] = tid < len ? dec[len - off - tid] : 0.f;
     }
-    if constexpr (OUT)
-      if (active && c > 0) store_out(c - 1);
     __syncthreads();
-    // the next chunk's rows, a third at a time: a burst would stall the waves
-    // behind the memory pipe
+    // the next chunk's rows, in two goes: a burst would stall the waves behind
+    // the memory pipe
     if (c + 1 < nch) load_chunk(c + 1, std::integral_constant<int, OUT ? 1 : 6>());
 
     if constexpr (OUT) {
@@ -667,7 +686,7 @@ void linattn_walk_kernel(Walk a) {
       } else {
         if (wave < 6) pair(wave < 2 ? wave : wave < 4 ? 2 : 3, wave < 2 ? 0 : wave & 1);
       }
-      if (c + 1 < nch) load_chunk(c + 1, std::integral_constant<int, 2>());
+      if (c + 1 < nch) load_chunk(c + 1, std::integral_constant<int, 6>());
     }
 
     if (active) {
@@ -705,18 +724,6 @@ void linattn_walk_kernel(Walk a) {
         }
       }
     }
-    if constexpr (OUT)
-      if (c + 1 < nch) load_chunk(c + 1, std::integral_constant<int, 4>());
-    if (active) {
-      // The state behind the chunk, where another chunk or the caller wants
-      // it.  What a caller or another workgroup gets takes all parts; a state
-      // that only multiplies bf16 rows keeps 2^-18 with two.
-      if (!OUT || (last && a.behind != nullptr)) {
-        update(len, std::integral_constant<int, Parts<IO>::most>());
-      } else if (c + 1 < nch) {
-        update(len, std::integral_constant<int, std::min(2, Parts<IO>::most)>());
-      }
-    }
 
     if constexpr (OUT) {
       opvec<IO> zf[NKC][CT];
@@ -738,11 +745,20 @@ void linattn_walk_kernel(Walk a) {
             for (int ct = 0; ct < CT; ++ct) acc[u][ct] = mma32(zf[kb][ct], pf, acc[u][ct]);
           }
         }
+        store_out();
       }
     }
+    if (active) {
+      // The state behind the chunk, where another chunk or the caller wants
+      // it.  One that only multiplies bf16 rows keeps 2^-18 with two parts;
+      // what a caller gets takes a second pass of two more (another
+      // workgroup's: three at once).
+      const bool handed = OUT && last && a.behind != nullptr;
+      if (!OUT || handed || c + 1 < nch) update(len, std::integral_constant<int, 0>());
+      if constexpr (NPART < Parts<IO>::most)
+        if (handed) update(len, std::integral_constant<int, 1>());
+    }
   }
-  if constexpr (OUT)
-    if (active && nch > 0) store_out(nch - 1);
 
   // (the lane's place is worked out again: kept, it costs the loop registers)
   int again = lane;
@@ -771,23 +787,71 @@ void linattn_walk_kernel(Walk a) {
   }
 }
 
+// BOTH: walks in either direction; else all forward (the reverse copy's
+// scalar registers cost a forward 8 %).
+template <typename IO, int NKB, int NP, bool OUT, bool BOTH>
+__global__ __launch_bounds__((WalkTiles<IO, NKB, NP, OUT>::threads), OUT ? 2 : 3)
+void linattn_walk_kernel(Walks walks) {
+  __shared__ __align__(16) char lds[WalkTiles<IO, NKB, NP, OUT>::bytes];
+  // Consecutive workgroups go round the 8 XCDs.  Items (segment, head) follow
+  // each other that way, so that unused slots and short segments fall on all
+  // of them alike; the slabs and walks of one item, which read the same rows,
+  // are 8 workgroups apart and so share an L2.
+  const int parts = (walks.w[0].N + NP - 1) / NP * walks.n;
+  const int full = gridDim.x / (8 * parts) * 8;  // items in whole groups of 8
+  const int id = blockIdx.x;
+  int part = (id >> 3) % parts, item = (id / (8 * parts)) * 8 + (id & 7);
+  if (id >= full * parts) {
+    part = (id - full * parts) % parts;
+    item = full + (id - full * parts) / parts;
+  }
+  const int slab = part / walks.n;
+  // (held in scalar registers: read again inside the loop, the arguments
+  // would make every wait for LDS wait for scalar memory too)
+  Walk a = walks.w[part - slab * walks.n];
+  asm volatile("" : "+s"(a.x), "+s"(a.y), "+s"(a.z), "+s"(a.out), "+s"(a.hx), "+s"(a.hy),
+               "+s"(a.hz), "+s"(a.H), "+s"(a.R), "+s"(a.N), "+s"(a.out_f32));
+  const int h = item % a.H, slot = item / a.H;
+  if constexpr (BOTH) {
+    if (a.rev) return walk_segment<IO, NKB, NP, OUT, true>(a, slab, h, slot, lds);
+  }
+  walk_segment<IO, NKB, NP, OUT, false>(a, slab, h, slot, lds);
+}
+
 // -------------------------------------------------------------- combine ---
 // The state in front of every segment, in place: buf[slot, h] holds each
-// segment's own contribution (all but the last in walk order) and becomes
-// the state entering it,  E' = a^len E + own.  A thread carries four state
-// elements through the sequence's segments; loads run ahead of the chain.
+// segment's own contribution (the last one's in walk order only with `fin`,
+// which takes the state behind it) and becomes the state entering it,
+// E' = a^len E + own.  A thread carries four state elements through the
+// sequence's segments; loads run ahead of the chain.
 // image: buf holds the states in register order (Walk::image, with CT column
 // tiles a block); init is a [dk, dv] matrix.
-template <bool REV>
+struct Combine {  // one of up to two directions of a launch
+  int rev;
+  const float* init;
+  float* buf;
+  float* fin;  // [sequences, H, dk, dv] or nullptr
+};
+struct Combines {
+  Combine c[2];
+  int n;
+};
+
 __global__ __launch_bounds__(256) void linattn_combine_kernel(Cut cut, int H, int R, int N,
                                                               int image, const float* log_decay,
-                                                              const float* init, float* buf) {
+                                                              Combines two) {
+  const Combine& dir = two.c[blockIdx.x % two.n];
+  const int id = blockIdx.x / two.n;
+  const bool rev = dir.rev != 0;
+  const float* init = dir.init;
+  float* buf = dir.buf;
+  float* fin = dir.fin;
   const int CT = N > 64 ? 2 : 1;
   const int elems = image ? (N + 16 * CT - 1) / (16 * CT) * 16 * CT * R : R * N;
   const int nblk = (elems / 4 + 255) / 256;
-  const int blk = blockIdx.x % nblk;
-  const int h = (blockIdx.x / nblk) % H;
-  const int seq = blockIdx.x / (nblk * H);
+  const int blk = id % nblk;
+  const int h = (id / nblk) % H;
+  const int seq = id / (nblk * H);
   int first, n, len;
   if (cut.cu == nullptr) {
     n = cut.per_seq;
@@ -809,7 +873,7 @@ __global__ __launch_bounds__(256) void linattn_combine_kernel(Cut cut, int H, in
   const int e4 = blk * 256 + threadIdx.x;
   if (e4 >= elems / 4) return;
   auto at = [&](int w) {  // w: index in walk order
-    const int j = REV ? n - 1 - w : w;
+    const int j = rev ? n - 1 - w : w;
     return reinterpret_cast<floatx4*>(
         buf + (static_cast<int64_t>(first + j) * H + h) * elems + 4 * e4);
   };
@@ -818,41 +882,46 @@ __global__ __launch_bounds__(256) void linattn_combine_kernel(Cut cut, int H, in
   auto load = [&](int w0) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-      if (w0 + u < n - 1) own[u] = *at(w0 + u);
+      if (w0 + u < n - (fin == nullptr)) own[u] = *at(w0 + u);
   };
   load(0);
 
+  // where the thread's four elements are in a [dk, dv] matrix: image: four
+  // rows of one column (past the last one: nowhere)
+  int place = 4 * e4, apart = 1;
+  if (image) {
+    const int lane = e4 & 63, tile = e4 >> 6, l16 = lane & 15;
+    const int ct = tile % CT, rt = tile / CT % (R / 16), cb = tile / (CT * (R / 16));
+    const int col = cb * 16 * CT + (CT == 2 ? 8 * (l16 >> 2) + (l16 & 3) + 4 * ct : l16);
+    place = col < N ? (rt * 16 + 4 * (lane >> 4)) * N + col : -1;
+    apart = N;
+  }
+  const int64_t state = (static_cast<int64_t>(seq) * H + h) * R * N;
   floatx4 E = {0.f, 0.f, 0.f, 0.f};
-  if (init != nullptr) {
-    init += (static_cast<int64_t>(seq) * H + h) * R * N;
-    if (image) {
-      const int lane = e4 & 63, tile = e4 >> 6, l16 = lane & 15;
-      const int ct = tile % CT, rt = tile / CT % (R / 16), cb = tile / (CT * (R / 16));
-      const int col = cb * 16 * CT + (CT == 2 ? 8 * (l16 >> 2) + (l16 & 3) + 4 * ct : l16);
-      if (col < N) {
+  if (init != nullptr && place >= 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) E[e] = init[(rt * 16 + 4 * (lane >> 4) + e) * N + col];
-      }
-    } else {
-      E = *reinterpret_cast<const floatx4*>(init + 4 * e4);
-    }
+    for (int e = 0; e < 4; ++e) E[e] = init[state + place + e * apart];
   }
   const double log_a = log_decay == nullptr ? 0.0 : static_cast<double>(ld_scalar(log_decay, h));
   const double ds = decay_pow(log_a, cut.span);
-  const double dt = REV ? decay_pow(log_a, len - (n - 1) * cut.span) : ds;  // the last segment's
+  const double dt = decay_pow(log_a, len - (n - 1) * cut.span);  // the short last segment's
   for (int w0 = 0; w0 < n; w0 += kAhead) {
     if (w0 > 0) load(w0);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (w0 + u >= n) break;
       *at(w0 + u) = E;
-      const double d = REV && w0 + u == 0 ? dt : ds;
-      if (w0 + u < n - 1) {
+      const double d = w0 + u == (rev ? 0 : n - 1) ? dt : ds;
+      if (w0 + u < n - (fin == nullptr)) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           E[e] = static_cast<float>(d * static_cast<double>(E[e]) + static_cast<double>(own[u][e]));
       }
     }
+  }
+  if (fin != nullptr && place >= 0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) fin[state + place + e * apart] = E[e];
   }
 }
 
@@ -994,89 +1063,98 @@ Cut make_cut(const LinAttn& p, const Plan& pl) {
   return Cut{p.varlen ? p.cu_seqlens : nullptr, p.nseq, p.T, pl.span, pl.per_seq};
 }
 
-template <typename IO, int NKB, int NP, bool OUT, bool REV>
-void launch_walk_t(const Walk& w, int64_t slots, hipStream_t s) {
-  const int64_t nslab = (w.N + NP - 1) / NP;
-  hipLaunchKernelGGL((linattn_walk_kernel<IO, NKB, NP, OUT, REV>),
-                     dim3(static_cast<unsigned>(slots * w.H * nslab)),
+template <typename IO, int NKB, int NP, bool OUT, bool BOTH>
+void launch_walk_t(const Walks& w, int64_t slots, hipStream_t s) {
+  const int64_t nslab = (w.w[0].N + NP - 1) / NP;
+  hipLaunchKernelGGL((linattn_walk_kernel<IO, NKB, NP, OUT, BOTH>),
+                     dim3(static_cast<unsigned>(slots * w.w[0].H * nslab * w.n)),
                      dim3(WalkTiles<IO, NKB, NP, OUT>::threads), 0, s, w);
 }
 
-template <typename IO, int NKB, bool OUT, bool REV>
-void launch_walk_n(const Walk& w, int64_t slots, hipStream_t s) {
-  if (w.N <= 32) return launch_walk_t<IO, NKB, 32, OUT, REV>(w, slots, s);
-  if (w.N <= 64) return launch_walk_t<IO, NKB, 64, OUT, REV>(w, slots, s);
-  launch_walk_t<IO, NKB, 128, OUT, REV>(w, slots, s);
+template <typename IO, int NKB, bool OUT, bool BOTH>
+void launch_walk_n(const Walks& w, int64_t slots, hipStream_t s) {
+  const int N = w.w[0].N;
+  if (N <= 32) return launch_walk_t<IO, NKB, 32, OUT, BOTH>(w, slots, s);
+  if (N <= 64) return launch_walk_t<IO, NKB, 64, OUT, BOTH>(w, slots, s);
+  launch_walk_t<IO, NKB, 128, OUT, BOTH>(w, slots, s);
 }
 
-template <typename IO, bool OUT, bool REV>
-void launch_walk_io(const Walk& w, int64_t slots, hipStream_t s) {
-  if (w.R > 128) {
-    if constexpr (OUT) return launch_walk_n<IO, 8, OUT, REV>(w, slots, s);
-  }
-  if (w.R > 64) return launch_walk_n<IO, 4, OUT, REV>(w, slots, s);
-  if (w.R > 32) return launch_walk_n<IO, 2, OUT, REV>(w, slots, s);
-  launch_walk_n<IO, 1, OUT, REV>(w, slots, s);
+template <typename IO, bool OUT, bool BOTH>
+void launch_walk_io(const Walks& w, int64_t slots, hipStream_t s) {
+  const int R = w.w[0].R;
+  if constexpr (OUT && BOTH)  // (a forward alone contracts over dk <= 128)
+    if (R > 128) return launch_walk_n<IO, 8, OUT, BOTH>(w, slots, s);
+  if (R > 64) return launch_walk_n<IO, 4, OUT, BOTH>(w, slots, s);
+  if (R > 32) return launch_walk_n<IO, 2, OUT, BOTH>(w, slots, s);
+  launch_walk_n<IO, 1, OUT, BOTH>(w, slots, s);
 }
 
-hipError_t launch_walk(const LinAttn& p, const Walk& w, int64_t slots, bool out, bool rev,
-                       int stage, hipStream_t s) {
+template <typename IO>
+void launch_walk_dir(const Walks& w, int64_t slots, bool out, hipStream_t s) {
+  const bool both = w.n > 1 || w.w[0].rev;
+  if (out)
+    both ? launch_walk_io<IO, true, true>(w, slots, s)
+         : launch_walk_io<IO, true, false>(w, slots, s);
+  else
+    both ? launch_walk_io<IO, false, true>(w, slots, s)
+         : launch_walk_io<IO, false, false>(w, slots, s);
+}
+
+// Walks of one shape (R, N, H) together.
+hipError_t launch_walks(const LinAttn& p, const Walks& w, int64_t slots, bool out, int stage,
+                        hipStream_t s) {
   StageScope scope(stage, s);
-  if (p.io == GDN_BF16) {
-    if (out)
-      rev ? launch_walk_io<bf16_t, true, true>(w, slots, s)
-          : launch_walk_io<bf16_t, true, false>(w, slots, s);
-    else
-      rev ? launch_walk_io<bf16_t, false, true>(w, slots, s)
-          : launch_walk_io<bf16_t, false, false>(w, slots, s);
-  } else {
-    if (out)
-      rev ? launch_walk_io<f32_t, true, true>(w, slots, s)
-          : launch_walk_io<f32_t, true, false>(w, slots, s);
-    else
-      rev ? launch_walk_io<f32_t, false, true>(w, slots, s)
-          : launch_walk_io<f32_t, false, false>(w, slots, s);
-  }
+  if (p.io == GDN_BF16)
+    launch_walk_dir<bf16_t>(w, slots, out, s);
+  else
+    launch_walk_dir<f32_t>(w, slots, out, s);
   return hipGetLastError();
 }
 
 // Elements of a state in register order: whole column blocks.
 int image_elems(const LinAttn& p) { return p.dk * (p.dv > 64 ? (p.dv + 31) / 32 * 32 : p.dv); }
 
-hipError_t launch_combine(const LinAttn& p, const Cut& cut, bool rev, bool image, const float* la,
-                          const float* init, float* buf, hipStream_t s) {
+// One direction of the states in front of every segment.
+struct Front {
+  bool rev;
+  const void *y, *z;
+  int hy, hz;
+  const float* init;
+  float *buf, *fin;
+};
+
+// States in front of every segment into the buffers, and behind the last ones
+// where wanted: own contributions, chained; one or two directions.
+hipError_t enter_states(const LinAttn& p, const Plan& pl, const Front* f, int n, bool image,
+                        const float* la, hipStream_t s) {
+  Walks w{};
+  Combines c{};
+  w.n = c.n = n;
+  for (int i = 0; i < n; ++i) {
+    Walk& a = w.w[i];
+    a.cut = make_cut(p, pl);
+    a.rev = f[i].rev ? 1 : 0;
+    a.y = f[i].y;
+    a.z = f[i].z;
+    a.hx = a.H = p.H;
+    a.hy = f[i].hy;
+    a.hz = f[i].hz;
+    a.R = p.dk;
+    a.N = p.dv;
+    a.log_decay = la;
+    a.behind = f[i].buf;
+    a.ends = f[i].fin != nullptr ? 1 : 0;
+    a.image = image ? 1 : 0;
+    c.c[i] = Combine{a.rev, f[i].init, f[i].buf, f[i].fin};
+  }
+  const hipError_t e = launch_walks(p, w, pl.slots, false, GDN_STAGE_FWD_TRANS, s);
+  if (e != hipSuccess) return e;
   StageScope scope(GDN_STAGE_FWD_COMBINE, s);
   const int elems = image ? image_elems(p) : p.dk * p.dv;
-  const int64_t grid = static_cast<int64_t>(p.nseq) * p.H * ((elems / 4 + 255) / 256);
-  if (rev)
-    hipLaunchKernelGGL(linattn_combine_kernel<true>, dim3(static_cast<unsigned>(grid)), dim3(256),
-                       0, s, cut, p.H, p.dk, p.dv, image ? 1 : 0, la, init, buf);
-  else
-    hipLaunchKernelGGL(linattn_combine_kernel<false>, dim3(static_cast<unsigned>(grid)),
-                       dim3(256), 0, s, cut, p.H, p.dk, p.dv, image ? 1 : 0, la, init, buf);
+  const int64_t grid = static_cast<int64_t>(p.nseq) * p.H * ((elems / 4 + 255) / 256) * n;
+  hipLaunchKernelGGL(linattn_combine_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s,
+                     w.w[0].cut, p.H, p.dk, p.dv, image ? 1 : 0, la, c);
   return hipGetLastError();
-}
-
-// States in front of every segment into `buf`: own contributions, chained.
-hipError_t enter_states(const LinAttn& p, const Plan& pl, bool rev, bool image, const void* y, const void* z,
-                        int hy, int hz, const float* la, const float* init, float* buf,
-                        hipStream_t s) {
-  Walk w{};
-  w.cut = make_cut(p, pl);
-  w.y = y;
-  w.z = z;
-  w.hx = p.H;
-  w.hy = hy;
-  w.hz = hz;
-  w.H = p.H;
-  w.R = p.dk;
-  w.N = p.dv;
-  w.log_decay = la;
-  w.behind = buf;
-  w.image = image ? 1 : 0;
-  hipError_t e = launch_walk(p, w, pl.slots, false, rev, GDN_STAGE_FWD_TRANS, s);
-  if (e != hipSuccess) return e;
-  return launch_combine(p, w.cut, rev, image, la, init, buf, s);
 }
 
 size_t state_bytes(const LinAttn& p, const Plan& pl) {
@@ -1105,7 +1183,7 @@ bool linattn_grid_ok(const LinAttn& p) {
   const Plan pl = plan_walk(p);
   const int64_t most = (int64_t(1) << 31) - 1;
   const int64_t blocks = (static_cast<int64_t>(image_elems(p)) / 4 + 255) / 256;
-  return pl.slots * p.H * 2 <= most && static_cast<int64_t>(p.nseq) * p.H * blocks <= most;
+  return pl.slots * p.H * 6 <= most && 2 * static_cast<int64_t>(p.nseq) * p.H * blocks <= most;
 }
 
 size_t linattn_fwd_workspace_bytes(const LinAttn& p) { return state_bytes(p, plan_walk(p)); }
@@ -1114,12 +1192,15 @@ hipError_t launch_linattn_fwd(const LinAttn& p, const void* q, const void* k, co
                               const float* la, const float* s0, void* o, float* s_final,
                               void* ws, hipStream_t s) {
   const Plan pl = plan_walk(p);
-  Walk w{};
+  Walks one{};
+  one.n = 1;
+  Walk& w = one.w[0];
   w.cut = make_cut(p, pl);
   w.enter = s0;
   if (pl.split) {
     float* buf = static_cast<float*>(ws);
-    const hipError_t e = enter_states(p, pl, false, true, k, v, p.hq, p.H, la, s0, buf, s);
+    const Front f{false, k, v, p.hq, p.H, s0, buf, s_final};
+    const hipError_t e = enter_states(p, pl, &f, 1, true, la, s);
     if (e != hipSuccess) return e;
     w.enter = buf;
     w.image = 1;
@@ -1133,8 +1214,8 @@ hipError_t launch_linattn_fwd(const LinAttn& p, const void* q, const void* k, co
   w.N = p.dv;
   w.log_decay = la;
   w.out = o;
-  w.behind = s_final;
-  return launch_walk(p, w, pl.slots, true, false, GDN_STAGE_FWD_SCAN, s);
+  w.behind = pl.split ? nullptr : s_final;
+  return launch_walks(p, one, pl.slots, true, GDN_STAGE_FWD_SCAN, s);
 }
 
 size_t linattn_bwd_workspace_bytes(const LinAttn& p) {
@@ -1154,9 +1235,9 @@ hipError_t launch_linattn_bwd(const LinAttn& p, const void* q, const void* k, co
     at += state_bytes(p, pl);
     float* bb = reinterpret_cast<float*>(at);
     at += state_bytes(p, pl);
-    e = enter_states(p, pl, false, false, k, v, p.hq, p.H, la, s0, bf, s);
-    if (e != hipSuccess) return e;
-    e = enter_states(p, pl, true, false, q, d_o, p.hq, p.H, la, ds_final, bb, s);
+    const Front f[2] = {{false, k, v, p.hq, p.H, s0, bf, nullptr},
+                        {true, q, d_o, p.hq, p.H, ds_final, bb, ds0}};
+    e = enter_states(p, pl, f, 2, false, la, s);
     if (e != hipSuccess) return e;
     front = bf;
     back = bb;
@@ -1175,36 +1256,43 @@ hipError_t launch_linattn_bwd(const LinAttn& p, const void* q, const void* k, co
   w.N = p.dk;
   w.hx = w.hy = p.H;
   w.hz = p.hq;
-  // dq
-  w.x = d_o;
-  w.y = v;
-  w.z = k;
-  w.enter = front;
-  w.out = shared ? static_cast<void*>(part_q) : dq;
-  e = launch_walk(p, w, pl.slots, true, false, GDN_STAGE_BWD_GRAD, s);
-  if (e != hipSuccess) return e;
-  // dk
-  w.x = v;
-  w.y = d_o;
-  w.z = q;
+  Walks all{};
+  Walk& dq_ = all.w[0] = w;
+  dq_.x = d_o;
+  dq_.y = v;
+  dq_.z = k;
+  dq_.enter = front;
+  dq_.out = shared ? static_cast<void*>(part_q) : dq;
+  w.rev = 1;
   w.enter = back;
-  w.out = shared ? static_cast<void*>(part_k) : dk;
-  e = launch_walk(p, w, pl.slots, true, true, GDN_STAGE_BWD_GRAD, s);
+  Walk& dk_ = all.w[1] = w;
+  dk_.x = v;
+  dk_.y = d_o;
+  dk_.z = q;
+  dk_.out = shared ? static_cast<void*>(part_k) : dk;
+  Walk& dv_ = all.w[2] = w;
+  dv_.turned = 0;
+  dv_.out_f32 = 0;
+  dv_.R = p.dk;
+  dv_.N = p.dv;
+  dv_.hx = dv_.hy = p.hq;
+  dv_.hz = p.H;
+  dv_.x = k;
+  dv_.y = q;
+  dv_.z = d_o;
+  dv_.out = dv;
+  dv_.behind = pl.split ? nullptr : ds0;
+  // dv's walk has the other two's shape when dk = dv
+  all.n = p.dk == p.dv ? 3 : 2;
+  e = launch_walks(p, all, pl.slots, true, GDN_STAGE_BWD_GRAD, s);
   if (e != hipSuccess) return e;
-  // dv
-  w.turned = 0;
-  w.out_f32 = 0;
-  w.R = p.dk;
-  w.N = p.dv;
-  w.hx = w.hy = p.hq;
-  w.hz = p.H;
-  w.x = k;
-  w.y = q;
-  w.z = d_o;
-  w.out = dv;
-  w.behind = ds0;
-  e = launch_walk(p, w, pl.slots, true, true, GDN_STAGE_BWD_GRAD, s);
-  if (e != hipSuccess) return e;
+  if (all.n == 2) {
+    Walks one{};
+    one.n = 1;
+    one.w[0] = dv_;
+    e = launch_walks(p, one, pl.slots, true, GDN_STAGE_BWD_GRAD, s);
+    if (e != hipSuccess) return e;
+  }
   if (!shared) return hipSuccess;
   const int64_t tok = static_cast<int64_t>(p.B) * p.T;
   const int64_t pieces = tok * p.hq * (p.dk / 4);
