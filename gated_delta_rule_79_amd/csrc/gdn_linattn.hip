@@ -50,6 +50,7 @@ struct Cut {
   int nseq, T;
   int span;           // tokens per segment
   int per_seq;        // dense: segments per sequence (>= 1)
+  int64_t slots;      // segment slots there is room for
 };
 
 struct Segment {
@@ -869,6 +870,8 @@ __global__ __launch_bounds__(256) void linattn_combine_kernel(Cut cut, int H, in
     int st, en;
     seq_range(cut, seq, &st, &en);
     len = en - st;
+    // (bounds that overlap need more slots than there are: none beyond them)
+    n = static_cast<int>(min(static_cast<int64_t>(n), max(cut.slots - first, int64_t(0))));
   }
   const int e4 = blk * 256 + threadIdx.x;
   if (e4 >= elems / 4) return;
@@ -926,13 +929,15 @@ __global__ __launch_bounds__(256) void linattn_combine_kernel(Cut cut, int H, in
 }
 
 // ---------------------------------------------------------- shared heads ---
-// Gradient of a q or k head: the sum over the v heads that read it, in head
-// order, from the fp32 rows of each (part: [tokens, H, d] -> out
-// [tokens, Hq, d]).  Tokens behind the last sequence are left alone.
+// Gradients of q and k heads: the sum over the v heads that read it, in head
+// order, from the fp32 rows of each (part and part + apart: [tokens, H, d] ->
+// out0 and out1: [tokens, Hq, d]).  Tokens behind the last sequence are left alone.
 template <typename IO>
-__global__ __launch_bounds__(256) void linattn_share_kernel(const float* part, void* out,
-                                                            int64_t tokens, int Hq, int grp,
+__global__ __launch_bounds__(256) void linattn_share_kernel(const float* part, int64_t apart,
+                                                            void* out0, void* out1, int64_t tokens, int Hq, int grp,
                                                             int d, const int32_t* cu, int nseq) {
+  void* const out = blockIdx.y == 0 ? out0 : out1;
+  part += blockIdx.y * apart;
   if (cu != nullptr) tokens = min(tokens, static_cast<int64_t>(max(cu[nseq], 0)));
   const int p4 = d / 4;
   const int64_t total = tokens * Hq * p4;
@@ -1060,7 +1065,7 @@ Plan plan_walk(const LinAttn& p) {
 }
 
 Cut make_cut(const LinAttn& p, const Plan& pl) {
-  return Cut{p.varlen ? p.cu_seqlens : nullptr, p.nseq, p.T, pl.span, pl.per_seq};
+  return Cut{p.varlen ? p.cu_seqlens : nullptr, p.nseq, p.T, pl.span, pl.per_seq, pl.slots};
 }
 
 template <typename IO, int NKB, int NP, bool OUT, bool BOTH>
@@ -1077,6 +1082,12 @@ void launch_walk_n(const Walks& w, int64_t slots, hipStream_t s) {
   if (N <= 32) return launch_walk_t<IO, NKB, 32, OUT, BOTH>(w, slots, s);
   if (N <= 64) return launch_walk_t<IO, NKB, 64, OUT, BOTH>(w, slots, s);
   launch_walk_t<IO, NKB, 128, OUT, BOTH>(w, slots, s);
+}
+
+// Tiles and slabs of a walk, as launch_walk_io picks them.
+int tiles_of(int R, int N) {
+  return (R > 128 ? 8 : R > 64 ? 4 : R > 32 ? 2 : 1) * 1024 +
+         (N <= 32 ? 0 : N <= 64 ? 1 : 1 + (N + 127) / 128);
 }
 
 template <typename IO, bool OUT, bool BOTH>
@@ -1100,7 +1111,7 @@ void launch_walk_dir(const Walks& w, int64_t slots, bool out, hipStream_t s) {
          : launch_walk_io<IO, false, false>(w, slots, s);
 }
 
-// Walks of one shape (R, N, H) together.
+// Walks of the same tiles together.
 hipError_t launch_walks(const LinAttn& p, const Walks& w, int64_t slots, bool out, int stage,
                         hipStream_t s) {
   StageScope scope(stage, s);
@@ -1282,8 +1293,8 @@ hipError_t launch_linattn_bwd(const LinAttn& p, const void* q, const void* k, co
   dv_.z = d_o;
   dv_.out = dv;
   dv_.behind = pl.split ? nullptr : ds0;
-  // dv's walk has the other two's shape when dk = dv
-  all.n = p.dk == p.dv ? 3 : 2;
+  // dv's walk joins the other two where its tiles are theirs
+  all.n = tiles_of(p.dv, p.dk) == tiles_of(p.dk, p.dv) ? 3 : 2;
   e = launch_walks(p, all, pl.slots, true, GDN_STAGE_BWD_GRAD, s);
   if (e != hipSuccess) return e;
   if (all.n == 2) {
@@ -1298,18 +1309,14 @@ hipError_t launch_linattn_bwd(const LinAttn& p, const void* q, const void* k, co
   const int64_t pieces = tok * p.hq * (p.dk / 4);
   if (pieces == 0) return hipSuccess;
   StageScope scope(GDN_STAGE_OTHER, s);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((pieces + 255) / 256, 4096)));
-  for (int u = 0; u < 2; ++u) {
-    const float* part = u == 0 ? part_q : part_k;
-    void* out = u == 0 ? dq : dk;
-    const int32_t* cu = p.varlen ? p.cu_seqlens : nullptr;
-    if (p.io == GDN_BF16)
-      hipLaunchKernelGGL(linattn_share_kernel<bf16_t>, grid, dim3(256), 0, s, part, out, tok,
-                         p.hq, p.H / p.hq, p.dk, cu, p.nseq);
-    else
-      hipLaunchKernelGGL(linattn_share_kernel<f32_t>, grid, dim3(256), 0, s, part, out, tok, p.hq,
-                         p.H / p.hq, p.dk, cu, p.nseq);
-  }
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((pieces + 255) / 256, 4096)), 2);
+  const int32_t* cu = p.varlen ? p.cu_seqlens : nullptr;
+  if (p.io == GDN_BF16)
+    hipLaunchKernelGGL(linattn_share_kernel<bf16_t>, grid, dim3(256), 0, s, part_q,
+                       part_k - part_q, dq, dk, tok, p.hq, p.H / p.hq, p.dk, cu, p.nseq);
+  else
+    hipLaunchKernelGGL(linattn_share_kernel<f32_t>, grid, dim3(256), 0, s, part_q,
+                       part_k - part_q, dq, dk, tok, p.hq, p.H / p.hq, p.dk, cu, p.nseq);
   return hipGetLastError();
 }
 

@@ -353,6 +353,62 @@ def test_captured_and_replayed(gpu_lib, seg):
         assert all(torch.equal(a, b) for a, b in zip(held, want)), k
 
 
+def test_offsets_past_four_gigabytes(gpu_lib):
+    # the last sequence's rows lie behind 2^32 bytes of every tensor
+    T, H, d = 600_000, 32, 128
+    cu = [0, T - 130, T]
+    x = {n: torch.zeros(1, T, H, d, dtype=BF16, device="cuda") for n in ("q", "k", "v", "do")}
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for t in x.values():
+        t[:, cu[1]:] = torch.randn(130, H, d, generator=g, device="cuda").to(BF16)
+    la = torch.log1p(-torch.exp2(-torch.linspace(1, 9, H))).cuda()
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    tail = {n: t[:, cu[1]:].contiguous() for n, t in x.items()}
+    host = dict({n: t.cpu() for n, t in tail.items()}, log_decay=la.cpu(), s0=None)
+    for seg in (-1, 4096):
+        o, sf = gdn.linear_attn_fwd(x["q"], x["k"], x["v"], la, cu_seqlens=cud, seg_chunks=seg)
+        o1, s1 = gdn.linear_attn_fwd(tail["q"], tail["k"], tail["v"], la, seg_chunks=-1)
+        torch.cuda.synchronize()
+        # Not cut, both walks are the same arithmetic.  Cut, the state that
+        # multiplies q holds two operand parts of each product where the
+        # other holds four: 2^-18 apart, its rounding to bf16 may fall on
+        # either side, so only the bounds above hold.
+        if seg == -1:
+            assert torch.equal(o[:, cu[1]:], o1) and torch.equal(sf[1], s1[0])
+        check_fwd(host, None, BF16, o[:, cu[1]:], sf[1:])
+        assert not sf[0].any()
+    del o
+    got = gdn.linear_attn_bwd(x["q"], x["k"], x["v"], la, None, x["do"], cu_seqlens=cud,
+                              need_ds0=False, seg_chunks=-1)
+    one = gdn.linear_attn_bwd(tail["q"], tail["k"], tail["v"], la, None, tail["do"],
+                              need_ds0=False, seg_chunks=-1)
+    torch.cuda.synchronize()
+    for a, b in zip(got[:3], one[:3]):
+        assert torch.equal(a[:, cu[1]:], b)
+
+
+def test_overlapping_bounds_stay_in_range(gpu_lib):
+    # malformed bounds are the caller's fault, but reach no memory outside
+    d, _ = make(1, 300, 2, 2, 32, 32, BF16, cu=[0, 1, 2, 3, 4], do=True)
+    x = gpu(d)
+    cud = torch.tensor([0, 300, 0, 300, 0], dtype=torch.int32, device="cuda")
+    need = gdn._bytes
+    pads = {n: Padded(t.shape, t.dtype) for n, t in
+            (("o", d["v"]), ("sf", d["s0"]), ("dq", d["q"]), ("dk", d["k"]), ("dv", d["v"]),
+             ("ds0", d["s0"]))}
+    p, hq, _ = gdn._linattn_problem(x["q"], x["k"], x["v"], x["log_decay"], cud, 1, 2)
+    ws = Padded((need(gpu_lib.gdn_linear_attn_bwd_workspace, p, hq),), torch.uint8)
+    gdn.linear_attn_fwd(x["q"], x["k"], x["v"], x["log_decay"], x["s0"], cu_seqlens=cud,
+                        o=pads["o"].t, s_final=pads["sf"].t, seg_chunks=1, workspace=ws.t)
+    gdn.linear_attn_bwd(x["q"], x["k"], x["v"], x["log_decay"], x["s0"], x["do"], x["ds"],
+                        cu_seqlens=cud, seg_chunks=1, workspace=ws.t,
+                        out=tuple(pads[n].t for n in ("dq", "dk", "dv", "ds0")))
+    torch.cuda.synchronize()
+    ws.check("workspace")
+    for n, q in pads.items():
+        q.check(n)
+
+
 def test_two_streams_at_once(gpu_lib):
     jobs = [make(1, 500, 4, 4, 64, 64, BF16, seed=s, do=True)[0] for s in (1, 2)]
     want = [[*run_fwd(d, None), *run_bwd(d, None)] for d in jobs]
