@@ -245,6 +245,20 @@ template <> struct Parts<bf16_t> {
   }
 };
 
+// What a rounding of two stacked tiles left behind, rounded in turn.
+__device__ inline bf16x8 pack2_rest(const floatx4& lo, const floatx4& hi, const bf16x8& r) {
+  const u32x4 u = __builtin_bit_cast(u32x4, r);
+  floatx4 a, b;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    a[2 * e] = lo[2 * e] - __uint_as_float(u[e] << 16);
+    a[2 * e + 1] = lo[2 * e + 1] - __uint_as_float(u[e] & 0xffff0000u);
+    b[2 * e] = hi[2 * e] - __uint_as_float(u[2 + e] << 16);
+    b[2 * e + 1] = hi[2 * e + 1] - __uint_as_float(u[2 + e] & 0xffff0000u);
+  }
+  return pack2<bf16_t>(a, b);
+}
+
 // ----------------------------------------------------------------- walk ---
 
 struct Walk {
@@ -290,9 +304,10 @@ struct WalkTiles {
   // (x) or by transposing reads (y, z: 32 bytes of a row) over the banks
   static constexpr int sx = RP + 16 / ob, sy = RP + (ob == 2 ? 16 : 4),
                        sz = NP + (ob == 2 ? 16 : 4);
-  static constexpr int off_y = OUT ? C * sx * ob : 0, off_z = off_y + C * sy * ob,
-                       off_p = off_z + C * sz * ob, off_d = off_p + (OUT ? C * C * ob : 0),
-                       off_w = off_d + (32 + C + 4) * 4, bytes = off_w + C * 4;
+  // (the small tables lie in front: a read's immediate reaches 64 KB)
+  static constexpr int off_d = 0, off_w = off_d + (32 + C + 4) * 4, off_x = off_w + C * 4,
+                       off_y = off_x + (OUT ? C * sx * ob : 0), off_z = off_y + C * sy * ob,
+                       off_p = off_z + C * sz * ob, bytes = off_p + (OUT ? C * C * 4 : 0);
   // y rows shift by 8 bytes every four rows (in the row's padding): 16 rows
   // read 8 bytes at a time then meet all banks, as the transposing reads do
   static constexpr int skew = ob == 2 ? 4 : 0;
@@ -305,7 +320,7 @@ struct WalkTiles {
 // One segment of one head and column slab.  The state sits in accumulator
 // registers.  Per chunk: rows of x, y, z arrive in LDS from registers that
 // were loaded during the previous chunk; x y^T on the matrix cores, decayed
-// and rounded once into operand fragments in LDS; out^T = M^T x^T (from the
+// and split into operand fragments in LDS; out^T = M^T x^T (from the
 // state's registers, re-packed as an operand), scaled in fp32, plus
 // z^T (x y^T)^T, stored at once; the state update last, while the stores
 // drain.
@@ -325,7 +340,7 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
   using L = WalkTiles<IO, NKB, NP, OUT>;
   constexpr int C = L::C, NI = L::NI, NKC = L::NKC, CT = L::CT, ob = L::ob, off = rev ? 0 : 1;
   constexpr int kThreads = L::threads;
-  char* const tx = lds;
+  char* const tx = lds + L::off_x;
   char* const ty = lds + L::off_y;
   char* const tz = lds + L::off_z;
   char* const tp = lds + L::off_p;
@@ -564,8 +579,14 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
       p0[e] *= d[-e];
       p1[e] *= d[-16 - e];
     }
-    *reinterpret_cast<opvec<IO>*>(tp + ((it * NKC + jp) * 64 + lane) * 8 * ob) =
-        pack2<IO>(p0, p1);
+    // In two parts: the first alone would add an output's half step again,
+    // which short sequences, all x y^T, show as 1.6 times the error of one
+    // rounding; the second costs 1 % (65k tokens) to 4 % (B8 T2048 backward).
+    const opvec<IO> r = pack2<IO>(p0, p1);
+    char* const at = tp + ((it * NKC + jp) * 64 + lane) * 8 * ob;
+    *reinterpret_cast<opvec<IO>*>(at) = r;
+    if constexpr (ob == 2)
+      *reinterpret_cast<opvec<IO>*>(at + C * C * ob) = pack2_rest(p0, p1, r);
   };
 
   // M <- a^n M + sum_j y_j (w_j z_j)^T, the weighted rows in NPART operand
@@ -692,7 +713,9 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
 
     if (active) {
       if constexpr (OUT) {
-        // M^T x^T, the state rounded once to the operand type
+        // M^T x^T, the state rounded once to the operand type (a second part of
+        // it would cost another 2 % to 5 % and take the outputs' error from
+        // 1.4 roundings of their own to 1)
         opvec<IO> xf[2][L::IPS];
         auto read_x = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
@@ -744,6 +767,12 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
             const opvec<IO> pf = lds_run8<IO>(p_run + (u * L::SETS * NKC + kb) * 512 * ob);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) acc[u][ct] = mma32(zf[kb][ct], pf, acc[u][ct]);
+            if constexpr (ob == 2) {
+              const opvec<IO> pr =
+                  lds_run8<IO>(p_run + (u * L::SETS * NKC + kb) * 512 * ob + C * C * ob);
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct) acc[u][ct] = mma32(zf[kb][ct], pr, acc[u][ct]);
+            }
           }
         }
         store_out();
@@ -779,7 +808,7 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
                                         again * 4) = S[rt][ct];
           continue;
         }
-        const int r = r0 + rt * 16 + 4 * (again >> 4), 
+        const int r = r0 + rt * 16 + 4 * (again >> 4),
                   n = n0 + col + (CT == 2 ? 8 * ((again & 15) >> 2) + (again & 3) + 4 * ct : again & 15);
         if (r >= a.R || n >= a.N) continue;
 #pragma unroll
