@@ -1053,11 +1053,21 @@ struct Plan {
   bool split;
 };
 
-Plan plan_walk(const LinAttn& p) {
+// Tiles and slabs of a walk, as launch_walk_io picks them.
+int tiles_of(int R, int N) {
+  return (R > 128 ? 8 : R > 64 ? 4 : R > 32 ? 2 : 1) * 1024 +
+         (N <= 32 ? 0 : N <= 64 ? 1 : 1 + (N + 127) / 128);
+}
+
+// dv's walk joins dq's and dk's where its tiles are theirs
+bool walks_join(const LinAttn& p) { return tiles_of(p.dv, p.dk) == tiles_of(p.dk, p.dv); }
+
+Plan plan_walk(const LinAttn& p, bool bwd) {
   const int C = p.io == GDN_BF16 ? 64 : 32;
   Plan r;
   const int64_t nch = (static_cast<int64_t>(p.T) + C - 1) / C;  // of one dense sequence, or all
-  const int64_t chains = static_cast<int64_t>(p.nseq) * p.H * ((p.dv + 127) / 128);
+  const int64_t slabs = (p.dv + 127) / 128, heads = static_cast<int64_t>(p.nseq) * p.H;
+  const int64_t chains = heads * slabs;
   const int64_t units = p.varlen ? nch * (chains / p.nseq) : nch * chains;  // chunks to walk
   int64_t L = nch;  // chunks per segment
   if (p.seg_req > 0) {
@@ -1073,13 +1083,25 @@ Plan plan_walk(const LinAttn& p) {
       const int64_t room = all - chains / 2;
       L = (units + room - 1) / room;
     } else {
-      // One workgroup a CU while walks are short, since every further segment
-      // costs four passes over its state (T4096 H16: 4 chunks 51 us, 2: 60;
-      // T16384 H8: 8 chunks 79, 4: 91); two where they are long.
-      const int64_t target = units < 48 * 256 ? 256 : 512;
-      const int64_t per_seq = std::max<int64_t>(1, target / chains);
-      L = (nch + per_seq - 1) / per_seq;
+      // Workgroups of an output launch that is not cut.  Where they take most
+      // CUs, two more passes over the tokens cost more than the idle ones
+      // (dk 128 dv 128 backward, 240 of them: T1024 70 us, cut 95; T8192 525,
+      // 570; 192 of them: T1024 69, 83; T4096 262, 233).
+      const int64_t whole = !bwd ? chains : walks_join(p) ? 3 * chains
+                                                          : std::min(2 * heads, chains);
+      if (whole < (nch <= 32 ? 192 : 200)) {
+        // One workgroup a CU while walks are short, since every further segment
+        // costs four passes over its state (T4096 H16: 4 chunks 47 us, 2: 55);
+        // two where they are long.
+        const int64_t target = units < 48 * 256 ? 256 : 512;
+        const int64_t per_seq = std::max<int64_t>(1, target / chains);
+        L = (nch + per_seq - 1) / per_seq;
+      }
     }
+    // The states are chained a segment after another: at least
+    // sqrt(chunks / 8) chunks each (T16384 H2: 2 chunks 73 us, 6: 57;
+    // T65536 H1: 4: 126, 12: 102).
+    while (8 * L * L < (p.varlen ? nch / p.nseq : nch)) ++L;
     L = std::min(L, nch);
   }
   L = std::max<int64_t>(L, 1);
@@ -1111,12 +1133,6 @@ void launch_walk_n(const Walks& w, int64_t slots, hipStream_t s) {
   if (N <= 32) return launch_walk_t<IO, NKB, 32, OUT, BOTH>(w, slots, s);
   if (N <= 64) return launch_walk_t<IO, NKB, 64, OUT, BOTH>(w, slots, s);
   launch_walk_t<IO, NKB, 128, OUT, BOTH>(w, slots, s);
-}
-
-// Tiles and slabs of a walk, as launch_walk_io picks them.
-int tiles_of(int R, int N) {
-  return (R > 128 ? 8 : R > 64 ? 4 : R > 32 ? 2 : 1) * 1024 +
-         (N <= 32 ? 0 : N <= 64 ? 1 : 1 + (N + 127) / 128);
 }
 
 template <typename IO, bool OUT, bool BOTH>
@@ -1220,18 +1236,18 @@ void launch_decode_dk(const LinAttn& p, const void* q, const void* k, const void
 }  // namespace
 
 bool linattn_grid_ok(const LinAttn& p) {
-  const Plan pl = plan_walk(p);
+  const Plan pl = plan_walk(p, false), plb = plan_walk(p, true);
   const int64_t most = (int64_t(1) << 31) - 1;
   const int64_t blocks = (static_cast<int64_t>(image_elems(p)) / 4 + 255) / 256;
-  return pl.slots * p.H * 6 <= most && 2 * static_cast<int64_t>(p.nseq) * p.H * blocks <= most;
+  return std::max(pl.slots, plb.slots) * p.H * 6 <= most && 2 * static_cast<int64_t>(p.nseq) * p.H * blocks <= most;
 }
 
-size_t linattn_fwd_workspace_bytes(const LinAttn& p) { return state_bytes(p, plan_walk(p)); }
+size_t linattn_fwd_workspace_bytes(const LinAttn& p) { return state_bytes(p, plan_walk(p, false)); }
 
 hipError_t launch_linattn_fwd(const LinAttn& p, const void* q, const void* k, const void* v,
                               const float* la, const float* s0, void* o, float* s_final,
                               void* ws, hipStream_t s) {
-  const Plan pl = plan_walk(p);
+  const Plan pl = plan_walk(p, false);
   Walks one{};
   one.n = 1;
   Walk& w = one.w[0];
@@ -1259,14 +1275,14 @@ hipError_t launch_linattn_fwd(const LinAttn& p, const void* q, const void* k, co
 }
 
 size_t linattn_bwd_workspace_bytes(const LinAttn& p) {
-  return 2 * state_bytes(p, plan_walk(p)) + 2 * part_bytes(p);
+  return 2 * state_bytes(p, plan_walk(p, true)) + 2 * part_bytes(p);
 }
 
 hipError_t launch_linattn_bwd(const LinAttn& p, const void* q, const void* k, const void* v,
                               const float* la, const float* s0, const void* d_o,
                               const float* ds_final, void* dq, void* dk, void* dv, float* ds0,
                               void* ws, hipStream_t s) {
-  const Plan pl = plan_walk(p);
+  const Plan pl = plan_walk(p, true);
   const float *front = s0, *back = ds_final;
   char* at = static_cast<char*>(ws);
   hipError_t e;
@@ -1322,8 +1338,7 @@ hipError_t launch_linattn_bwd(const LinAttn& p, const void* q, const void* k, co
   dv_.z = d_o;
   dv_.out = dv;
   dv_.behind = pl.split ? nullptr : ds0;
-  // dv's walk joins the other two where its tiles are theirs
-  all.n = tiles_of(p.dv, p.dk) == tiles_of(p.dk, p.dv) ? 3 : 2;
+  all.n = walks_join(p) ? 3 : 2;
   e = launch_walks(p, all, pl.slots, true, GDN_STAGE_BWD_GRAD, s);
   if (e != hipSuccess) return e;
   if (all.n == 2) {
