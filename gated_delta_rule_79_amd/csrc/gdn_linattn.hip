@@ -643,8 +643,15 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
 #pragma unroll
         for (int v = 0; v < GR; ++v)
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-            S[rt + v][ct] = mma32(yf[step & 1][v], wz[ct].p[u], S[rt + v][ct]);
+          for (int ct = 0; ct < CT; ++ct) {
+            if constexpr (ob == 2)
+              S[rt + v][ct] = mma32(yf[step & 1][v], wz[ct].p[u], S[rt + v][ct]);
+            else  // (a step adds four rows only: summed apart, the chunk rounds
+                  // the state once, a third of the error after thousands of
+                  // tokens for 0 to 2 % of the time)
+              S[rt + v][ct] +=
+                  mma32(yf[step & 1][v], wz[ct].p[u], floatx4{0.f, 0.f, 0.f, 0.f});
+          }
       // the next rows' decay, between the products
       if (pass == 0 && kb == 0 && step + 1 < PER) {
 #pragma unroll
