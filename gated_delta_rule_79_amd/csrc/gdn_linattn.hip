@@ -992,9 +992,12 @@ __global__ __launch_bounds__(256) void linattn_share_kernel(const float* part, i
 
 // --------------------------------------------------------------- decode ---
 // M <- a M + k v^T, o = M^T q: every state element read once and written
-// once in 16-byte pieces; a workgroup takes one (sequence, head) and 64
-// columns, a thread DK / 16 rows of 4 columns.  No step waits for another
-// before the store, so only the reading and writing of the state bounds it.
+// once in 16-byte pieces, so that memory bounds it (3 flops per 8 bytes); a
+// workgroup takes one (sequence, head) and 64 columns, a thread DK / 16 rows
+// of 4 columns.  Four loads of a thread are in flight (N256 H32 of 128 x 128,
+// 1.08 GB: 189 us, 5.7 TB/s; all eight 193, with the stores between them
+// 197, one 185 but 47.3 against 46.7 at N64), and the stores wait for the
+// workgroup's loads, since memory turns round less often.
 template <int DK, typename IO>
 __global__ __launch_bounds__(256) void linattn_decode_kernel(
     int H, int grp, int dv, const void* __restrict__ q, const void* __restrict__ k,
@@ -1006,33 +1009,37 @@ __global__ __launch_bounds__(256) void linattn_decode_kernel(
   const int slab = blockIdx.x - nh * nslab;
   const int n = nh / H, h = nh - n * H;
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
-  const int col = slab * 64 + cg * 4;
-  const bool active = col < dv;
+  const bool active = slab * 64 + cg * 4 < dv;
+  const int col = active ? slab * 64 + cg * 4 : 0;  // (idle lanes read what others do)
   float* M = state + static_cast<int64_t>(nh) * DK * dv + col;
-  floatx4 m[RPT];
-#pragma unroll
-  for (int j = 0; j < RPT; ++j)
-    m[j] = active ? __builtin_nontemporal_load(
-                        reinterpret_cast<const floatx4*>(M + (rg + 16 * j) * dv))
-                  : floatx4{0.f, 0.f, 0.f, 0.f};
-  const int64_t qo = (static_cast<int64_t>(n) * (H / grp) + h / grp) * DK;
+  const int64_t qo = (static_cast<int64_t>(n) * (H / grp) + h / grp) * DK + rg;
   const int64_t vo = static_cast<int64_t>(nh) * dv + col;
-  const float a =
-      log_decay == nullptr ? 1.0f : static_cast<float>(exp(static_cast<double>(log_decay[h])));
-  floatx4 vv = {0.f, 0.f, 0.f, 0.f}, w = vv;
-  if (active) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) vv[c] = io<IO>::load(v, vo + c);
-  }
+  float kr[RPT], qr[RPT];
 #pragma unroll
   for (int j = 0; j < RPT; ++j) {
-    const int r = rg + 16 * j;
-    const float kr = io<IO>::load(k, qo + r), qr = io<IO>::load(q, qo + r);
+    kr[j] = io<IO>::load(k, qo + 16 * j);
+    qr[j] = io<IO>::load(q, qo + 16 * j);
+  }
+  floatx4 vv;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) m[j][c] = __builtin_fmaf(a, m[j][c], kr * vv[c]);
-    w += m[j] * qr;
-    if (active)
-      __builtin_nontemporal_store(m[j], reinterpret_cast<floatx4*>(M + r * dv));
+  for (int c = 0; c < 4; ++c) vv[c] = io<IO>::load(v, vo + c);
+  floatx4 m[RPT];
+#pragma unroll
+  for (int j = 0; j < RPT; ++j) {
+    m[j] = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(M + (rg + 16 * j) * dv));
+    if (j % 4 == 3 && j + 1 < RPT) {
+      __builtin_amdgcn_s_waitcnt(0x0f70);  // loads: none left
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  const float a =
+      log_decay == nullptr ? 1.0f : static_cast<float>(exp(static_cast<double>(log_decay[h])));
+  floatx4 w = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < RPT; ++j) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) m[j][c] = __builtin_fmaf(a, m[j][c], kr[j] * vv[c]);
+    w += m[j] * qr[j];
   }
   // over the 16 row groups: 4 in the wave, then the 4 waves through LDS
 #pragma unroll
@@ -1041,7 +1048,11 @@ __global__ __launch_bounds__(256) void linattn_decode_kernel(
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   if (lane < 16) sw[wave][lane] = w;
   __syncthreads();
-  if (threadIdx.x < 16 && active) {
+  if (!active) return;
+#pragma unroll
+  for (int j = 0; j < RPT; ++j)
+    __builtin_nontemporal_store(m[j], reinterpret_cast<floatx4*>(M + (rg + 16 * j) * dv));
+  if (threadIdx.x < 16) {
     w = sw[0][cg] + sw[1][cg] + sw[2][cg] + sw[3][cg];
     *reinterpret_cast<typename acc4<IO>::type*>(static_cast<char*>(o) +
                                                 vo * opstore<IO>::bytes) = from_f4<IO>(w);
