@@ -69,20 +69,22 @@ __device__ inline int seg_count(int len, int span) {
   return max(1, len / span + (len % span != 0));
 }
 
-// First segment slot of each of 64 sequences from `base` on (exclusive scan
-// over the lanes), given the running total before them.
-__device__ inline int lane_slots(const Cut& c, int base, int lane, int* cnt) {
-  int n = 0;
+// Segment slots of 64 sequences from `base` on in front of each (exclusive
+// scan over the lanes).  Bounds that overlap could add up to more slots than
+// there are: 64 counts of at most 2^25 + 1 and a total held at `slots`
+// (< 2^29) stay below 2^32.
+__device__ inline uint32_t lane_slots(const Cut& c, int base, int lane, uint32_t* cnt) {
+  uint32_t n = 0;
   if (base + lane < c.nseq) {
     int st, en;
     seq_range(c, base + lane, &st, &en);
     n = seg_count(en - st, c.span);
   }
   *cnt = n;
-  int incl = n;
+  uint32_t incl = n;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int up = __shfl_up(incl, d, 64);
+    const uint32_t up = __shfl_up(incl, d, 64);
     if (lane >= d) incl += up;
   }
   return incl - n;
@@ -99,12 +101,12 @@ __device__ inline Segment find_segment(const Cut& c, int slot) {
     return s;
   }
   const int lane = threadIdx.x & 63;
-  int before = 0;
+  uint32_t before = 0, cnt;
   s.seq = -1;
   for (int base = 0; base < c.nseq; base += 64) {
-    int cnt;
-    const int first = before + lane_slots(c, base, lane, &cnt);
-    const uint64_t hit = __ballot(slot >= first && slot < first + cnt);
+    const uint32_t first = before + lane_slots(c, base, lane, &cnt);
+    const uint32_t at = static_cast<uint32_t>(slot);
+    const uint64_t hit = __ballot(at >= first && at < first + cnt);
     if (hit != 0) {
       const int l = __ffsll(static_cast<unsigned long long>(hit)) - 1;
       s.seq = base + l;
@@ -112,7 +114,7 @@ __device__ inline Segment find_segment(const Cut& c, int slot) {
       s.n = __shfl(cnt, l, 64);
       break;
     }
-    before = __shfl(first + cnt, 63, 64);
+    before = min(__shfl(first + cnt, 63, 64), static_cast<uint32_t>(c.slots));
   }
   s.seq = __builtin_amdgcn_readfirstlane(s.seq);
   if (s.seq < 0) return s;
@@ -498,21 +500,21 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       const int n = n_lane + 4 * ct;
-      const bool in = active && n < a.N;
+      const bool there = active && a.enter != nullptr, in = there && n < a.N;
       if (a.image) {
-        const uint32_t at = active ? image_at + ct * 1024 : kOob;
+        const uint32_t at = there ? image_at + ct * 1024 : kOob;
 #pragma unroll
         for (int rt = 0; rt < L::RPS; ++rt)
           S[rt][ct] = __builtin_bit_cast(
-              floatx4, __builtin_amdgcn_raw_buffer_load_b128(
-                           rs, at, rt * 16 < a.R ? rt * CT * 1024 : 0x40000000, 0));
+              floatx4, __builtin_amdgcn_raw_buffer_load_b128(rs, rt * 16 < a.R ? at : kOob,
+                                                             rt * CT * 1024, 0));
       } else if (a.turned) {
         const uint32_t at = in ? (n * a.R + 4 * g) * 4 : kOob;
 #pragma unroll
         for (int rt = 0; rt < L::RPS; ++rt)
           S[rt][ct] = __builtin_bit_cast(
-              floatx4, __builtin_amdgcn_raw_buffer_load_b128(
-                           rs, at, rt * 16 < a.R ? rt * 64 : 0x40000000, 0));
+              floatx4, __builtin_amdgcn_raw_buffer_load_b128(rs, rt * 16 < a.R ? at : kOob,
+                                                             rt * 64, 0));
       } else {
         const uint32_t at = in ? (4 * g * a.N + n) * 4 : kOob;
 #pragma unroll
@@ -520,7 +522,8 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             S[rt][ct][e] = __uint_as_float(
-                __builtin_amdgcn_raw_buffer_load_b32(rs, at, (rt * 16 + e) * a.N * 4, 0));
+                __builtin_amdgcn_raw_buffer_load_b32(rs, rt * 16 < a.R ? at : kOob,
+                                                     (rt * 16 + e) * a.N * 4, 0));
       }
     }
   } else {
@@ -896,18 +899,19 @@ __global__ __launch_bounds__(256) void linattn_combine_kernel(Cut cut, int H, in
     len = cut.T;
   } else {
     const int lane = threadIdx.x & 63;
-    int before = 0, f = 0, cnt = 0;
+    const uint32_t slots = static_cast<uint32_t>(cut.slots);
+    uint32_t before = 0, f = 0, cnt = 0;
     for (int base = 0; base <= seq; base += 64) {
       f = before + lane_slots(cut, base, lane, &cnt);
-      before = __shfl(f + cnt, 63, 64);
+      before = min(__shfl(f + cnt, 63, 64), slots);
     }
-    first = __shfl(f, seq & 63, 64);
-    n = __shfl(cnt, seq & 63, 64);
+    f = min(__shfl(f, seq & 63, 64), slots);
+    // (bounds that overlap need more slots than there are: none beyond them)
+    first = static_cast<int>(f);
+    n = static_cast<int>(min(__shfl(cnt, seq & 63, 64), slots - f));
     int st, en;
     seq_range(cut, seq, &st, &en);
     len = en - st;
-    // (bounds that overlap need more slots than there are: none beyond them)
-    n = static_cast<int>(min(static_cast<int64_t>(n), max(cut.slots - first, int64_t(0))));
   }
   const int e4 = blk * 256 + threadIdx.x;
   if (e4 >= elems / 4) return;
