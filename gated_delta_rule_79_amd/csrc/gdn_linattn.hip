@@ -276,8 +276,8 @@ struct Walk {
   // matrices, nullptr = zeros; `turned`: M is that matrix transposed
   const float* enter;
   int turned;
-  // enter (OUT) and behind (not OUT) in register order instead: per 16 CT
-  // columns and 16 rows, CT tiles of 64 lanes' four rows
+  // enter (OUT) and behind (not OUT) in register order instead: per 32 columns
+  // (16 where N <= 64) and 16 rows, two tiles (one) of 64 lanes' four rows
   int image;
   // state behind the walk: of each (sequence, head), where a segment is the
   // whole sequence (OUT); of each (slot, head), the last ones in walk order
@@ -286,7 +286,7 @@ struct Walk {
   int ends;
 };
 
-// Tiles of a workgroup: R up to 32 NKB, slabs of NP columns.  A wave owns CT
+// Tiles of a workgroup: R up to 32 NKB, slabs of NP columns (launch_walk_n).  A wave owns CT
 // 16-column tiles; with narrow slabs SETS groups of W waves share the output
 // rows (OUT) or the state's rows.
 template <typename IO, int NKB, int NP, bool OUT>
@@ -366,9 +366,17 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
   const bool active = set < L::SETS && n0 + col < a.N;
   const int r0 = OUT ? 0 : set * L::RPS * 16;
 
-  // this wave's place in a state in register order
-  const uint32_t image_elems = (a.N + 16 * CT - 1) / (16 * CT) * 16 * CT * a.R;
-  const uint32_t image_at = (n0 + col) * a.R * 4 + lane * 16;
+  // this lane's place in a state in register order, bytes between row tiles
+  // (a wave of one column tile finds its columns among the interleaved two)
+  const bool wide = a.N > 64;
+  const uint32_t image_elems = (wide ? (a.N + 31) / 32 * 32 : a.N) * a.R;
+  const uint32_t image_step = wide ? 2048 : 1024;
+  auto image_place = [&](int ln) __attribute__((always_inline)) {
+    if (CT == 2 || !wide) return static_cast<uint32_t>((n0 + col) * a.R * 4 + ln * 16);
+    const int n = n0 + col + (ln & 15), c = n & 31;
+    return static_cast<uint32_t>((n >> 5) * a.R * 128 + ((c >> 2) & 1) * 1024 +
+                                 ((ln & 48) + (c >> 3) * 4 + (c & 3)) * 16);
+  };
 
   // Rows of the next chunk, loaded ahead into registers as 16-byte pieces.
   // Row r of the walk is token t0 + r, backwards t0 + len - 1 - r.  Tokens are
@@ -502,12 +510,12 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
       const int n = n_lane + 4 * ct;
       const bool there = active && a.enter != nullptr, in = there && n < a.N;
       if (a.image) {
-        const uint32_t at = there ? image_at + ct * 1024 : kOob;
+        const uint32_t at = there ? image_place(lane) + ct * 1024 : kOob;
 #pragma unroll
         for (int rt = 0; rt < L::RPS; ++rt)
           S[rt][ct] = __builtin_bit_cast(
               floatx4, __builtin_amdgcn_raw_buffer_load_b128(rs, rt * 16 < a.R ? at : kOob,
-                                                             rt * CT * 1024, 0));
+                                                             rt * image_step, 0));
       } else if (a.turned) {
         const uint32_t at = in ? (n * a.R + 4 * g) * 4 : kOob;
 #pragma unroll
@@ -814,8 +822,8 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
       for (int ct = 0; ct < CT; ++ct) {
         if (!OUT && a.image) {
           if (r0 + rt * 16 < a.R)
-            *reinterpret_cast<floatx4*>(bh + (n0 + col) * a.R + ((r0 / 16 + rt) * CT + ct) * 256 +
-                                        again * 4) = S[rt][ct];
+            *reinterpret_cast<floatx4*>(reinterpret_cast<char*>(bh) + image_place(again) +
+                                        (r0 / 16 + rt) * image_step + ct * 1024) = S[rt][ct];
           continue;
         }
         const int r = r0 + rt * 16 + 4 * (again >> 4),
@@ -1075,7 +1083,7 @@ struct Plan {
   bool split;
 };
 
-// Tiles and slabs of a walk, as launch_walk_io picks them.
+// Tiles of a walk, as launch_walk_io and launch_walk_n pick them.
 int tiles_of(int R, int N) {
   return (R > 128 ? 8 : R > 64 ? 4 : R > 32 ? 2 : 1) * 1024 +
          (N <= 32 ? 0 : N <= 64 ? 1 : 1 + (N + 127) / 128);
@@ -1152,8 +1160,17 @@ void launch_walk_t(const Walks& w, int64_t slots, hipStream_t s) {
 template <typename IO, int NKB, bool OUT, bool BOTH>
 void launch_walk_n(const Walks& w, int64_t slots, hipStream_t s) {
   const int N = w.w[0].N;
-  if (N <= 32) return launch_walk_t<IO, NKB, 32, OUT, BOTH>(w, slots, s);
-  if (N <= 64) return launch_walk_t<IO, NKB, 64, OUT, BOTH>(w, slots, s);
+  // A workgroup's chunk takes less time the fewer columns it has (dk 128: 4.6
+  // us for 128, 3.2 for 64, 2.8 for 32), so slabs are as narrow as leave every
+  // workgroup a CU of its own (T256 H16: 128 columns 25.8 us, 64: 18.9, 32:
+  // 17.5).  Past that the x and y rows that all slabs read, and their x y^T,
+  // cost more (B8 T2048 H8 backward, 192 workgroups: 128 columns 134 us, 64:
+  // 143; 96 of them: 129, 103).
+  auto fits = [&](int np) {
+    return slots * w.w[0].H * ((N + np - 1) / np) * w.n <= 256;
+  };
+  if (N <= 32 || fits(32)) return launch_walk_t<IO, NKB, 32, OUT, BOTH>(w, slots, s);
+  if (N <= 64 || fits(64)) return launch_walk_t<IO, NKB, 64, OUT, BOTH>(w, slots, s);
   launch_walk_t<IO, NKB, 128, OUT, BOTH>(w, slots, s);
 }
 
