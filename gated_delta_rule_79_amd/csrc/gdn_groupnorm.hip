@@ -13,7 +13,10 @@
 // 16-byte pieces (fp32: two); the lanes of a row are a power of two, those
 // past d / 8 idle.  The row stays in registers between its statistics and
 // its output, so x (z, dy) is read once and y (dx, dz) written once: the
-// pass is a stream and HBM bounds it.  All arithmetic is fp32, the variance
+// pass is a stream and HBM bounds it (forward, 65536 gated rows of 128 in
+// bf16: 50 MB in 11.5 us, 4.4 TB/s; backward, 262144 of 256: 671 MB in 135
+// us, 5.0 TB/s; holding the next row's pieces in registers meanwhile took
+// 13.5 us, two rows a turn 15).  All arithmetic is fp32, the variance
 // taken around the mean.  A thread keeps its head over its rows (the grid's
 // stride is a whole number of tokens), so its weights are loaded once and
 // its share of dw, db stays in registers.
@@ -205,7 +208,8 @@ __global__ __launch_bounds__(kThreads) void group_norm_kernel(Args a) {
 
 // Sums of the partial dw, db rows of each group (row index mod `period`), in
 // a fixed order: out[g, c] = sum_k part[g + k period, c].  Sixteen columns of
-// one group a workgroup, 64 runs of rows added up in LDS.
+// one group a workgroup, 64 runs of rows added up in LDS (16k tokens, H16,
+// d 256: 8 us for 17 MB).
 constexpr int kRuns = 64;
 __global__ __launch_bounds__(16 * kRuns) void group_norm_sum_kernel(const float* pw,
                                                                     const float* pb, int64_t rows,
@@ -257,6 +261,7 @@ int partial_rows(const GroupNorm& p) {
   return p.shared ? 1 : per % p.H == 0 ? p.H : per;
 }
 
+// (eight and four blocks a CU: the forward measured slower at 1024 and 4096)
 constexpr int64_t kFwdBlocks = 2048, kBwdBlocks = 1024;
 
 template <typename IO, int LPR, int ACT, bool BWD>

@@ -24,6 +24,15 @@
 //   M_out = a^len M_in + sum_j a^{len-off-j} y_j z_j^T
 // Every power of a has a non-negative exponent, so no factor overflows for
 // a <= 1 and a = 0 (log_decay = -inf) is exact; a^0 is 1.
+//
+// A long sequence with few heads is cut into segments: one launch walks the
+// segments' own states (no outputs), one chains them, one walks the outputs
+// from the chained states (plan_walk).  The whole needs 4 dk dv flops a token
+// and head for 4 rows of bytes (bf16 128 x 128: 64 flops a byte), so memory
+// bounds large calls: 65k packed tokens of 16 heads take 406 us for 1.09 GB
+// that must move (2.7 TB/s; 1.8 GB with k and v read twice and the states,
+// 4.4 TB/s).  Small ones are bound by the chain: a workgroup's chunk has
+// three barriers and takes 2.8 to 4.6 us alone on its CU.
 
 #include <algorithm>
 #include <type_traits>
@@ -326,6 +335,10 @@ struct WalkTiles {
 // state's registers, re-packed as an operand), scaled in fp32, plus
 // z^T (x y^T)^T, stored at once; the state update last, while the stores
 // drain.
+// Alone on a CU a workgroup (four waves, one a SIMD) waits most of a chunk
+// (matrix cores 15 % busy); two share it where there is work for them (25 %,
+// 65k tokens), which memory then bounds: 256 us for 1.1 GB.  Eight waves
+// instead of four took 315 us there, a second chunk of rows in flight 283.
 // The update's weights go onto z in fp32, and the product is split into
 // bf16 parts, so the carried state keeps the fp32 accuracy of its storage.
 // Operand reads run one step ahead of the products that take them
@@ -871,7 +884,9 @@ void linattn_walk_kernel(Walks walks) {
 // segment's own contribution (the last one's in walk order only with `fin`,
 // which takes the state behind it) and becomes the state entering it,
 // E' = a^len E + own.  A thread carries four state elements through the
-// sequence's segments; loads run ahead of the chain.
+// sequence's segments; sixteen loads run ahead of the chain.  Memory bounds
+// it (16k tokens in 4 sequences, dk 128 dv 256, both directions: 140 MB in 32
+// us, 4.4 TB/s), in short calls the launch (T4096 H16: 33 MB in 8 us).
 // image: buf holds the states in register order (Walk::image, with CT column
 // tiles a block); init is a [dk, dv] matrix.
 struct Combine {  // one of up to two directions of a launch
@@ -979,11 +994,15 @@ __global__ __launch_bounds__(256) void linattn_combine_kernel(Cut cut, int H, in
 // ---------------------------------------------------------- shared heads ---
 // Gradients of q and k heads: the sum over the v heads that read it, in head
 // order, from the fp32 rows of each (part and part + apart: [tokens, H, d] ->
-// out0 and out1: [tokens, Hq, d]).  Tokens behind the last sequence are left alone.
+// out0 and out1: [tokens, Hq, d]).  Tokens behind the last sequence are left
+// alone.  A stream: 16k tokens of 16 heads over 8, d 128, 335 MB in 64 us
+// (5.2 TB/s).  Atomics into one fp32 row would save the pass but add in an
+// order that changes.
 template <typename IO>
 __global__ __launch_bounds__(256) void linattn_share_kernel(const float* part, int64_t apart,
-                                                            void* out0, void* out1, int64_t tokens, int Hq, int grp,
-                                                            int d, const int32_t* cu, int nseq) {
+                                                            void* out0, void* out1,
+                                                            int64_t tokens, int Hq, int grp, int d,
+                                                            const int32_t* cu, int nseq) {
   void* const out = blockIdx.y == 0 ? out0 : out1;
   part += blockIdx.y * apart;
   if (cu != nullptr) tokens = min(tokens, static_cast<int64_t>(max(cu[nseq], 0)));
