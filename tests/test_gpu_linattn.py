@@ -133,6 +133,30 @@ def test_backward(gpu_lib, shape, dtype):
         check_bwd(d, cu, dtype, run_bwd(d, cu, seg_chunks=seg))
 
 
+# Enough heads that slabs are 128 columns wide (fewer workgroups than CUs take
+# 64 or 32): every size class of rows and columns, partial slabs among them.
+WIDE = [(2, 70, 66, 33, 128, 128), (1, 67, 88, 88, 64, 144), (1, 66, 70, 35, 128, 224),
+        (2, 70, 66, 66, 32, 112), (2, 70, 66, 66, 16, 80)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", WIDE)
+def test_many_heads(gpu_lib, shape, dtype):
+    log(f"[linattn many heads] {shape} {dtype}")
+    d, cu = make(*shape, dtype, do=True)
+    f = f64(d)
+    m = absolute(f)
+    args = ("q", "k", "v", "log_decay", "s0")
+    n = shape[1] + max(shape[4:]) + 64
+    fwd = [oracle.linattn_fwd(*(x[a] for a in args)) for x in (f, m)]
+    bwd = [oracle.linattn_bwd(*(x[a] for a in args), x["do"], x["ds"]) for x in (f, m)]
+    for seg in (-1, 1):
+        for name, g, r, a in zip(("o", "s_final"), run_fwd(d, cu, seg_chunks=seg), *fwd):
+            check(name, g, r, a, dtype, n, state=name == "s_final")
+        for name, g, r, a in zip(("dq", "dk", "dv", "ds0"), run_bwd(d, cu, seg_chunks=seg), *bwd):
+            check(name, g, r, a, dtype, n, state=name == "ds0")
+
+
 CUTS = [[0, 0, 1, 64, 64, 129, 300], [0, 300], [0, 150, 150], [0, 63, 127, 300], [0, 1, 2, 3]]
 
 
