@@ -576,6 +576,23 @@ def _want(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
+def _result(t, name, like):
+    """A caller's preallocated output, checked, or a new tensor like ``like``."""
+    if t is None:
+        return torch.empty_like(like)
+    _want(t, name, like.shape, like.dtype, like.device)
+    return t
+
+
+def _states(t, name, shape, device, like):
+    """The same for fp32 states; ``like``: a tensor of that kind or None."""
+    if t is None:
+        return (torch.empty(shape, dtype=torch.float32, device=device) if like is None
+                else torch.empty_like(like))
+    _want(t, name, shape, torch.float32, device)
+    return t
+
+
 def _bytes(fn, p, *args):
     need = ctypes.c_size_t(0)
     _lib.check(fn(ctypes.byref(p), *args, ctypes.byref(need)), fn.__name__)
@@ -596,23 +613,27 @@ def _workspace(ws, need, device):
 def _linattn_problem(q, k, v, log_decay, cu_seqlens, seg_chunks, lead):
     """The problem of a linear-attention call; `lead`: dimensions in front of
     the heads (batch and time, or the sequences of a decode step)."""
-    if q.dim() != lead + 2 or v.dim() != lead + 2:
+    qs, vs, dtype, device = q.shape, v.shape, q.dtype, q.device
+    if len(qs) != lead + 2 or len(vs) != lead + 2:
         raise ValueError(f"q and v must have {lead + 2} dimensions")
     if not q.is_cuda:
         raise ValueError("libgdn takes GPU tensors")
-    hq, dk = q.shape[lead:]
-    H, dv = v.shape[lead:]
-    _want(k, "k", q.shape, q.dtype, q.device)
-    _want(v, "v", (*q.shape[:lead], H, dv), q.dtype, q.device)
-    _want(log_decay, "log_decay", (H,), torch.float32, q.device)
-    _check_cu(cu_seqlens, q)
-    if cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2):
-        raise ValueError("cu_seqlens must hold the bounds of at least one sequence")
-    packed = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
-    p = _lib.GdnProblem(q.shape[0], q.shape[1] if lead == 2 else 1, H, dk, dv, 0, packed,
+    _want(k, "k", qs, dtype, device)
+    if vs[:lead] != qs[:lead] or v.dtype != dtype or v.device != device:
+        raise ValueError(f"v must be a {dtype} tensor of {tuple(qs[:lead])} rows on {device}")
+    hq, dk = qs[lead:]
+    H, dv = vs[lead:]
+    _want(log_decay, "log_decay", (H,), torch.float32, device)
+    packed = 0
+    if cu_seqlens is not None:
+        _check_cu(cu_seqlens, q)
+        packed = cu_seqlens.numel() - 1
+        if cu_seqlens.dim() != 1 or packed < 1:
+            raise ValueError("cu_seqlens must hold the bounds of at least one sequence")
+    p = _lib.GdnProblem(qs[0], qs[1] if lead == 2 else 1, H, dk, dv, 0, packed,
                         _ptr(cu_seqlens), _dtype_code(q), _lib.GDN_F32, _lib.GDN_GATE_NONE,
                         int(seg_chunks))
-    return p, hq, (packed or q.shape[0], H, dk, dv)
+    return p, hq, (packed or qs[0], H, dk, dv)
 
 
 def linear_attn_fwd(q, k, v, log_decay=None, s0=None, cu_seqlens=None,
@@ -628,8 +649,8 @@ def linear_attn_fwd(q, k, v, log_decay=None, s0=None, cu_seqlens=None,
     lib = _lib.load()
     p, hq, states = _linattn_problem(q, k, v, log_decay, cu_seqlens, seg_chunks, 2)
     _want(s0, "s0", states, torch.float32, q.device)
-    o = _out(o, v.shape, q.dtype, q.device)
-    sf = _out(s_final, states, torch.float32, q.device) if output_final_state else None
+    o = _result(o, "o", v)
+    sf = _states(s_final, "s_final", states, q.device, s0) if output_final_state else None
     ws, nbytes = _workspace(workspace, _bytes(lib.gdn_linear_attn_fwd_workspace, p, hq), q.device)
     _launch(lib.gdn_linear_attn_fwd, q.device, ctypes.byref(p), hq, _ptr(q), _ptr(k), _ptr(v),
             _ptr(log_decay), _ptr(s0), _ptr(o), _ptr(sf), _ptr(ws), nbytes)
@@ -648,10 +669,10 @@ def linear_attn_bwd(q, k, v, log_decay, s0, d_o, ds_final=None, cu_seqlens=None,
     _want(d_o, "d_o", v.shape, v.dtype, q.device)
     _want(ds_final, "ds_final", states, torch.float32, q.device)
     out = (None,) * 4 if out is None else tuple(out)
-    dq = _out(out[0], q.shape, q.dtype, q.device)
-    dk = _out(out[1], k.shape, k.dtype, q.device)
-    dv = _out(out[2], v.shape, v.dtype, q.device)
-    ds0 = _out(out[3], states, torch.float32, q.device) if need_ds0 else None
+    dq = _result(out[0], "dq", q)
+    dk = _result(out[1], "dk", k)
+    dv = _result(out[2], "dv", v)
+    ds0 = _states(out[3], "ds0", states, q.device, s0) if need_ds0 else None
     ws, nbytes = _workspace(workspace, _bytes(lib.gdn_linear_attn_bwd_workspace, p, hq), q.device)
     _launch(lib.gdn_linear_attn_bwd, q.device, ctypes.byref(p), hq, _ptr(q), _ptr(k), _ptr(v),
             _ptr(log_decay), _ptr(s0), _ptr(d_o), _ptr(ds_final), _ptr(dq), _ptr(dk), _ptr(dv),
@@ -669,7 +690,7 @@ def linear_attn_decode_step(q, k, v, log_decay, state, o=None):
     if state is None:
         raise ValueError("state must be given")
     _want(state, "state", states, torch.float32, q.device)
-    o = _out(o, v.shape, q.dtype, q.device)
+    o = _result(o, "o", v)
     _launch(lib.gdn_linear_attn_decode_step, q.device, ctypes.byref(p), hq, _ptr(q), _ptr(k),
             _ptr(v), _ptr(log_decay), _ptr(state), _ptr(o))
     return o
@@ -686,12 +707,14 @@ def _norm_problem(x, weight, bias, gate, act):
         raise ValueError("libgdn takes GPU tensors")
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
-    B, T, H, d = x.shape
-    _want(gate, "gate", x.shape, x.dtype, x.device)
-    one = next((t for t in (weight, bias) if t is not None), None)
+    xs, device = x.shape, x.device
+    B, T, H, d = xs
+    _want(gate, "gate", xs, x.dtype, device)
+    one = bias if weight is None else weight
     shared = one is not None and one.dim() == 1
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        _want(t, name, (d,) if shared else (H, d), torch.float32, x.device)
+    shape = (d,) if shared else (H, d)
+    _want(weight, "weight", shape, torch.float32, device)
+    _want(bias, "bias", shape, torch.float32, device)
     p = _lib.GdnProblem(B, T, H, d, d, 0, 0, None, _dtype_code(x))
     return p, _ACTS[act], int(shared)
 
@@ -706,7 +729,7 @@ def group_norm_fwd(x, weight=None, bias=None, gate=None, act: str = "silu", eps:
     output (may be x or gate itself).  Returns y."""
     lib = _lib.load()
     p, code, shared = _norm_problem(x, weight, bias, gate, act)
-    y = _out(y, x.shape, x.dtype, x.device)
+    y = _result(y, "y", x)
     _launch(lib.gdn_group_norm_fwd, x.device, ctypes.byref(p), p.dv, code, int(center), shared,
             eps, _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y))
     return y

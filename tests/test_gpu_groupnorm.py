@@ -209,7 +209,7 @@ def test_refusals(gpu_lib):
     for kw in (dict(weight=w[:1]), dict(weight=w.bfloat16()), dict(bias=w.cpu()),
                dict(weight=w, bias=w[0].contiguous()), dict(gate=x.float()),
                dict(gate=x[:, :3].contiguous()), dict(act="gelu"), dict(weight=w.t()),
-               dict(y=x.float())):
+               dict(y=x.float()), dict(y=x.cpu())):
         with pytest.raises(ValueError):
             gdn.group_norm_fwd(x, **kw)
     with pytest.raises(gdn.GdnError):

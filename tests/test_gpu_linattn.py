@@ -480,6 +480,18 @@ def test_refusals(gpu_lib):
         gdn.linear_attn_fwd(q3, q3, v, la)
     with pytest.raises(ValueError):
         gdn.linear_attn_bwd(q, k, v, la, s0, v.float())
+    # outputs of another shape, type, layout or memory
+    for kw in (dict(o=torch.empty_like(v, device="cpu")), dict(o=v.float()),
+               dict(o=torch.empty(1, 4, 20, 32, device="cuda", dtype=BF16).transpose(1, 2)),
+               dict(s_final=s0.cpu()), dict(s_final=s0[:, :2].contiguous()),
+               dict(workspace=torch.empty(1 << 20, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            gdn.linear_attn_fwd(q, k, v, la, s0, **kw)
+    for i, t in ((0, q.cpu()), (1, k.float()), (2, v[:, :4].contiguous()), (3, s0.cpu())):
+        out = [None] * 4
+        out[i] = t
+        with pytest.raises(ValueError):
+            gdn.linear_attn_bwd(q, k, v, la, s0, v, out=out)
     with pytest.raises(ValueError):
         gdn.linear_attn_decode_step(q[:, 0].contiguous(), k[:, 0].contiguous(),
                                     v[:, 0].contiguous(), la, s0.bfloat16())
