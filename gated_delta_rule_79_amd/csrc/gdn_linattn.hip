@@ -295,9 +295,9 @@ struct Walk {
   int ends;
 };
 
-// Tiles of a workgroup: R up to 32 NKB, slabs of NP columns (launch_walk_n).  A wave owns CT
-// 16-column tiles; with narrow slabs SETS groups of W waves share the output
-// rows (OUT) or the state's rows.
+// Tiles of a workgroup: R up to 32 NKB, slabs of NP columns (launch_walk_n).
+// A wave owns CT 16-column tiles; with narrow slabs SETS groups of W waves
+// share the output rows (OUT) or the state's rows.
 template <typename IO, int NKB, int NP, bool OUT>
 struct WalkTiles {
   static constexpr int C = walk_chunk<IO>();
@@ -338,7 +338,8 @@ struct WalkTiles {
 // Alone on a CU a workgroup (four waves, one a SIMD) waits most of a chunk
 // (matrix cores 15 % busy); two share it where there is work for them (25 %,
 // 65k tokens), which memory then bounds: 256 us for 1.1 GB.  Eight waves
-// instead of four took 315 us there, a second chunk of rows in flight 283.
+// instead of four took 315 us there, one copy of the code for both directions
+// 283.
 // The update's weights go onto z in fp32, and the product is split into
 // bf16 parts, so the carried state keeps the fp32 accuracy of its storage.
 // Operand reads run one step ahead of the products that take them
@@ -839,8 +840,8 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
                                         (r0 / 16 + rt) * image_step + ct * 1024) = S[rt][ct];
           continue;
         }
-        const int r = r0 + rt * 16 + 4 * (again >> 4),
-                  n = n0 + col + (CT == 2 ? 8 * ((again & 15) >> 2) + (again & 3) + 4 * ct : again & 15);
+        const int l = again & 15, r = r0 + rt * 16 + 4 * (again >> 4),
+                  n = n0 + col + (CT == 2 ? 8 * (l >> 2) + (l & 3) + 4 * ct : l);
         if (r >= a.R || n >= a.N) continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e) bh[(r + e) * a.N + n] = S[rt][ct][e];
@@ -1126,8 +1127,9 @@ Plan plan_walk(const LinAttn& p, bool bwd) {
     if (p.varlen) {
       // Segments for two workgroups a CU (512), in whole rounds: each chain
       // ends in a segment that is half full on average, which may take up
-      // to a quarter of a round (65k tokens in 7 sequences: 37 chunks 390 us,
-      // 12: 441; 32k in 24: 10 to 12 chunks 232, 26: 251)
+      // to a quarter of a round (65k tokens of 16 heads in 7 sequences: 36
+      // chunks 431 us, 24: 425, 32: 473, 12: 448; backward of 16k in 16: 11
+      // chunks 300, 24: 343).
       const int64_t all = std::max<int64_t>(512, (2 * chains + 511) / 512 * 512);
       const int64_t room = all - chains / 2;
       L = (units + room - 1) / room;
@@ -1297,7 +1299,8 @@ bool linattn_grid_ok(const LinAttn& p) {
   const Plan pl = plan_walk(p, false), plb = plan_walk(p, true);
   const int64_t most = (int64_t(1) << 31) - 1;
   const int64_t blocks = (static_cast<int64_t>(image_elems(p)) / 4 + 255) / 256;
-  return std::max(pl.slots, plb.slots) * p.H * 6 <= most && 2 * static_cast<int64_t>(p.nseq) * p.H * blocks <= most;
+  return std::max(pl.slots, plb.slots) * p.H * 6 <= most &&
+         2 * static_cast<int64_t>(p.nseq) * p.H * blocks <= most;
 }
 
 size_t linattn_fwd_workspace_bytes(const LinAttn& p) { return state_bytes(p, plan_walk(p, false)); }

@@ -427,7 +427,8 @@ gdn_status gdn_decode_step_product(const gdn_problem* p, int32_t nh, const void*
  *   log_decay : [H] fp32, 16-byte aligned, or NULL for a = 1 (plain causal
  *               linear attention).  Normally <= 0; -inf is a = 0.
  *   s0, s_final : [nseq, H, dk, dv] fp32 or NULL, as in gdn_chunk_fwd.
- *   ws        : at least gdn_linear_attn_fwd_workspace bytes.
+ *   ws        : at least gdn_linear_attn_fwd_workspace bytes; calls that
+ *               overlap in time (streams, captured graphs) need one each.
  * Products of bf16 operands are summed in fp32; the state is carried (and
  * s_final written) to fp32 accuracy in either type; only the copy of the
  * state that multiplies bf16 rows is rounded to bf16 (half a step of 2^-8),
