@@ -745,9 +745,11 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
 
     if (active) {
       if constexpr (OUT) {
-        // M^T x^T, the state rounded once to the operand type (a second part of
-        // it would cost another 2 % to 5 % and take the outputs' error from
-        // 1.4 roundings of their own to 1)
+        // M^T x^T, the copy of the state in two operand parts (2^-17 left):
+        // with one, its rounding takes the outputs' error from one rounding of
+        // their own to 1.4, in every call that enters with a state or runs on
+        // past a chunk.  The second part costs 3 % (65k tokens: 409 us, 420)
+        // to 10 % (B8 T2048 H8 backward: 130 us, 142).
         opvec<IO> xf[2][L::IPS];
         auto read_x = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
@@ -771,6 +773,16 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
               acc[it][ct] = mma32(m[ct], xf[kb & 1][it], acc[it][ct]);
+          if constexpr (ob == 2) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+              m[ct] = pack2_rest(S[2 * kb][ct], S[2 * kb + 1][ct], m[ct]);
+#pragma unroll
+            for (int it = 0; it < L::IPS; ++it)
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct)
+                acc[it][ct] = mma32(m[ct], xf[kb & 1][it], acc[it][ct]);
+          }
         }
 #pragma unroll
         for (int it = 0; it < L::IPS; ++it) {

@@ -430,9 +430,9 @@ gdn_status gdn_decode_step_product(const gdn_problem* p, int32_t nh, const void*
  *   ws        : at least gdn_linear_attn_fwd_workspace bytes; calls that
  *               overlap in time (streams, captured graphs) need one each.
  * Products of bf16 operands are summed in fp32; the state is carried (and
- * s_final written) to fp32 accuracy in either type; only the copy of the
- * state that multiplies bf16 rows is rounded to bf16 (half a step of 2^-8),
- * q k^T goes in two bf16 parts (2^-17).  Rows
+ * s_final written) to fp32 accuracy in either type; the copy of the state
+ * that multiplies bf16 rows and the decayed q k^T go in two bf16 parts each
+ * (2^-17 of a value left), so an output is the exact one rounded once.  Rows
  * of packed tensors behind cu_seqlens[nseq] are neither read nor written.
  * A NaN or infinity in a token reaches the outputs of its own chunk and of
  * all later tokens of its sequence, never another sequence.  Deterministic.
