@@ -214,8 +214,11 @@ __device__ inline opvec<IO> lds_col8(const char* p) {
 }
 
 // A column of 8 weighted values as operand parts.  bf16: N parts after
-// SKIP earlier ones; k parts leave 2^(-9 k) of the value behind.  fp32
-// operands are the value itself.
+// SKIP earlier ones.  Each keeps 8 bits rounded to nearest, so one leaves at
+// most 2^-8 of the value, two 2^-17 (the rest's sign carries the ninth bit),
+// and three hold the 24 bits of an fp32 one (a product whose rest is formed
+// by a fused multiply-add may keep bits behind those: 1e-9 of a state, which
+// its fp32 sums do not hold).  fp32 operands are the value itself.
 template <typename IO> struct Parts;
 template <> struct Parts<f32_t> {
   static constexpr int most = 1;
@@ -614,11 +617,12 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
       *reinterpret_cast<opvec<IO>*>(at + C * C * ob) = pack2_rest(p0, p1, r);
   };
 
-  // M <- a^n M + sum_j y_j (w_j z_j)^T, the weighted rows in NPART operand
-  // parts (pass 0), or M += their next NPART parts (pass 1)
-  constexpr int NPART = OUT ? std::min(2, Parts<IO>::most) : Parts<IO>::most;
+  // M <- a^n M + sum_j y_j (w_j z_j)^T, the weighted rows in their first
+  // FIRST operand parts (pass 0), or M += the parts left (pass 1)
+  constexpr int FIRST = OUT ? std::min(2, Parts<IO>::most) : Parts<IO>::most;
   auto update = [&](int n, auto which) __attribute__((always_inline)) {
     constexpr int pass = decltype(which)::value;
+    constexpr int NPART = pass == 0 ? FIRST : Parts<IO>::most - FIRST;
     const float mul = n == C ? mul_full : mul_tail, add = n == C ? add_full : add_tail;
     auto fade = [&](int rt) __attribute__((always_inline)) {
 #pragma unroll
@@ -659,7 +663,7 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = lo[e], w[4 + e] = hi[e];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) wz[ct].template set<NPART, pass * NPART>(zf[ct], w);
+        for (int ct = 0; ct < CT; ++ct) wz[ct].template set<NPART, pass * FIRST>(zf[ct], w);
         if (kb + 1 < NKC) read_z(kb + 1);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -824,12 +828,14 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
     }
     if (active) {
       // The state behind the chunk, where another chunk or the caller wants
-      // it.  One that only multiplies bf16 rows keeps 2^-18 with two parts;
-      // what a caller gets takes a second pass of two more (another
-      // workgroup's: three at once).
+      // it.  One that only multiplies bf16 rows keeps 2^-17 of each term with
+      // two parts; what a caller gets takes a second pass with the third
+      // (another workgroup's: three at once).  A fourth changed nothing but
+      // bits below fp32 and cost 4 to 6 % (B32 T1024 H16, uncut: forward 172
+      // us, 162; backward 425, 409).
       const bool handed = OUT && last && a.behind != nullptr;
       if (!OUT || handed || c + 1 < nch) update(len, std::integral_constant<int, 0>());
-      if constexpr (NPART < Parts<IO>::most)
+      if constexpr (FIRST < Parts<IO>::most)
         if (handed) update(len, std::integral_constant<int, 1>());
     }
   }

@@ -90,6 +90,18 @@ def test_the_bound_tells_parts_apart(shape):
             check(f"{copy}, {own}", rounded_fwd(d, copy, own), ref, mag, T, dk)
 
 
+def test_what_parts_leave():
+    # the shares named above are met but not passed, and three parts are whole
+    r = np.random.default_rng(5)
+    x = (r.standard_normal(1 << 18) * 2.0 ** r.integers(-30, 30, 1 << 18)).astype(np.float32)
+    x = np.concatenate([x, np.nextafter(np.float32(1), np.float32(2)) + np.float32(2.0 ** -8),
+                        np.float32(2) - np.float32(2.0 ** -23)], axis=None).astype(np.float64)
+    for n, most in ((1, 2.0 ** -8), (2, 2.0 ** -17), (3, 0.0)):
+        left = np.abs(x - parts(x, n)) / np.abs(x)
+        assert left.max() <= most, n
+        assert n == 3 or left.max() > most / 2, n
+
+
 # ------------------------------------------------------------------ the kernels
 
 @pytest.mark.gpu
