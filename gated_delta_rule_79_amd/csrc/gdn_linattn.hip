@@ -35,6 +35,7 @@
 // three barriers and takes 2.8 to 4.6 us alone on its CU.
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "gdn_chunk_common.hpp"
@@ -50,16 +51,18 @@ template <typename IO> constexpr int walk_chunk() { return opstore<IO>::bytes ==
 // ------------------------------------------------------------- segments ---
 // A walk is cut into segments of `span` tokens (a multiple of the chunk,
 // counted from each sequence's first token); one workgroup walks one segment
-// of one head and column slab.  Segment slots of packed sequences are found
-// from cu_seqlens by every wave for itself (lengths clamped into [0, T], so
-// malformed bounds cannot send a kernel out of range).
+// of one head and column slab.  Of a packed batch only sequences longer than
+// `span` are cut: their segments take the first `slots` slots, found from
+// cu_seqlens by every wave for itself, and slot slots + i is sequence i where
+// it is walked whole (lengths clamped into [0, T], so malformed bounds cannot
+// send a kernel out of range).
 
 struct Cut {
   const int32_t* cu;  // device [nseq + 1], or nullptr: dense
   int nseq, T;
   int span;           // tokens per segment
   int per_seq;        // dense: segments per sequence (>= 1)
-  int64_t slots;      // segment slots there is room for
+  int64_t slots;      // segment slots there is room for (packed: of cut sequences)
 };
 
 struct Segment {
@@ -74,20 +77,21 @@ __device__ inline void seq_range(const Cut& c, int seq, int* st, int* en) {
   *en = min(max(c.cu[seq + 1], *st), c.T);
 }
 
-__device__ inline int seg_count(int len, int span) {
-  return max(1, len / span + (len % span != 0));
+// Segments of a packed sequence that is cut, 0 for one that is not.
+__device__ inline int cut_count(int len, int span) {
+  return len <= span ? 0 : len / span + (len % span != 0);
 }
 
-// Segment slots of 64 sequences from `base` on in front of each (exclusive
-// scan over the lanes).  Bounds that overlap could add up to more slots than
-// there are: 64 counts of at most 2^25 + 1 and a total held at `slots`
-// (< 2^29) stay below 2^32.
+// Cut sequences' slots of 64 sequences from `base` on in front of each
+// (exclusive scan over the lanes).  Bounds that overlap could add up to more
+// slots than there are: 64 counts of at most 2^25 + 1 and a total held at
+// `slots` (< 2^29) stay below 2^32.
 __device__ inline uint32_t lane_slots(const Cut& c, int base, int lane, uint32_t* cnt) {
   uint32_t n = 0;
   if (base + lane < c.nseq) {
     int st, en;
     seq_range(c, base + lane, &st, &en);
-    n = seg_count(en - st, c.span);
+    n = cut_count(en - st, c.span);
   }
   *cnt = n;
   uint32_t incl = n;
@@ -107,6 +111,17 @@ __device__ inline Segment find_segment(const Cut& c, int slot) {
     s.n = c.per_seq;
     s.tok0 = static_cast<int64_t>(s.seq) * c.T + static_cast<int64_t>(s.j) * c.span;
     s.len = min(c.span, c.T - s.j * c.span);
+    return s;
+  }
+  int st, en;
+  if (slot >= c.slots) {
+    s.seq = slot - static_cast<int>(c.slots);
+    seq_range(c, s.seq, &st, &en);
+    s.j = 0;
+    s.n = 1;
+    s.tok0 = st;
+    s.len = en - st;
+    if (s.len > c.span) s.seq = -1;
     return s;
   }
   const int lane = threadIdx.x & 63;
@@ -129,7 +144,6 @@ __device__ inline Segment find_segment(const Cut& c, int slot) {
   if (s.seq < 0) return s;
   s.j = __builtin_amdgcn_readfirstlane(s.j);
   s.n = __builtin_amdgcn_readfirstlane(s.n);
-  int st, en;
   seq_range(c, s.seq, &st, &en);
   s.tok0 = st + static_cast<int64_t>(s.j) * c.span;
   s.len = min(c.span, en - st - s.j * c.span);
@@ -284,16 +298,17 @@ struct Walk {
   const float* log_decay;  // [H] or nullptr (a = 1)
   void* out;               // [tokens, H, N]
   int out_f32;             // 1: out is fp32 whatever the operands are
-  // state in front of each (segment slot, head) in walk order: [dk, dv]
-  // matrices, nullptr = zeros; `turned`: M is that matrix transposed
-  const float* enter;
+  // state in front in walk order, [dk, dv] matrices: of each (sequence, head)
+  // (nullptr = zeros), taken where a segment is the whole sequence, and of
+  // each (segment slot, head); `turned`: M is that matrix transposed
+  const float *init, *enter;
   int turned;
   // enter (OUT) and behind (not OUT) in register order instead: per 32 columns
   // (16 where N <= 64) and 16 rows, two tiles (one) of 64 lanes' four rows
   int image;
   // state behind the walk: of each (sequence, head), where a segment is the
-  // whole sequence (OUT); of each (slot, head), the last ones in walk order
-  // only if `ends` (not OUT)
+  // whole sequence (OUT; nullptr = not wanted); of each (slot, head), the last
+  // ones in walk order only if `ends` (not OUT)
   float* behind;
   int ends;
 };
@@ -370,6 +385,7 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
   if (seg.seq < 0) return;
   const bool last = rev ? seg.j == 0 : seg.j == seg.n - 1;  // in walk order
   if (!OUT && last && !a.ends) return;
+  const bool whole = seg.n == 1;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -516,17 +532,17 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
   // the state's, and a state that is not there, read zeros from no memory).
   floatx4 S[L::RPS][CT];
   if constexpr (OUT) {
-    const uint32_t elems = a.image ? image_elems : a.R * a.N;
+    const float* const enter = whole ? a.init : a.enter;
+    const bool image = !whole && a.image;
+    const uint32_t elems = image ? image_elems : a.R * a.N;
+    const int64_t at = (static_cast<int64_t>(whole ? seg.seq : slot) * a.H + h) * elems;
     const __amdgpu_buffer_rsrc_t rs =
-        make_rsrc(a.enter + (a.enter == nullptr
-                                 ? 0
-                                 : (static_cast<int64_t>(slot) * a.H + h) * elems),
-                  a.enter == nullptr ? 0 : elems * 4);
+        make_rsrc(enter + (enter == nullptr ? 0 : at), enter == nullptr ? 0 : elems * 4);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       const int n = n_lane + 4 * ct;
-      const bool there = active && a.enter != nullptr, in = there && n < a.N;
-      if (a.image) {
+      const bool there = active && enter != nullptr, in = there && n < a.N;
+      if (image) {
         const uint32_t at = there ? image_place(lane) + ct * 1024 : kOob;
 #pragma unroll
         for (int rt = 0; rt < L::RPS; ++rt)
@@ -833,7 +849,7 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
       // (another workgroup's: three at once).  A fourth changed nothing but
       // bits below fp32 and cost 4 to 6 % (B32 T1024 H16, uncut: forward 172
       // us, 162; backward 425, 409).
-      const bool handed = OUT && last && a.behind != nullptr;
+      const bool handed = OUT && whole && a.behind != nullptr;
       if (!OUT || handed || c + 1 < nch) update(len, std::integral_constant<int, 0>());
       if constexpr (FIRST < Parts<IO>::most)
         if (handed) update(len, std::integral_constant<int, 1>());
@@ -844,7 +860,7 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
   int again = lane;
   asm volatile("" : "+v"(again));
   float* bh = a.behind;
-  if (bh != nullptr && active && (OUT ? last && set == 0 : true)) {
+  if (bh != nullptr && active && (OUT ? whole && set == 0 : true)) {
     const int64_t at = OUT ? static_cast<int64_t>(seg.seq) * a.H + h
                            : static_cast<int64_t>(slot) * a.H + h;
     bh += at * (!OUT && a.image ? image_elems : a.R * a.N);
@@ -899,9 +915,10 @@ void linattn_walk_kernel(Walks walks) {
 }
 
 // -------------------------------------------------------------- combine ---
-// The state in front of every segment, in place: buf[slot, h] holds each
-// segment's own contribution (the last one's in walk order only with `fin`,
-// which takes the state behind it) and becomes the state entering it,
+// The state in front of every segment of the sequences that are cut, in
+// place: buf[slot, h] holds each segment's own contribution (the last one's
+// in walk order only with `fin`, which takes the state behind it) and becomes
+// the state entering it,
 // E' = a^len E + own.  A thread carries four state elements through the
 // sequence's segments; sixteen loads run ahead of the chain.  Memory bounds
 // it (16k tokens in 4 sequences, dk 128 dv 256, both directions: 140 MB in 32
@@ -933,7 +950,7 @@ __global__ __launch_bounds__(256) void linattn_combine_kernel(Cut cut, int H, in
   const int nblk = (elems / 4 + 255) / 256;
   const int blk = id % nblk;
   const int h = (id / nblk) % H;
-  const int seq = id / (nblk * H);
+  int seq = id / (nblk * H);  // packed: the how manyeth of the cut sequences
   int first, n, len;
   if (cut.cu == nullptr) {
     n = cut.per_seq;
@@ -943,14 +960,25 @@ __global__ __launch_bounds__(256) void linattn_combine_kernel(Cut cut, int H, in
     const int lane = threadIdx.x & 63;
     const uint32_t slots = static_cast<uint32_t>(cut.slots);
     uint32_t before = 0, f = 0, cnt = 0;
-    for (int base = 0; base <= seq; base += 64) {
+    int rank = seq, l = -1, base = 0;  // rank: cut sequences still to pass
+    for (; base < cut.nseq; base += 64) {
       f = before + lane_slots(cut, base, lane, &cnt);
+      const uint64_t is_cut = __ballot(cnt > 0);
+      const int upto = __popcll(is_cut & ((uint64_t(1) << lane) - 1));
+      const uint64_t hit = __ballot(cnt > 0 && upto == rank);
+      if (hit != 0) {
+        l = __ffsll(static_cast<unsigned long long>(hit)) - 1;
+        break;
+      }
+      rank -= __popcll(is_cut);
       before = min(__shfl(f + cnt, 63, 64), slots);
     }
-    f = min(__shfl(f, seq & 63, 64), slots);
+    if (l < 0) return;  // fewer are cut than there is room for
+    seq = __builtin_amdgcn_readfirstlane(base + l);
+    f = min(__shfl(f, l, 64), slots);
     // (bounds that overlap need more slots than there are: none beyond them)
     first = static_cast<int>(f);
-    n = static_cast<int>(min(__shfl(cnt, seq & 63, 64), slots - f));
+    n = static_cast<int>(min(__shfl(cnt, l, 64), slots - f));
     int st, en;
     seq_range(cut, seq, &st, &en);
     len = en - st;
@@ -1117,7 +1145,9 @@ size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 struct Plan {
   int span;        // tokens per segment
   int per_seq;     // dense: segments per sequence
-  int64_t slots;   // segment slots (an upper bound when packed)
+  int64_t slots;   // segment slots; packed: an upper bound, of the cut sequences
+  int64_t cuts;    // sequences that are cut (packed: an upper bound)
+  int64_t walks;   // slots of an output launch: the cut sequences' and the whole ones
   bool split;
 };
 
@@ -1142,22 +1172,44 @@ Plan plan_walk(const LinAttn& p, bool bwd) {
     L = std::min<int64_t>(nch, p.seg_req);
   } else if (p.seg_req == 0 && nch > 6) {
     // (six chunks or fewer are walked faster than two more launches take)
+    // Workgroups of an output launch that is not cut.
+    const int64_t whole =
+        !bwd ? chains : walks_join(p) ? 3 * chains : std::min(2 * heads, chains);
     if (p.varlen) {
-      // Segments for two workgroups a CU (512), in whole rounds: each chain
-      // ends in a segment that is half full on average, which may take up
-      // to a quarter of a round (65k tokens of 16 heads in 7 sequences: 36
-      // chunks 431 us, 24: 425, 32: 473, 12: 448; backward of 16k in 16: 11
-      // chunks 300, 24: 343).
-      const int64_t all = std::max<int64_t>(512, (2 * chains + 511) / 512 * 512);
-      const int64_t room = all - chains / 2;
-      L = (units + room - 1) / room;
+      // The longest of n sequences is likely to have about ln n + 0.58 times
+      // the mean's tokens (bounds drawn at random).  A longer one may be there
+      // all the same, a prompt among single tokens, so a batch of any size has
+      // a length that it is cut at; what is shorter costs nothing but the two
+      // launches.
+      const double apart = std::log(static_cast<double>(p.nseq)) + 0.58;
+      const bool few = nch * apart <= 6.0 * p.nseq;  // six chunks or fewer, most likely
+      if (few && nch <= 12) {
+        // (7 sequences of 64 tokens at 16 heads: 17 us, cut 29)
+        L = nch;
+      } else if (whole >= 256 * apart) {
+        // Whole sequences fill the machine, and most likely the longest ends
+        // before the others do; one that would take as long as all work
+        // together (a CU of its own walks a chunk in half the time) is cut.
+        // 65k tokens of 16 heads in 256: not cut 403 us, L 64 419, 8 565; in
+        // 1024: 712, 759, 1049; backward in 32: 885, 192 883, 16 996.
+        L = std::max<int64_t>(6, (nch * whole + 256 * p.nseq - 1) / (256 * p.nseq));
+      } else if (chains > 256 || few) {
+        // An even share of two workgroups a CU (65k tokens of 16 heads in 64:
+        // L 32 463 us, 11 489, not cut 832; 16k of 2 heads in 256: 6 57, 1 77).
+        L = std::max<int64_t>(6, (units + 511) / 512);
+      } else {
+        // Segments for two workgroups a CU (512): each chain ends in a segment
+        // that is half full on average (65k tokens of 16 heads in 7 sequences:
+        // 36 chunks 431 us, 24: 425, 32: 473, 12: 448; backward of 16k in 16:
+        // 11 chunks 300, 24: 343).
+        const int64_t room = 512 - chains / 2;
+        L = (units + room - 1) / room;
+      }
     } else {
-      // Workgroups of an output launch that is not cut.  Where they take most
-      // CUs, two more passes over the tokens cost more than the idle ones
-      // (dk 128 dv 128 backward, 240 of them: T1024 70 us, cut 95; T8192 525,
-      // 570; 192 of them: T1024 69, 83; T4096 262, 233).
-      const int64_t whole = !bwd ? chains : walks_join(p) ? 3 * chains
-                                                          : std::min(2 * heads, chains);
+      // Where workgroups that are not cut take most CUs, two more passes over
+      // the tokens cost more than the idle ones (dk 128 dv 128 backward, 240
+      // of them: T1024 70 us, cut 95; T8192 525, 570; 192 of them: T1024 69,
+      // 83; T4096 262, 233).
       if (whole < (nch <= 32 ? 192 : 200)) {
         // One workgroup a CU while walks are short, since every further segment
         // costs four passes over its state (T4096 H16: 4 chunks 47 us, 2: 55);
@@ -1177,10 +1229,16 @@ Plan plan_walk(const LinAttn& p, bool bwd) {
   r.split = L < nch;
   r.span = static_cast<int>(std::min<int64_t>(r.split ? L * C : int64_t(1) << 30, 1 << 30));
   r.per_seq = r.split ? static_cast<int>((nch + L - 1) / L) : 1;
-  if (p.varlen)
-    r.slots = r.split ? p.T / r.span + p.nseq : p.nseq;
-  else
-    r.slots = static_cast<int64_t>(p.nseq) * r.per_seq;
+  if (p.varlen) {
+    // a sequence that is cut has more than `span` tokens, and one segment
+    // more than whole spans
+    r.cuts = r.split ? std::min<int64_t>(p.nseq, p.T / (static_cast<int64_t>(r.span) + 1)) : 0;
+    r.slots = r.split ? p.T / r.span + r.cuts : 0;
+    r.walks = r.slots + p.nseq;
+  } else {
+    r.cuts = p.nseq;
+    r.slots = r.walks = static_cast<int64_t>(p.nseq) * r.per_seq;
+  }
   return r;
 }
 
@@ -1285,7 +1343,7 @@ hipError_t enter_states(const LinAttn& p, const Plan& pl, const Front* f, int n,
   if (e != hipSuccess) return e;
   StageScope scope(GDN_STAGE_FWD_COMBINE, s);
   const int elems = image ? image_elems(p) : p.dk * p.dv;
-  const int64_t grid = static_cast<int64_t>(p.nseq) * p.H * ((elems / 4 + 255) / 256) * n;
+  const int64_t grid = pl.cuts * p.H * ((elems / 4 + 255) / 256) * n;
   hipLaunchKernelGGL(linattn_combine_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s,
                      w.w[0].cut, p.H, p.dk, p.dv, image ? 1 : 0, la, c);
   return hipGetLastError();
@@ -1317,7 +1375,7 @@ bool linattn_grid_ok(const LinAttn& p) {
   const Plan pl = plan_walk(p, false), plb = plan_walk(p, true);
   const int64_t most = (int64_t(1) << 31) - 1;
   const int64_t blocks = (static_cast<int64_t>(image_elems(p)) / 4 + 255) / 256;
-  return std::max(pl.slots, plb.slots) * p.H * 6 <= most &&
+  return std::max(pl.walks, plb.walks) * p.H * 6 <= most &&
          2 * static_cast<int64_t>(p.nseq) * p.H * blocks <= most;
 }
 
@@ -1331,7 +1389,7 @@ hipError_t launch_linattn_fwd(const LinAttn& p, const void* q, const void* k, co
   one.n = 1;
   Walk& w = one.w[0];
   w.cut = make_cut(p, pl);
-  w.enter = s0;
+  w.init = s0;
   if (pl.split) {
     float* buf = static_cast<float*>(ws);
     const Front f{false, k, v, p.hq, p.H, s0, buf, s_final};
@@ -1349,8 +1407,8 @@ hipError_t launch_linattn_fwd(const LinAttn& p, const void* q, const void* k, co
   w.N = p.dv;
   w.log_decay = la;
   w.out = o;
-  w.behind = pl.split ? nullptr : s_final;
-  return launch_walks(p, one, pl.slots, true, GDN_STAGE_FWD_SCAN, s);
+  w.behind = s_final;
+  return launch_walks(p, one, pl.walks, true, GDN_STAGE_FWD_SCAN, s);
 }
 
 size_t linattn_bwd_workspace_bytes(const LinAttn& p) {
@@ -1362,7 +1420,7 @@ hipError_t launch_linattn_bwd(const LinAttn& p, const void* q, const void* k, co
                               const float* ds_final, void* dq, void* dk, void* dv, float* ds0,
                               void* ws, hipStream_t s) {
   const Plan pl = plan_walk(p, true);
-  const float *front = s0, *back = ds_final;
+  const float *front = nullptr, *back = nullptr;  // of every segment
   char* at = static_cast<char*>(ws);
   hipError_t e;
   if (pl.split) {
@@ -1396,9 +1454,11 @@ hipError_t launch_linattn_bwd(const LinAttn& p, const void* q, const void* k, co
   dq_.x = d_o;
   dq_.y = v;
   dq_.z = k;
+  dq_.init = s0;
   dq_.enter = front;
   dq_.out = shared ? static_cast<void*>(part_q) : dq;
   w.rev = 1;
+  w.init = ds_final;
   w.enter = back;
   Walk& dk_ = all.w[1] = w;
   dk_.x = v;
@@ -1416,15 +1476,15 @@ hipError_t launch_linattn_bwd(const LinAttn& p, const void* q, const void* k, co
   dv_.y = q;
   dv_.z = d_o;
   dv_.out = dv;
-  dv_.behind = pl.split ? nullptr : ds0;
+  dv_.behind = ds0;
   all.n = walks_join(p) ? 3 : 2;
-  e = launch_walks(p, all, pl.slots, true, GDN_STAGE_BWD_GRAD, s);
+  e = launch_walks(p, all, pl.walks, true, GDN_STAGE_BWD_GRAD, s);
   if (e != hipSuccess) return e;
   if (all.n == 2) {
     Walks one{};
     one.n = 1;
     one.w[0] = dv_;
-    e = launch_walks(p, one, pl.slots, true, GDN_STAGE_BWD_GRAD, s);
+    e = launch_walks(p, one, pl.walks, true, GDN_STAGE_BWD_GRAD, s);
     if (e != hipSuccess) return e;
   }
   if (!shared) return hipSuccess;

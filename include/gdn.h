@@ -420,7 +420,8 @@ gdn_status gdn_decode_step_product(const gdn_problem* p, int32_t nh, const void*
  *   p         : B, T, H, dk, dv, nseq, cu_seqlens, io_dtype and seg_chunks as
  *               in the chunked calls; gate must be GDN_GATE_NONE; chunk and
  *               gate_dtype are ignored (chunks take 64 tokens in bf16, 32 in
- *               fp32, and seg_chunks counts those).
+ *               fp32, and seg_chunks counts those).  Of packed sequences only
+ *               those longer than a segment are cut.
  *   hq        : heads of q and k; v head h reads q / k head h / (H / hq).
  *               hq in 1 .. H dividing H, else GDN_ERR_SHAPE.
  *   q, k      : [B, T, hq, dk];  v, o : [B, T, H, dv], io_dtype.

@@ -199,3 +199,30 @@ def test_binding_refuses_what_does_not_fit():
         gdn.group_norm_fwd(q)
     with pytest.raises(ValueError):
         gdn.group_norm_fwd(q[0])
+
+
+def state_slots(lib, which, p, hq):
+    """States for segments that a call's workspace has room for, of a problem
+    without shared heads and dv <= 128."""
+    n = need(getattr(lib, f"gdn_linear_attn_{which}_workspace"), p, hq)
+    assert n[0] == _lib.GDN_OK
+    return n[1] / (p.H * p.dk * p.dv * 4) / (1 if which == "fwd" else 2)
+
+
+@pytest.mark.parametrize("which", ["fwd", "bwd"])
+def test_packed_batches_of_short_sequences_need_little(lib, which):
+    # states are kept for the segments of sequences that are cut, none of six
+    # chunks or fewer where there are many: a sequence that is cut has one
+    # segment more than whole spans, at most twice the spans in all
+    for T, nseq, H in ((2000, 24, 32), (16384, 256, 16), (16384, 256, 2), (65536, 1024, 16),
+                       (4096, 24, 32), (8192, 24, 16), (900, 30, 2), (32768, 64, 16)):
+        p = prob(T=T, H=H, dv=128, nseq=nseq, cu_seqlens=A)
+        assert state_slots(lib, which, p, H) <= 2 * (T // (6 * 64)), (T, nseq, H)
+    # a handful of chunks in all: one walk
+    assert state_slots(lib, which, prob(T=448, H=16, dv=128, nseq=7, cu_seqlens=A), 16) == 0
+    # few long sequences are cut as before
+    p = prob(T=65536, H=16, dv=128, nseq=7, cu_seqlens=A)
+    assert state_slots(lib, which, p, 16) == 28 + 7
+    # segments asked for: each long sequence has its own, each short one none
+    p = prob(T=640, H=4, dv=128, nseq=100, cu_seqlens=A, seg_chunks=2)
+    assert state_slots(lib, which, p, 4) == 5 + 4
