@@ -982,9 +982,13 @@ gdn_status gdn_decode_step_product(const gdn_problem* p, int32_t nh, const void*
 
 namespace {
 
-// Checks of the linear-attention entry points; decode: one token of p->B
-// sequences, the packing ignored.
-gdn_status check_linattn(const gdn_problem* p, int32_t hq, bool decode, gdn::LinAttn* out) {
+enum class LinCall { fwd, bwd, step };
+
+// Checks of the linear-attention entry points; step: one token of p->B
+// sequences, the packing ignored.  Sizes are bounded before they are
+// multiplied, and every launch of the call is known to fit before the first.
+gdn_status check_linattn(const gdn_problem* p, int32_t hq, LinCall call, gdn::LinAttn* out) {
+  const bool decode = call == LinCall::step;
   if (p == nullptr) return GDN_FAIL(GDN_ERR_NULL);
   if (!dtype_ok(p->io_dtype)) return GDN_FAIL(GDN_ERR_DTYPE);
   if (p->gate != GDN_GATE_NONE) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
@@ -1006,10 +1010,7 @@ gdn_status check_linattn(const gdn_problem* p, int32_t hq, bool decode, gdn::Lin
   out->cu_seqlens = out->varlen ? p->cu_seqlens : nullptr;
   out->io = p->io_dtype;
   out->seg_req = decode ? 0 : p->seg_chunks;
-  if (decode) {
-    const int64_t blocks = static_cast<int64_t>(p->B) * p->H * ((p->dv + 63) / 64);
-    return blocks <= (int64_t(1) << 31) - 1 ? GDN_OK : GDN_FAIL(GDN_ERR_SHAPE);
-  }
+  if (decode) return gdn::linattn_step_fits(*out) ? GDN_OK : GDN_FAIL(GDN_ERR_SHAPE);
   if (p->T < 0 || p->nseq < 0) return GDN_FAIL(GDN_ERR_SHAPE);
   if (p->nseq > 0) {
     if (p->B != 1) return GDN_FAIL(GDN_ERR_SHAPE);
@@ -1019,8 +1020,9 @@ gdn_status check_linattn(const gdn_problem* p, int32_t hq, bool decode, gdn::Lin
     return GDN_FAIL(GDN_ERR_SHAPE);
   }
   if (p->T > (1 << 30) ||
-      static_cast<int64_t>(p->B) * p->T * p->H * 256 > (int64_t(1) << 46) ||
-      !gdn::linattn_grid_ok(*out))
+      static_cast<int64_t>(p->B) * p->T > (int64_t(1) << 38) / p->H ||
+      static_cast<int64_t>(out->nseq) * p->H > (int64_t(1) << 31) ||
+      !gdn::linattn_fits(*out, call == LinCall::bwd))
     return GDN_FAIL(GDN_ERR_SHAPE);
   return GDN_OK;
 }
@@ -1085,7 +1087,7 @@ gdn_status gdn_linear_attn_fwd_workspace(const gdn_problem* p, int32_t hq, size_
   try {
     if (bytes == nullptr) return GDN_FAIL(GDN_ERR_NULL);
     gdn::LinAttn pp;
-    GDN_TRY(check_linattn(p, hq, false, &pp));
+    GDN_TRY(check_linattn(p, hq, LinCall::fwd, &pp));
     *bytes = gdn::linattn_fwd_workspace_bytes(pp);
     return GDN_OK;
   } catch (...) {
@@ -1099,7 +1101,7 @@ gdn_status gdn_linear_attn_fwd(const gdn_problem* p, int32_t hq, const void* q, 
   GDN_ENTRY();
   try {
     gdn::LinAttn pp;
-    GDN_TRY(check_linattn(p, hq, false, &pp));
+    GDN_TRY(check_linattn(p, hq, LinCall::fwd, &pp));
     GDN_TRY(check_linattn_rows(pp, q, k, v, o, log_decay));
     GDN_TRY(opt(s0));
     GDN_TRY(opt(s_final));
@@ -1119,7 +1121,7 @@ gdn_status gdn_linear_attn_bwd_workspace(const gdn_problem* p, int32_t hq, size_
   try {
     if (bytes == nullptr) return GDN_FAIL(GDN_ERR_NULL);
     gdn::LinAttn pp;
-    GDN_TRY(check_linattn(p, hq, false, &pp));
+    GDN_TRY(check_linattn(p, hq, LinCall::bwd, &pp));
     *bytes = gdn::linattn_bwd_workspace_bytes(pp);
     return GDN_OK;
   } catch (...) {
@@ -1134,7 +1136,7 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem* p, int32_t hq, const void* q, 
   GDN_ENTRY();
   try {
     gdn::LinAttn pp;
-    GDN_TRY(check_linattn(p, hq, false, &pp));
+    GDN_TRY(check_linattn(p, hq, LinCall::bwd, &pp));
     GDN_TRY(check_linattn_rows(pp, q, k, v, d_o, log_decay));
     const int64_t tok = static_cast<int64_t>(pp.B) * pp.T;
     GDN_TRY(need(dq, tok * pp.hq * pp.dk));
@@ -1160,7 +1162,7 @@ gdn_status gdn_linear_attn_decode_step(const gdn_problem* p, int32_t hq, const v
   GDN_ENTRY();
   try {
     gdn::LinAttn pp;
-    GDN_TRY(check_linattn(p, hq, true, &pp));
+    GDN_TRY(check_linattn(p, hq, LinCall::step, &pp));
     GDN_TRY(check_linattn_rows(pp, q, k, v, o, log_decay));
     GDN_TRY(need(state, static_cast<int64_t>(pp.B) * pp.H));
     if (g_fail_launch.load()) return launched(pp, hipErrorLaunchFailure);  // test hook

@@ -119,7 +119,9 @@ struct LinAttn {
   int io;                     // gdn_dtype
   int seg_req;                // gdn_problem::seg_chunks
 };
-bool linattn_grid_ok(const LinAttn& p);  // whether the launches fit the grid
+// whether every launch of a call fits the grid
+bool linattn_fits(const LinAttn& p, bool bwd);
+bool linattn_step_fits(const LinAttn& p);
 size_t linattn_fwd_workspace_bytes(const LinAttn& p);
 hipError_t launch_linattn_fwd(const LinAttn& p, const void* q, const void* k, const void* v,
                               const float* la, const float* s0, void* o, float* s_final,

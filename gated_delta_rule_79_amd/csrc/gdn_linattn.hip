@@ -1371,12 +1371,27 @@ void launch_decode_dk(const LinAttn& p, const void* q, const void* k, const void
 
 }  // namespace
 
-bool linattn_grid_ok(const LinAttn& p) {
-  const Plan pl = plan_walk(p, false), plb = plan_walk(p, true);
-  const int64_t most = (int64_t(1) << 31) - 1;
+// A launch takes fewer than 2^32 threads (HIP's limit).
+bool linattn_fits(const LinAttn& p, bool bwd) {
+  const Plan pl = plan_walk(p, bwd);
+  const int64_t most = (int64_t(1) << 32) - 1;
+  // n walks over `slots` slots with N columns and R state rows (narrower slabs
+  // are taken where there are few workgroups only)
+  auto walks = [&](int64_t slots, int R, int N, int n) {
+    return slots * p.H * ((N + 127) / 128) * n * (R > 128 && N > 64 ? 512 : 256);
+  };
   const int64_t blocks = (static_cast<int64_t>(image_elems(p)) / 4 + 255) / 256;
-  return std::max(pl.walks, plb.walks) * p.H * 6 <= most &&
-         2 * static_cast<int64_t>(p.nseq) * p.H * blocks <= most;
+  const int both = bwd ? 2 : 1;
+  if (pl.split && std::max(walks(pl.slots, p.dk, p.dv, both),
+                           pl.cuts * p.H * blocks * both * 256) > most)
+    return false;
+  if (!bwd) return walks(pl.walks, p.dk, p.dv, 1) <= most;
+  return std::max(walks(pl.walks, p.dv, p.dk, walks_join(p) ? 3 : 2),
+                  walks(pl.walks, p.dk, p.dv, 1)) <= most;
+}
+
+bool linattn_step_fits(const LinAttn& p) {
+  return static_cast<int64_t>(p.B) * p.H * ((p.dv + 63) / 64) * 256 <= (int64_t(1) << 32) - 1;
 }
 
 size_t linattn_fwd_workspace_bytes(const LinAttn& p) { return state_bytes(p, plan_walk(p, false)); }

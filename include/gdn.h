@@ -438,7 +438,9 @@ gdn_status gdn_decode_step_product(const gdn_problem* p, int32_t nh, const void*
  * A NaN or infinity in a token reaches the outputs of its own chunk and of
  * all later tokens of its sequence, never another sequence.  Deterministic.
  * Errors as gdn_chunk_fwd; GDN_ERR_UNSUPPORTED for another gate or for rows
- * of 2^25 bytes or more (all heads of one token). */
+ * of 2^25 bytes or more (all heads of one token); GDN_ERR_SHAPE where a
+ * launch would take 2^32 threads (256 for each segment, head and 128 columns,
+ * three times that in the backward; 2^20 sequences of 16 heads, for one). */
 gdn_status gdn_linear_attn_fwd_workspace(const gdn_problem* p, int32_t hq, size_t* bytes);
 gdn_status gdn_linear_attn_fwd(const gdn_problem* p, int32_t hq, const void* q, const void* k,
                                const void* v, const float* log_decay, const float* s0, void* o,

@@ -226,3 +226,34 @@ def test_packed_batches_of_short_sequences_need_little(lib, which):
     # segments asked for: each long sequence has its own, each short one none
     p = prob(T=640, H=4, dv=128, nseq=100, cu_seqlens=A, seg_chunks=2)
     assert state_slots(lib, which, p, 4) == 5 + 4
+
+
+SMALL = dict(dk=16, dv=16, H=16, T=1)
+
+
+@pytest.mark.parametrize("which,kw,hq", [
+    # a launch takes fewer than 2^32 threads: 2^20 sequences of 16 heads are
+    # one workgroup too many, the backward's three walks reach it earlier
+    ("step", dict(SMALL, B=1 << 20), 16), ("fwd", dict(SMALL, B=1 << 20), 16),
+    ("bwd", dict(SMALL, B=(1 << 20) // 3 + 1), 16),
+    ("fwd", dict(SMALL, nseq=1 << 20, T=1 << 20, cu_seqlens=A), 16),
+    # the wide walks of dv = 256 take 512 threads
+    ("bwd", dict(SMALL, dk=128, dv=256, B=1 << 18), 16),
+    # products of sizes that pass 64 bits
+    ("fwd", dict(SMALL, B=1 << 28, T=1 << 28, H=1), 1),
+    ("bwd", dict(SMALL, B=1 << 30, T=1 << 30, H=16), 16),
+    ("fwd", dict(SMALL, nseq=(1 << 31) - 1, T=1 << 30, H=1 << 19, cu_seqlens=A), 1),
+    ("step", dict(SMALL, B=(1 << 31) - 1, H=1 << 19), 1),
+])
+def test_sizes_past_a_launch_are_refused(lib, which, kw, hq):
+    assert call(lib, which, prob(**kw), hq=hq) == _lib.GDN_ERR_SHAPE
+    if which != "step":
+        query = getattr(lib, f"gdn_linear_attn_{which}_workspace")
+        assert need(query, prob(**kw), hq)[0] == _lib.GDN_ERR_SHAPE
+
+
+@pytest.mark.parametrize("which,kw", [
+    ("step", dict(SMALL, B=(1 << 20) - 1)), ("fwd", dict(SMALL, B=(1 << 20) - 1)),
+    ("bwd", dict(SMALL, B=(1 << 20) // 3)), ("bwd", dict(SMALL, dk=128, dv=256, B=(1 << 18) - 1))])
+def test_the_largest_launches_are_not(lib, which, kw):
+    assert call(lib, which, prob(**kw), hq=16) == _lib.GDN_ERR_HIP  # the launch hook's
