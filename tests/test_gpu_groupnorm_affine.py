@@ -1,0 +1,100 @@
+"""Group norm with a weight and no bias (the gated RMS form of a block) or a
+bias and no weight, and rows far from zero, against the fp64 oracle (bounds as
+in test_gpu_groupnorm)."""
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_79_amd as gdn
+import oracle
+from gpu_util import np64
+from test_gpu_groupnorm import BF16, F32, check, dev, f64, kappa, make
+
+U = 2.0 ** -24
+
+
+def magnitudes(p, act_slope, eps, center):
+    """|n| with its condition, the factor of act and its slope, 1/std, kappa."""
+    x = p["x"]
+    c = x - x.mean(-1, keepdims=True) if center else x
+    r = 1 / np.sqrt((c * c).mean(-1, keepdims=True) + eps)
+    w = 1.0 if p["weight"] is None else np.abs(p["weight"])
+    b = 0.0 if p["bias"] is None else np.abs(p["bias"])
+    n = np.abs(c * r) * w + b + w
+    f = 1 + n if p["gate"] is None else 1 + np.abs(p["gate"])
+    return n + 0 * x, f, r, w + 0 * x, np.abs(c * r), kappa(x, eps, center)
+
+
+def check_all(d, dtype, act, center, eps=1e-5):
+    p = {k: f64(t) for k, t in d.items()}
+    kw = dict(weight=p["weight"], bias=p["bias"], gate=p["gate"], kind=act, eps=eps, center=center)
+    g = {k: dev(t) for k, t in d.items()}
+    gkw = dict(weight=g["weight"], bias=g["bias"], gate=g["gate"], act=act, eps=eps, center=center)
+    y = gdn.group_norm_fwd(g["x"], **gkw)
+    dx, dz, dw, db = gdn.group_norm_bwd(g["x"], g["dy"], **gkw)
+    torch.cuda.synchronize()
+    n, f, r, w, xh, k = magnitudes(p, act, eps, center)
+    top = lambda t: t.max(-1, keepdims=True)  # noqa: E731
+    ref = oracle.group_norm_bwd(p["x"], p["dy"], **kw)
+    dyf = np.abs(p["dy"]) * f
+    check("y", y, oracle.group_norm_fwd(p["x"], **kw), top(n * f) * k, dtype)
+    lead = top(dyf * w * (n if p["gate"] is None else 1.0)) * k
+    check("dx", dx, ref[0], 4 * r * lead * top(1 + n), dtype)
+    for got, a in ((dz, "gate"), (dw, "weight"), (db, "bias")):
+        assert (got is None) == (p[a] is None), a
+    if dz is not None:
+        check("dz", dz, ref[1], top(np.abs(p["dy"]) * n * f) * k, dtype)
+    rows = int(np.prod(p["x"].shape[:3]))
+    for name, got, rr, term in (("dw", dw, ref[2], dyf * (1 + n) * (1 + xh)),
+                                ("db", db, ref[3], dyf * (1 + n))):
+        if got is None:
+            continue
+        over = (0, 1) if rr.ndim == 2 else (0, 1, 2)
+        mag = (top(term) * k + 0 * p["x"]).sum(over)
+        assert np.all(np.abs(np64(got) - rr) <= (2.0 ** -17 + rows * U) * mag), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("affine", ["group", "shared"])
+@pytest.mark.parametrize("only", ["weight", "bias"])
+def test_weight_or_bias_alone(gpu_lib, only, affine, gate, dtype):
+    for center in (False, True):
+        for H, d in ((3, 64), (8, 80), (2, 256)):
+            x = make(1, 41, H, d, dtype, affine, gate)
+            x["bias" if only == "weight" else "weight"] = None
+            check_all(x, dtype, "silu", center)
+
+
+FAR = [(F32, 100.0, 1e-5), (F32, 1000.0, 1e-8), (F32, -4000.0, 1e-5), (BF16, 30.0, 1e-5),
+       (BF16, -200.0, 1e-8)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,mean,eps", FAR)
+@pytest.mark.parametrize("gate", [False, True])
+def test_rows_far_from_zero(gpu_lib, gate, dtype, mean, eps):
+    for H, d in ((3, 64), (2, 112), (1, 256)):
+        check_all(make(1, 29, H, d, dtype, "group", gate, mean=mean), dtype, "silu", True, eps)
+
+
+@pytest.mark.parametrize("mean,eps", [(1000.0, 1e-8), (-4000.0, 1e-5)])
+def test_the_bound_tells_the_variance_apart(mean, eps):
+    # in 32 bits, the variance around the mean holds the bound and the mean
+    # square less the squared mean does not
+    d = make(1, 29, 2, 112, F32, "none", False, mean=mean)
+    x = d["x"].numpy()
+    p = {k: f64(t) for k, t in d.items()}
+    n, f, _, _, _, k = magnitudes(p, "none", eps, True)
+    ref = oracle.group_norm_fwd(p["x"], kind="none", eps=eps)
+    mag = (n * f).max(-1, keepdims=True) * k
+    m = x.mean(-1, keepdims=True, dtype=np.float32)
+    c = x - m
+    good = c / np.sqrt((c * c).mean(-1, keepdims=True, dtype=np.float32) + np.float32(eps))
+    check("around the mean", torch.from_numpy(good), ref, mag, F32)
+    var = (x * x).mean(-1, keepdims=True, dtype=np.float32) - m * m
+    bad = c / np.sqrt(np.maximum(var, 0) + np.float32(eps))
+    with pytest.raises(AssertionError):
+        check("mean square", torch.from_numpy(bad), ref, mag, F32)
