@@ -385,7 +385,9 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
   if (seg.seq < 0) return;
   const bool last = rev ? seg.j == 0 : seg.j == seg.n - 1;  // in walk order
   if (!OUT && last && !a.ends) return;
-  const bool whole = seg.n == 1;
+  // (lane 0's, as everything here is the wave's: the state's descriptor is then
+  // known to be one for all lanes)
+  const bool whole = __builtin_amdgcn_readfirstlane(seg.n) == 1;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -535,7 +537,8 @@ __device__ __forceinline__ void walk_segment(const Walk& a, int slab, int h, int
     const float* const enter = whole ? a.init : a.enter;
     const bool image = !whole && a.image;
     const uint32_t elems = image ? image_elems : a.R * a.N;
-    const int64_t at = (static_cast<int64_t>(whole ? seg.seq : slot) * a.H + h) * elems;
+    const int place = __builtin_amdgcn_readfirstlane(whole ? seg.seq : slot);
+    const int64_t at = (static_cast<int64_t>(place) * a.H + h) * elems;
     const __amdgpu_buffer_rsrc_t rs =
         make_rsrc(enter + (enter == nullptr ? 0 : at), enter == nullptr ? 0 : elems * 4);
 #pragma unroll
