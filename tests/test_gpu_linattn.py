@@ -6,10 +6,12 @@ operand and state replaced by its absolute value (the sum of the magnitudes
 of all terms of the exact expression).  u = 2^-24 is an fp32 half step, each
 accumulated term passes at most n additions (n: rows of the contraction plus
 tokens plus a few), so fp32 arithmetic is off by at most n u A.  With bf16
-rows the copy of the state and of x y^T that multiplies them is rounded once
-(half a step, 2^-9 of its value and so 2^-9 A in all), the carried state keeps
-2^-27 of each term from its three-part products, and the result is rounded
-once more (2^-9 |out|).  2^-8 is used for both, the finfo half step."""
+rows the copy of the state that multiplies them, x y^T and the weighted rows
+that enter the state go in two operand parts each (2^-17 of a value left), the
+state that is handed out keeps the fp32 value of each term in three, and the
+result is rounded once (half a step, 2^-8 |out|).  The bounds here are wider:
+2^-8 A besides, as one rounding of the state's copy and of x y^T would need;
+test_gpu_linattn_rounding holds the outputs to one rounding of their own."""
 
 import numpy as np
 import pytest
@@ -395,7 +397,7 @@ def test_offsets_past_four_gigabytes(gpu_lib):
         torch.cuda.synchronize()
         # Not cut, both walks are the same arithmetic.  Cut, the state that
         # multiplies q holds two operand parts of each product where the
-        # other holds four: 2^-18 apart, its rounding to bf16 may fall on
+        # other holds three: 2^-17 apart, an output's rounding may fall on
         # either side, so only the bounds above hold.
         if seg == -1:
             assert torch.equal(o[:, cu[1]:], o1) and torch.equal(sf[1], s1[0])
