@@ -98,3 +98,30 @@ def test_the_bound_tells_the_variance_apart(mean, eps):
     bad = c / np.sqrt(np.maximum(var, 0) + np.float32(eps))
     with pytest.raises(AssertionError):
         check("mean square", torch.from_numpy(bad), ref, mag, F32)
+
+
+@pytest.mark.gpu
+def test_offsets_past_four_gigabytes(gpu_lib):
+    # the last rows lie behind 2^32 bytes and 2^31 elements
+    T, H, d, last = 70_000, 128, 256, 40
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, z, dy = (torch.zeros(1, T, H, d, dtype=BF16, device="cuda") for _ in range(3))
+    for t in (x, z, dy):
+        t[:, -last:] = torch.randn(last, H, d, generator=g, device="cuda").to(BF16)
+    w, b = (torch.randn(H, d, generator=g, device="cuda") for _ in range(2))
+    end = [t[:, -last:].contiguous() for t in (x, z, dy)]
+    y = gdn.group_norm_fwd(x, w, b, z)
+    y1 = gdn.group_norm_fwd(end[0], w, b, end[1])
+    torch.cuda.synchronize()
+    assert torch.equal(y[:, -last:], y1)
+    del y
+    dx, dz, dw, db = gdn.group_norm_bwd(x, dy, w, b, z)
+    one = gdn.group_norm_bwd(end[0], end[2], w, b, end[1])
+    torch.cuda.synchronize()
+    assert torch.equal(dx[:, -last:], one[0]) and torch.equal(dz[:, -last:], one[1])
+    # the other rows' dy are zero; their sums run in another order of the same
+    # `last` terms (at most `last` additions of 2^-24 each)
+    xh = torch.nn.functional.normalize(end[0].double() - end[0].double().mean(-1, True), dim=-1)
+    dn = (end[2].double() * end[1].double() * torch.sigmoid(end[1].double())).abs()
+    for a, c, mag in ((dw, one[2], dn * xh.abs() * d ** 0.5), (db, one[3], dn)):
+        assert bool(((a - c).abs().double() <= 2 * last * U * 1.01 * mag.sum((0, 1))).all())
