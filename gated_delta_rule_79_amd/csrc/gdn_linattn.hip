@@ -29,10 +29,10 @@
 // segments' own states (no outputs), one chains them, one walks the outputs
 // from the chained states (plan_walk).  The whole needs 4 dk dv flops a token
 // and head for 4 rows of bytes (bf16 128 x 128: 64 flops a byte), so memory
-// bounds large calls: 65k packed tokens of 16 heads take 406 us for 1.09 GB
-// that must move (2.7 TB/s; 1.8 GB with k and v read twice and the states,
-// 4.4 TB/s).  Small ones are bound by the chain: a workgroup's chunk has
-// three barriers and takes 2.8 to 4.6 us alone on its CU.
+// bounds large calls: 65k packed tokens of 16 heads take 414 us for 1.09 GB
+// that must move (2.6 TB/s; 1.7 GB with k and v read twice and the states,
+// 4.2 TB/s).  Small ones are bound by the chain: a workgroup's chunk has
+// three barriers and takes 3.1 to 4.7 us alone on its CU.
 
 #include <algorithm>
 #include <cmath>
@@ -354,10 +354,10 @@ struct WalkTiles {
 // z^T (x y^T)^T, stored at once; the state update last, while the stores
 // drain.
 // Alone on a CU a workgroup (four waves, one a SIMD) waits most of a chunk
-// (matrix cores 15 % busy); two share it where there is work for them (25 %,
-// 65k tokens), which memory then bounds: 256 us for 1.1 GB.  Eight waves
-// instead of four took 315 us there, one copy of the code for both directions
-// 283.
+// (matrix cores 17 % busy); two share it where there is work for them (32 %,
+// 65k tokens), which memory then bounds: 267 us for 1.1 GB.  (With one part of
+// the state's copy 256; eight waves instead of four took 315 then, one copy of
+// the code for both directions 283.)
 // The update's weights go onto z in fp32, and the product is split into
 // bf16 parts, so the carried state keeps the fp32 accuracy of its storage.
 // Operand reads run one step ahead of the products that take them
@@ -1187,35 +1187,35 @@ Plan plan_walk(const LinAttn& p, bool bwd) {
       const double apart = std::log(static_cast<double>(p.nseq)) + 0.58;
       const bool few = nch * apart <= 6.0 * p.nseq;  // six chunks or fewer, most likely
       if (few && nch <= 12) {
-        // (7 sequences of 64 tokens at 16 heads: 17 us, cut 29)
+        // (7 sequences of 64 tokens at 16 heads: 16 us, cut 27)
         L = nch;
       } else if (whole >= 256 * apart) {
         // Whole sequences fill the machine, and most likely the longest ends
         // before the others do; one that would take as long as all work
         // together (a CU of its own walks a chunk in half the time) is cut.
-        // 65k tokens of 16 heads in 256: not cut 403 us, L 64 419, 8 565; in
-        // 1024: 712, 759, 1049; backward in 32: 885, 192 883, 16 996.
+        // 65k tokens of 16 heads in 256: not cut 389 us, L 64 400, 8 529; in
+        // 1024: 617, 667, 951; backward in 32: 880, L 192 875, 16 976.
         L = std::max<int64_t>(6, (nch * whole + 256 * p.nseq - 1) / (256 * p.nseq));
       } else if (chains > 256 || few) {
         // An even share of two workgroups a CU (65k tokens of 16 heads in 64:
-        // L 32 463 us, 11 489, not cut 832; 16k of 2 heads in 256: 6 57, 1 77).
+        // L 32 446 us, 12 476, not cut 826; 16k of 2 heads in 256: 6 55, 4 60).
         L = std::max<int64_t>(6, (units + 511) / 512);
       } else {
         // Segments for two workgroups a CU (512): each chain ends in a segment
         // that is half full on average (65k tokens of 16 heads in 7 sequences:
-        // 36 chunks 431 us, 24: 425, 32: 473, 12: 448; backward of 16k in 16:
-        // 11 chunks 300, 24: 343).
+        // 36 chunks 445 us, 24: 433, 48: 468, 12: 453, 96: 783; backward of
+        // 16k in 16: 11 chunks 290, 24: 301, 4: 320).
         const int64_t room = 512 - chains / 2;
         L = (units + room - 1) / room;
       }
     } else {
       // Where workgroups that are not cut take most CUs, two more passes over
-      // the tokens cost more than the idle ones (dk 128 dv 128 backward, 240
-      // of them: T1024 70 us, cut 95; T8192 525, 570; 192 of them: T1024 69,
-      // 83; T4096 262, 233).
+      // the tokens cost more than the idle ones (dk 128 dv 128 backward, us
+      // not cut / cut, 198 of them: T1024 73 / 98, T2048 141 / 158, T8192 550
+      // / 562; 192: T1024 73 / 81, T2048 142 / 140, T4096 280 / 245).
       if (whole < (nch <= 32 ? 192 : 200)) {
         // One workgroup a CU while walks are short, since every further segment
-        // costs four passes over its state (T4096 H16: 4 chunks 47 us, 2: 55);
+        // costs four passes over its state (T4096 H16: 4 chunks 43 us, 2: 51);
         // two where they are long.
         const int64_t target = units < 48 * 256 ? 256 : 512;
         const int64_t per_seq = std::max<int64_t>(1, target / chains);
@@ -1223,8 +1223,8 @@ Plan plan_walk(const LinAttn& p, bool bwd) {
       }
     }
     // The states are chained a segment after another: at least
-    // sqrt(chunks / 8) chunks each (T16384 H2: 2 chunks 73 us, 6: 57;
-    // T65536 H1: 4: 126, 12: 102).
+    // sqrt(chunks / 8) chunks each (T16384 H2: 2 chunks 70 us, 6: 47;
+    // T65536 H1: 4: 126, 12: 85).
     while (8 * L * L < (p.varlen ? nch / p.nseq : nch)) ++L;
     L = std::min(L, nch);
   }
@@ -1260,12 +1260,12 @@ void launch_walk_t(const Walks& w, int64_t slots, hipStream_t s) {
 template <typename IO, int NKB, bool OUT, bool BOTH>
 void launch_walk_n(const Walks& w, int64_t slots, hipStream_t s) {
   const int N = w.w[0].N;
-  // A workgroup's chunk takes less time the fewer columns it has (dk 128: 4.6
-  // us for 128, 3.2 for 64, 2.8 for 32), so slabs are as narrow as leave every
-  // workgroup a CU of its own (T256 H16: 128 columns 25.8 us, 64: 18.9, 32:
-  // 17.5).  Past that the x and y rows that all slabs read, and their x y^T,
-  // cost more (B8 T2048 H8 backward, 192 workgroups: 128 columns 134 us, 64:
-  // 143; 96 of them: 129, 103).
+  // A workgroup's chunk takes less time the fewer columns it has (dk 128: 4.7
+  // us for 128, 3.3 for 64, 3.1 for 32), so slabs are as narrow as leave every
+  // workgroup a CU of its own (T256 H16: 128 columns 25.3 us, 64: 18.2, 32:
+  // 17.0).  Past that the x and y rows that all slabs read, and their x y^T,
+  // cost more (B8 T2048 H8 backward, not cut, 192 workgroups of 128 columns:
+  // 142 us, 64: 139, 32: 216; 96 of them: 141, 108, 121).
   auto fits = [&](int np) {
     return slots * w.w[0].H * ((N + np - 1) / np) * w.n <= 256;
   };
