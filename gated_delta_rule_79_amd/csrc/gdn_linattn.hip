@@ -1195,7 +1195,8 @@ Plan plan_walk(const LinAttn& p, bool bwd) {
         // together (a CU of its own walks a chunk in half the time) is cut.
         // 65k tokens of 16 heads in 256: not cut 389 us, L 64 400, 8 529; in
         // 1024: 617, 667, 951; backward in 32: 880, L 192 875, 16 976.
-        L = std::max<int64_t>(6, (nch * whole + 256 * p.nseq - 1) / (256 * p.nseq));
+        const int64_t share = int64_t(256) * p.nseq;
+        L = std::max<int64_t>(6, (nch * whole + share - 1) / share);
       } else if (chains > 256 || few) {
         // An even share of two workgroups a CU (65k tokens of 16 heads in 64:
         // L 32 446 us, 12 476, not cut 826; 16k of 2 heads in 256: 6 55, 4 60).

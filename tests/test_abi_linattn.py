@@ -257,3 +257,15 @@ def test_sizes_past_a_launch_are_refused(lib, which, kw, hq):
     ("bwd", dict(SMALL, B=(1 << 20) // 3)), ("bwd", dict(SMALL, dk=128, dv=256, B=(1 << 18) - 1))])
 def test_the_largest_launches_are_not(lib, which, kw):
     assert call(lib, which, prob(**kw), hq=16) == _lib.GDN_ERR_HIP  # the launch hook's
+
+
+@pytest.mark.parametrize("which", ["fwd", "bwd"])
+@pytest.mark.parametrize("nseq", [1 << 22, (1 << 23) + 1, 1 << 24, 1 << 25, (1 << 31) - 1])
+def test_more_sequences_than_tokens(lib, which, nseq):
+    # (the plan's own products of the number of sequences stay in 64 bits; a
+    # sequence needs a workgroup even if it is empty, so past 2^24 there are
+    # too many, in the backward past a third of that)
+    p = prob(T=1000, H=1, dk=16, dv=16, nseq=nseq, cu_seqlens=A)
+    status, _ = need(getattr(lib, f"gdn_linear_attn_{which}_workspace"), p, 1)
+    fits = nseq * (3 if which == "bwd" else 1) < 1 << 24
+    assert status == (_lib.GDN_OK if fits else _lib.GDN_ERR_SHAPE)
