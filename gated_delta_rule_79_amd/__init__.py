@@ -752,3 +752,229 @@ def group_norm_bwd(x, dy, weight=None, bias=None, gate=None, act: str = "silu",
             eps, _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(dy), _ptr(dx), _ptr(dz),
             _ptr(dw), _ptr(db), _ptr(ws), nbytes)
     return dx, dz, dw, db
+
+
+# ------------------------- selective scan, short convolution, draft acceptance ---
+
+def _packed(cu_seqlens, x):
+    """Packed sequences of a call (0: dense), their bounds checked."""
+    if cu_seqlens is None:
+        return 0
+    _check_cu(cu_seqlens, x)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must hold the bounds of at least one sequence")
+    return cu_seqlens.numel() - 1
+
+
+def _scan_problem(x, dt, a, b, c, d, dt_bias, z, cu_seqlens, seg_chunks, lead):
+    """The problem of a selective-scan call, its rows of b and c, and the shape
+    of its states; `lead`: dimensions in front of the heads."""
+    xs, dtype, device = x.shape, x.dtype, x.device
+    if len(xs) != lead + 2 or b.dim() != lead + 2 or a.dim() != 3:
+        raise ValueError(f"x and b must have {lead + 2} dimensions, a 3")
+    if not x.is_cuda:
+        raise ValueError("libgdn takes GPU tensors")
+    H, dv = xs[lead:]
+    hb, dk = b.shape[lead:]
+    _want(dt, "dt", xs, dtype, device)
+    _want(z, "z", xs, dtype, device)
+    _want(b, "b", (*xs[:lead], hb, dk), dtype, device)
+    _want(c, "c", b.shape, dtype, device)
+    _want(a, "a", (H, dk, dv), torch.float32, device)
+    _want(d, "d", (H, dv), torch.float32, device)
+    _want(dt_bias, "dt_bias", (H, dv), torch.float32, device)
+    packed = _packed(cu_seqlens, x)
+    p = _lib.GdnProblem(xs[0], xs[1] if lead == 2 else 1, H, dk, dv, 0, packed, _ptr(cu_seqlens),
+                        _dtype_code(x), _lib.GDN_F32, _lib.GDN_GATE_NONE, int(seg_chunks))
+    return p, hb, (packed or xs[0], H, dk, dv)
+
+
+def selective_scan_fwd(x, dt, a, b, c, d=None, dt_bias=None, z=None, s0=None,
+                       softplus: bool = True, cu_seqlens=None, output_final_state: bool = True,
+                       workspace: Optional[torch.Tensor] = None, seg_chunks: int = 0,
+                       y=None, s_final=None):
+    """Selective state space scan over whole sequences (gdn_selective_scan_fwd):
+    delta = softplus(dt + dt_bias), S_t[n,j] = exp(delta_t[j] a[n,j]) S_{t-1}[n,j]
+    + delta_t[j] x_t[j] b_t[n], y_t[j] = (sum_n c_t[n] S_t[n,j] + d[j] x_t[j]) *
+    silu(z_t[j]).  x, dt, z [B,T,H,dv]; b, c [B,T,Hb,dk] with Hb dividing H
+    (head h reads row h // (H // Hb)); a [H,dk,dv], d, dt_bias [H,dv] fp32; s0
+    [nseq,H,dk,dv] fp32 or None; cu_seqlens packs sequences (B = 1).  y /
+    s_final: optional preallocated outputs.  Returns (y, s_final or None)."""
+    lib = _lib.load()
+    p, hb, states = _scan_problem(x, dt, a, b, c, d, dt_bias, z, cu_seqlens, seg_chunks, 2)
+    _want(s0, "s0", states, torch.float32, x.device)
+    y = _result(y, "y", x)
+    sf = _states(s_final, "s_final", states, x.device, s0) if output_final_state else None
+    ws, nbytes = _workspace(workspace, _bytes(lib.gdn_selective_scan_fwd_workspace, p, hb),
+                            x.device)
+    _launch(lib.gdn_selective_scan_fwd, x.device, ctypes.byref(p), hb, int(softplus), _ptr(x),
+            _ptr(dt), _ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(dt_bias), _ptr(z), _ptr(s0),
+            _ptr(y), _ptr(sf), _ptr(ws), nbytes)
+    return y, sf
+
+
+def selective_scan_bwd(x, dt, a, b, c, dy, d=None, dt_bias=None, z=None, s0=None, ds_final=None,
+                       softplus: bool = True, cu_seqlens=None,
+                       workspace: Optional[torch.Tensor] = None, seg_chunks: int = 0):
+    """Backward of :func:`selective_scan_fwd` (gdn_selective_scan_bwd):
+    gradients of <dy, y> + <ds_final, s_final>.  Returns (dx, ddt, da, db, dc,
+    dd, ddt_bias, dz, ds0); the last four are None where their input is."""
+    lib = _lib.load()
+    p, hb, states = _scan_problem(x, dt, a, b, c, d, dt_bias, z, cu_seqlens, seg_chunks, 2)
+    _want(s0, "s0", states, torch.float32, x.device)
+    _want(ds_final, "ds_final", states, torch.float32, x.device)
+    if dy is None:
+        raise ValueError("dy must be given")
+    _want(dy, "dy", x.shape, x.dtype, x.device)
+    dx, ddt, da, db, dc = (torch.empty_like(t) for t in (x, dt, a, b, c))
+    dd, dbias, dz, ds0 = (None if t is None else torch.empty_like(t) for t in (d, dt_bias, z, s0))
+    ws, nbytes = _workspace(workspace, _bytes(lib.gdn_selective_scan_bwd_workspace, p, hb),
+                            x.device)
+    _launch(lib.gdn_selective_scan_bwd, x.device, ctypes.byref(p), hb, int(softplus), _ptr(x),
+            _ptr(dt), _ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(dt_bias), _ptr(z), _ptr(s0),
+            _ptr(dy), _ptr(ds_final), _ptr(dx), _ptr(ddt), _ptr(da), _ptr(db), _ptr(dc), _ptr(dd),
+            _ptr(dbias), _ptr(dz), _ptr(ds0), _ptr(ws), nbytes)
+    return dx, ddt, da, db, dc, dd, dbias, dz, ds0
+
+
+def selective_scan_step(x, dt, a, b, c, state, d=None, dt_bias=None, z=None,
+                        softplus: bool = True, y=None):
+    """One token per sequence of :func:`selective_scan_fwd`'s rule
+    (gdn_selective_scan_step); ``state`` [N,H,dk,dv] fp32 is updated in place.
+    x, dt, z [N,H,dv]; b, c [N,Hb,dk].  Returns y [N,H,dv]."""
+    lib = _lib.load()
+    p, hb, states = _scan_problem(x, dt, a, b, c, d, dt_bias, z, None, 0, 1)
+    if state is None:
+        raise ValueError("state must be given")
+    _want(state, "state", states, torch.float32, x.device)
+    y = _result(y, "y", x)
+    _launch(lib.gdn_selective_scan_step, x.device, ctypes.byref(p), hb, int(softplus), _ptr(x),
+            _ptr(dt), _ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(dt_bias), _ptr(z), _ptr(state),
+            _ptr(y))
+    return y
+
+
+def _conv_problem(x, taps, bias, act, cu_seqlens, lead):
+    """The problem of a short convolution, its width and activation, and the
+    shape of its histories."""
+    xs, device = x.shape, x.device
+    if len(xs) != lead + 2 or taps.dim() != 3:
+        raise ValueError(f"x must have {lead + 2} dimensions, taps 3")
+    if not x.is_cuda:
+        raise ValueError("libgdn takes GPU tensors")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    H, d = xs[lead:]
+    width = taps.shape[-1]
+    _want(taps, "taps", (H, d, width), torch.float32, device)
+    _want(bias, "bias", (H, d), torch.float32, device)
+    packed = _packed(cu_seqlens, x)
+    p = _lib.GdnProblem(xs[0], xs[1] if lead == 2 else 1, H, d, d, 0, packed, _ptr(cu_seqlens),
+                        _dtype_code(x))
+    return p, width, _ACTS[act], (packed or xs[0], max(width - 1, 0), H, d)
+
+
+def short_conv_fwd(x, taps, bias=None, s0=None, act: str = "silu", cu_seqlens=None,
+                   output_final_state: bool = True, y=None, s_final=None):
+    """Short causal depthwise convolution with a carried history
+    (gdn_short_conv_fwd): y_t = act(bias + sum_j taps[..., j] x_{t-j}).
+    x [B,T,H,d]; taps [H,d,W], bias [H,d] fp32; s0 [nseq,W-1,H,d] in x's
+    dtype: each sequence's last W - 1 inputs, oldest first, or None (zeros).
+    act: "none", "silu" or "sigmoid".  y / s_final: optional preallocated
+    outputs.  Returns (y, s_final or None)."""
+    lib = _lib.load()
+    p, width, code, hist = _conv_problem(x, taps, bias, act, cu_seqlens, 2)
+    _want(s0, "s0", hist, x.dtype, x.device)
+    y = _result(y, "y", x)
+    if not output_final_state:
+        s_final = None
+    elif s_final is None:
+        s_final = torch.empty(hist, dtype=x.dtype, device=x.device)
+    else:
+        _want(s_final, "s_final", hist, x.dtype, x.device)
+        if s0 is not None and s_final.data_ptr() == s0.data_ptr() and s0.numel():
+            raise ValueError("s_final must not be s0")
+    _launch(lib.gdn_short_conv_fwd, x.device, ctypes.byref(p), width, code, _ptr(x), _ptr(taps),
+            _ptr(bias), _ptr(s0), _ptr(y), _ptr(s_final))
+    return y, s_final
+
+
+def short_conv_bwd(x, taps, dy, bias=None, s0=None, ds_final=None, act: str = "silu",
+                   cu_seqlens=None, workspace: Optional[torch.Tensor] = None):
+    """Backward of :func:`short_conv_fwd` (gdn_short_conv_bwd): gradients of
+    <dy, y> + <ds_final, s_final>.  Returns (dx, dtaps, dbias, ds0); the last
+    two are None where their input is."""
+    lib = _lib.load()
+    p, width, code, hist = _conv_problem(x, taps, bias, act, cu_seqlens, 2)
+    _want(s0, "s0", hist, x.dtype, x.device)
+    _want(ds_final, "ds_final", hist, x.dtype, x.device)
+    if dy is None:
+        raise ValueError("dy must be given")
+    _want(dy, "dy", x.shape, x.dtype, x.device)
+    dx, dtaps = torch.empty_like(x), torch.empty_like(taps)
+    dbias, ds0 = (None if t is None else torch.empty_like(t) for t in (bias, s0))
+    ws, nbytes = _workspace(workspace, _bytes(lib.gdn_short_conv_bwd_workspace, p, width),
+                            x.device)
+    _launch(lib.gdn_short_conv_bwd, x.device, ctypes.byref(p), width, code, _ptr(x), _ptr(taps),
+            _ptr(bias), _ptr(s0), _ptr(dy), _ptr(ds_final), _ptr(dx), _ptr(dtaps), _ptr(dbias),
+            _ptr(ds0), _ptr(ws), nbytes)
+    return dx, dtaps, dbias, ds0
+
+
+def short_conv_step(x, taps, state, bias=None, act: str = "silu", y=None):
+    """One token per sequence of :func:`short_conv_fwd`'s rule
+    (gdn_short_conv_step); ``state`` [N,W-1,H,d] in x's dtype moves up by the
+    token in place.  x [N,H,d].  Returns y [N,H,d] (may be x itself)."""
+    lib = _lib.load()
+    p, width, code, hist = _conv_problem(x, taps, bias, act, None, 1)
+    if state is None:
+        raise ValueError("state must be given")
+    _want(state, "state", hist, x.dtype, x.device)
+    y = _result(y, "y", x)
+    _launch(lib.gdn_short_conv_step, x.device, ctypes.byref(p), width, code, _ptr(x), _ptr(taps),
+            _ptr(bias), _ptr(state), _ptr(y))
+    return y
+
+
+def draft_accept(tokens, target, draft, uniform, parent=None, cu_seqlens=None,
+                 workspace: Optional[torch.Tensor] = None, out=None):
+    """Acceptance of drafted tokens against the target's probabilities from
+    given uniform numbers (gdn_draft_accept), between :func:`tree_verify` and
+    :func:`tree_commit`.  tokens int32 [B,n] (or [nodes] with cu_seqlens);
+    target [B,n+1,V] (or [nodes + ntrees, V]), fp32 or bf16: row 0 of a tree
+    behind the committed tokens, row i + 1 behind node i; draft the same of the
+    draft model, or None where the drafts were certain; uniform [B,n+1] (or
+    [nodes + ntrees]) fp32 in [0, 1), the last of a tree for its next token;
+    parent as in tree_verify, None: chains.  out: optional preallocated
+    results.  Returns int32 (accepted node or -1, accepted nodes, next token),
+    each [ntrees]."""
+    lib = _lib.load()
+    device = tokens.device
+    if not tokens.is_cuda:
+        raise ValueError("libgdn takes GPU tensors")
+    packed = _packed(cu_seqlens, tokens)
+    if tokens.dim() != (1 if packed else 2) or target.dim() != (2 if packed else 3):
+        raise ValueError("tokens must be [B, n] and target [B, n + 1, V], or packed [nodes] and "
+                         "[nodes + ntrees, V]")
+    n, V = tokens.shape[-1], target.shape[-1]
+    rows = (n + packed,) if packed else (tokens.shape[0], n + 1)
+    trees = packed or tokens.shape[0]
+    _want(tokens, "tokens", tokens.shape, torch.int32, device)
+    _want(target, "target", (*rows, V), target.dtype, device)
+    _want(draft, "draft", target.shape, target.dtype, device)
+    _want(uniform, "uniform", rows, torch.float32, device)
+    _want(parent, "parent", tokens.shape, torch.int32, device)
+    # a tree without nodes is a chain without nodes
+    parents = _ptr(parent) if n else None
+    p = _lib.GdnProblem(1 if packed else trees, n, 1, 16, 16, 0, packed, _ptr(cu_seqlens),
+                        _dtype_code(target))
+    if out is None:
+        out = tuple(torch.empty(3, trees, dtype=torch.int32, device=device)) if trees % 4 == 0 \
+            else tuple(torch.empty(trees, dtype=torch.int32, device=device) for _ in range(3))
+    for t in out:
+        _want(t, "out", (trees,), torch.int32, device)
+    ws, nbytes = _workspace(
+        workspace, _bytes(lib.gdn_draft_accept_workspace, p, V, int(parents is not None)), device)
+    _launch(lib.gdn_draft_accept, device, ctypes.byref(p), V, parents, _ptr(tokens), _ptr(target),
+            _ptr(draft), _ptr(uniform), *(_ptr(t) for t in out), _ptr(ws), nbytes)
+    return tuple(out)

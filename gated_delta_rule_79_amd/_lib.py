@@ -38,6 +38,10 @@ EXPORTED = (
     "gdn_linear_attn_bwd_workspace", "gdn_linear_attn_bwd",
     "gdn_linear_attn_decode_step", "gdn_group_norm_fwd",
     "gdn_group_norm_bwd_workspace", "gdn_group_norm_bwd",
+    "gdn_selective_scan_fwd_workspace", "gdn_selective_scan_fwd",
+    "gdn_selective_scan_bwd_workspace", "gdn_selective_scan_bwd", "gdn_selective_scan_step",
+    "gdn_short_conv_fwd", "gdn_short_conv_bwd_workspace", "gdn_short_conv_bwd",
+    "gdn_short_conv_step", "gdn_draft_accept_workspace", "gdn_draft_accept",
 )
 STAGE_COUNT = 12
 STAGES = ("chunk_map", "fwd_prep", "fwd_scan", "decode", "bwd_states",
@@ -148,6 +152,28 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.gdn_group_norm_bwd_workspace.argtypes = [pp, i32, ctypes.POINTER(sz)]
     lib.gdn_group_norm_bwd.restype = i32
     lib.gdn_group_norm_bwd.argtypes = [pp, i32, i32, i32, i32, f32] + [vp] * 10 + [sz, vp]
+    lib.gdn_selective_scan_fwd_workspace.restype = i32
+    lib.gdn_selective_scan_fwd_workspace.argtypes = [pp, i32, ctypes.POINTER(sz)]
+    lib.gdn_selective_scan_fwd.restype = i32
+    lib.gdn_selective_scan_fwd.argtypes = [pp, i32, i32] + [vp] * 12 + [sz, vp]
+    lib.gdn_selective_scan_bwd_workspace.restype = i32
+    lib.gdn_selective_scan_bwd_workspace.argtypes = [pp, i32, ctypes.POINTER(sz)]
+    lib.gdn_selective_scan_bwd.restype = i32
+    lib.gdn_selective_scan_bwd.argtypes = [pp, i32, i32] + [vp] * 21 + [sz, vp]
+    lib.gdn_selective_scan_step.restype = i32
+    lib.gdn_selective_scan_step.argtypes = [pp, i32, i32] + [vp] * 11
+    lib.gdn_short_conv_fwd.restype = i32
+    lib.gdn_short_conv_fwd.argtypes = [pp, i32, i32] + [vp] * 7
+    lib.gdn_short_conv_bwd_workspace.restype = i32
+    lib.gdn_short_conv_bwd_workspace.argtypes = [pp, i32, ctypes.POINTER(sz)]
+    lib.gdn_short_conv_bwd.restype = i32
+    lib.gdn_short_conv_bwd.argtypes = [pp, i32, i32] + [vp] * 11 + [sz, vp]
+    lib.gdn_short_conv_step.restype = i32
+    lib.gdn_short_conv_step.argtypes = [pp, i32, i32] + [vp] * 6
+    lib.gdn_draft_accept_workspace.restype = i32
+    lib.gdn_draft_accept_workspace.argtypes = [pp, i32, i32, ctypes.POINTER(sz)]
+    lib.gdn_draft_accept.restype = i32
+    lib.gdn_draft_accept.argtypes = [pp, i32] + [vp] * 9 + [sz, vp]
     if path is None:
         _LIB = lib
     return lib

@@ -1244,3 +1244,376 @@ gdn_status gdn_group_norm_bwd(const gdn_problem* p, int32_t d, int32_t act, int3
 }
 
 }  // extern "C"
+
+// --------------------------------------- selective scan, short convolution ---
+
+namespace {
+
+// Rows of dense or packed sequences, as the linear-attention calls take them.
+gdn_status check_packing(const gdn_problem* p) {
+  if (p->T < 0 || p->nseq < 0) return GDN_FAIL(GDN_ERR_SHAPE);
+  if (p->nseq > 0) {
+    if (p->B != 1) return GDN_FAIL(GDN_ERR_SHAPE);
+    if (p->cu_seqlens == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+    if ((reinterpret_cast<uintptr_t>(p->cu_seqlens) & 3u) != 0) return GDN_FAIL(GDN_ERR_ALIGN);
+  } else if (p->cu_seqlens != nullptr) {
+    return GDN_FAIL(GDN_ERR_SHAPE);
+  }
+  return p->T > (1 << 30) ? GDN_FAIL(GDN_ERR_SHAPE) : GDN_OK;
+}
+
+// Checks of the scan entry points; step: one token of p->B sequences, the
+// packing ignored.  Sizes are bounded before they are multiplied.
+gdn_status check_scan(const gdn_problem* p, int32_t hb, int32_t softplus, bool step,
+                      gdn::Scan* out) {
+  if (p == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+  if (!dtype_ok(p->io_dtype)) return GDN_FAIL(GDN_ERR_DTYPE);
+  if (p->gate != GDN_GATE_NONE) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  if (p->B < 1 || p->H < 1 || p->dv < 1) return GDN_FAIL(GDN_ERR_SHAPE);
+  if (hb < 1 || hb > p->H || p->H % hb != 0) return GDN_FAIL(GDN_ERR_SHAPE);
+  if (p->dk < 4 || p->dk > 64 || p->dk % 4 != 0) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  const int64_t ch = static_cast<int64_t>(p->H) * p->dv;
+  if (ch > (int64_t(1) << 22)) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  if (!step) GDN_TRY(check_packing(p));
+  out->B = p->B;
+  out->T = step ? 1 : p->T;
+  out->H = p->H;
+  out->dk = p->dk;
+  out->dv = p->dv;
+  out->hb = hb;
+  out->varlen = !step && p->nseq > 0;
+  out->nseq = out->varlen ? p->nseq : p->B;
+  out->cu_seqlens = out->varlen ? p->cu_seqlens : nullptr;
+  out->io = p->io_dtype;
+  out->seg_req = step ? 0 : p->seg_chunks;
+  out->softplus = softplus != 0;
+  if (static_cast<int64_t>(out->B) * out->T > (int64_t(1) << 38) / ch ||
+      out->nseq > (int64_t(1) << 38) / (ch * p->dk) || !gdn::scan_fits(*out))
+    return GDN_FAIL(GDN_ERR_SHAPE);
+  return GDN_OK;
+}
+
+gdn_status check_scan_in(const gdn::Scan& p, const gdn::ScanIn& in) {
+  const int64_t tok = static_cast<int64_t>(p.B) * p.T, ch = static_cast<int64_t>(p.H) * p.dv;
+  GDN_TRY(need(in.x, tok * ch));
+  GDN_TRY(need(in.dt, tok * ch));
+  GDN_TRY(need(in.a, ch * p.dk));
+  GDN_TRY(need(in.b, tok * p.hb * p.dk));
+  GDN_TRY(need(in.c, tok * p.hb * p.dk));
+  GDN_TRY(opt(in.d));
+  GDN_TRY(opt(in.bias));
+  GDN_TRY(opt(in.z));
+  return opt(in.s0);
+}
+
+gdn_status launched(const gdn::Scan& p, hipError_t e) {
+  if (log_on()) {
+    fprintf(stderr, "gdn: %s: B=%d T=%d H=%d hb=%d dk=%d dv=%d io=%s nseq=%d%s%s -> %s\n", t_entry,
+            p.B, p.T, p.H, p.hb, p.dk, p.dv, dtype_name(p.io), p.nseq,
+            p.varlen ? " (varlen)" : "", p.softplus ? " softplus" : "", hipGetErrorName(e));
+  }
+  return e == hipSuccess ? GDN_OK : GDN_FAIL(GDN_ERR_HIP);
+}
+
+enum class ConvCall { fwd, bwd, step };
+
+gdn_status check_conv(const gdn_problem* p, int32_t width, int32_t act, ConvCall call,
+                      gdn::ShortConv* out) {
+  const bool step = call == ConvCall::step;
+  if (p == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+  if (!dtype_ok(p->io_dtype)) return GDN_FAIL(GDN_ERR_DTYPE);
+  if (p->B < 1 || p->H < 1 || p->dv < 1) return GDN_FAIL(GDN_ERR_SHAPE);
+  if (width < 1 || width > 8) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  if (act < GDN_ACT_NONE || act > GDN_ACT_SIGMOID) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  const int64_t ch = static_cast<int64_t>(p->H) * p->dv;
+  if (ch > (int64_t(1) << 22)) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  if (!step) GDN_TRY(check_packing(p));
+  out->B = p->B;
+  out->T = step ? 1 : p->T;
+  out->ch = static_cast<int>(ch);
+  out->width = width;
+  out->varlen = !step && p->nseq > 0;
+  out->nseq = out->varlen ? p->nseq : p->B;
+  out->cu_seqlens = out->varlen ? p->cu_seqlens : nullptr;
+  out->io = p->io_dtype;
+  out->act = act;
+  if (static_cast<int64_t>(out->B) * out->T > (int64_t(1) << 38) / ch ||
+      out->nseq > (int64_t(1) << 38) / (ch * 8) ||
+      !gdn::short_conv_fits(*out, call == ConvCall::bwd))
+    return GDN_FAIL(GDN_ERR_SHAPE);
+  return GDN_OK;
+}
+
+gdn_status launched(const gdn::ShortConv& p, hipError_t e) {
+  if (log_on()) {
+    fprintf(stderr, "gdn: %s: B=%d T=%d channels=%d width=%d act=%d io=%s nseq=%d%s -> %s\n",
+            t_entry, p.B, p.T, p.ch, p.width, p.act, dtype_name(p.io), p.nseq,
+            p.varlen ? " (varlen)" : "", hipGetErrorName(e));
+  }
+  return e == hipSuccess ? GDN_OK : GDN_FAIL(GDN_ERR_HIP);
+}
+
+gdn_status check_accept(const gdn_problem* p, int32_t vocab, bool tree, gdn::Accept* out) {
+  if (p == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+  if (!dtype_ok(p->io_dtype)) return GDN_FAIL(GDN_ERR_DTYPE);
+  if (p->B < 1 || vocab < 1 || vocab > (1 << 28)) return GDN_FAIL(GDN_ERR_SHAPE);
+  GDN_TRY(check_packing(p));
+  if (p->nseq == 0 && p->T > 64) return GDN_FAIL(GDN_ERR_SHAPE);
+  out->trees = p->nseq > 0 ? p->nseq : p->B;
+  out->n = p->T;
+  out->V = vocab;
+  out->cu_seqlens = p->nseq > 0 ? p->cu_seqlens : nullptr;
+  out->io = p->io_dtype;
+  out->tree = tree;
+  if (out->trees > (1 << 20)) return GDN_FAIL(GDN_ERR_SHAPE);
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_selective_scan_fwd_workspace(const gdn_problem* p, int32_t hb, size_t* bytes) {
+  GDN_ENTRY();
+  try {
+    if (bytes == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+    gdn::Scan pp;
+    GDN_TRY(check_scan(p, hb, 1, false, &pp));
+    *bytes = gdn::scan_fwd_workspace_bytes(pp);
+    return GDN_OK;
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_selective_scan_fwd(const gdn_problem* p, int32_t hb, int32_t softplus,
+                                  const void* x, const void* dt, const float* a, const void* b,
+                                  const void* c, const float* d, const float* dt_bias,
+                                  const void* z, const float* s0, void* y, float* s_final,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  GDN_ENTRY();
+  try {
+    gdn::Scan pp;
+    GDN_TRY(check_scan(p, hb, softplus, false, &pp));
+    const gdn::ScanIn in{x, dt, a, b, c, d, dt_bias, z, s0};
+    GDN_TRY(check_scan_in(pp, in));
+    GDN_TRY(need(y, static_cast<int64_t>(pp.B) * pp.T));
+    GDN_TRY(opt(s_final));
+    const size_t need_ws = gdn::scan_fwd_workspace_bytes(pp);
+    if (need_ws > 0 && (ws == nullptr || ws_bytes < need_ws)) return GDN_FAIL(GDN_ERR_WORKSPACE);
+    GDN_TRY(opt(ws));
+    if (g_fail_launch.load()) return launched(pp, hipErrorLaunchFailure);  // test hook
+    return launched(pp, gdn::launch_scan_fwd(pp, in, y, s_final, ws,
+                                             static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_selective_scan_bwd_workspace(const gdn_problem* p, int32_t hb, size_t* bytes) {
+  GDN_ENTRY();
+  try {
+    if (bytes == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+    gdn::Scan pp;
+    GDN_TRY(check_scan(p, hb, 1, false, &pp));
+    *bytes = gdn::scan_bwd_workspace_bytes(pp);
+    return GDN_OK;
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_selective_scan_bwd(const gdn_problem* p, int32_t hb, int32_t softplus,
+                                  const void* x, const void* dt, const float* a, const void* b,
+                                  const void* c, const float* d, const float* dt_bias,
+                                  const void* z, const float* s0, const void* dy,
+                                  const float* ds_final, void* dx, void* ddt, float* da, void* db,
+                                  void* dc, float* dd, float* ddt_bias, void* dz, float* ds0,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  GDN_ENTRY();
+  try {
+    gdn::Scan pp;
+    GDN_TRY(check_scan(p, hb, softplus, false, &pp));
+    const gdn::ScanIn in{x, dt, a, b, c, d, dt_bias, z, s0};
+    GDN_TRY(check_scan_in(pp, in));
+    const int64_t tok = static_cast<int64_t>(pp.B) * pp.T;
+    GDN_TRY(need(dy, tok));
+    GDN_TRY(opt(ds_final));
+    GDN_TRY(need(dx, tok));
+    GDN_TRY(need(ddt, tok));
+    GDN_TRY(need(da, 1));
+    GDN_TRY(need(db, tok));
+    GDN_TRY(need(dc, tok));
+    GDN_TRY(opt(dd));
+    GDN_TRY(opt(ddt_bias));
+    if (z != nullptr) GDN_TRY(need(dz, tok));
+    GDN_TRY(opt(ds0));
+    if (ws == nullptr || ws_bytes < gdn::scan_bwd_workspace_bytes(pp))
+      return GDN_FAIL(GDN_ERR_WORKSPACE);
+    GDN_TRY(opt(ws));
+    if (g_fail_launch.load()) return launched(pp, hipErrorLaunchFailure);  // test hook
+    const gdn::ScanGrad out{dx, ddt, da, db, dc, dd, ddt_bias, dz, ds0};
+    return launched(pp, gdn::launch_scan_bwd(pp, in, dy, ds_final, out, ws,
+                                             static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_selective_scan_step(const gdn_problem* p, int32_t hb, int32_t softplus,
+                                   const void* x, const void* dt, const float* a, const void* b,
+                                   const void* c, const float* d, const float* dt_bias,
+                                   const void* z, float* state, void* y, void* stream) {
+  GDN_ENTRY();
+  try {
+    gdn::Scan pp;
+    GDN_TRY(check_scan(p, hb, softplus, true, &pp));
+    const gdn::ScanIn in{x, dt, a, b, c, d, dt_bias, z, nullptr};
+    GDN_TRY(check_scan_in(pp, in));
+    GDN_TRY(need(y, pp.B));
+    GDN_TRY(need(state, pp.B));
+    if (g_fail_launch.load()) return launched(pp, hipErrorLaunchFailure);  // test hook
+    return launched(pp,
+                    gdn::launch_scan_step(pp, in, state, y, static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_short_conv_fwd(const gdn_problem* p, int32_t width, int32_t act, const void* x,
+                              const float* taps, const float* bias, const void* s0, void* y,
+                              void* s_final, void* stream) {
+  GDN_ENTRY();
+  try {
+    gdn::ShortConv pp;
+    GDN_TRY(check_conv(p, width, act, ConvCall::fwd, &pp));
+    const int64_t tok = static_cast<int64_t>(pp.B) * pp.T;
+    GDN_TRY(need(x, tok));
+    GDN_TRY(need(taps, 1));
+    GDN_TRY(opt(bias));
+    GDN_TRY(opt(s0));
+    GDN_TRY(need(y, tok));
+    GDN_TRY(opt(s_final));
+    if (g_fail_launch.load()) return launched(pp, hipErrorLaunchFailure);  // test hook
+    return launched(pp, gdn::launch_short_conv_fwd(pp, x, taps, bias, s0, y, s_final,
+                                                   static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_short_conv_bwd_workspace(const gdn_problem* p, int32_t width, size_t* bytes) {
+  GDN_ENTRY();
+  try {
+    if (bytes == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+    gdn::ShortConv pp;
+    GDN_TRY(check_conv(p, width, GDN_ACT_NONE, ConvCall::bwd, &pp));
+    *bytes = gdn::short_conv_bwd_workspace_bytes(pp);
+    return GDN_OK;
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_short_conv_bwd(const gdn_problem* p, int32_t width, int32_t act, const void* x,
+                              const float* taps, const float* bias, const void* s0,
+                              const void* dy, const void* ds_final, void* dx, float* dtaps,
+                              float* dbias, void* ds0, void* ws, size_t ws_bytes, void* stream) {
+  GDN_ENTRY();
+  try {
+    gdn::ShortConv pp;
+    GDN_TRY(check_conv(p, width, act, ConvCall::bwd, &pp));
+    const int64_t tok = static_cast<int64_t>(pp.B) * pp.T;
+    GDN_TRY(need(x, tok));
+    GDN_TRY(need(taps, 1));
+    GDN_TRY(opt(bias));
+    GDN_TRY(opt(s0));
+    GDN_TRY(need(dy, tok));
+    GDN_TRY(opt(ds_final));
+    GDN_TRY(need(dx, tok));
+    GDN_TRY(need(dtaps, 1));
+    GDN_TRY(opt(dbias));
+    GDN_TRY(opt(ds0));
+    if (ws == nullptr || ws_bytes < gdn::short_conv_bwd_workspace_bytes(pp))
+      return GDN_FAIL(GDN_ERR_WORKSPACE);
+    GDN_TRY(opt(ws));
+    if (g_fail_launch.load()) return launched(pp, hipErrorLaunchFailure);  // test hook
+    return launched(pp, gdn::launch_short_conv_bwd(pp, x, taps, bias, s0, dy, ds_final, dx, dtaps,
+                                                   dbias, ds0, ws,
+                                                   static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_short_conv_step(const gdn_problem* p, int32_t width, int32_t act, const void* x,
+                               const float* taps, const float* bias, void* state, void* y,
+                               void* stream) {
+  GDN_ENTRY();
+  try {
+    gdn::ShortConv pp;
+    GDN_TRY(check_conv(p, width, act, ConvCall::step, &pp));
+    GDN_TRY(need(x, 1));
+    GDN_TRY(need(taps, 1));
+    GDN_TRY(opt(bias));
+    GDN_TRY(need(state, width - 1));
+    GDN_TRY(need(y, 1));
+    if (g_fail_launch.load()) return launched(pp, hipErrorLaunchFailure);  // test hook
+    return launched(pp, gdn::launch_short_conv_step(pp, x, taps, bias, state, y,
+                                                    static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+// -------------------------------------------------------- draft acceptance ---
+
+gdn_status gdn_draft_accept_workspace(const gdn_problem* p, int32_t vocab, int32_t tree,
+                                      size_t* bytes) {
+  GDN_ENTRY();
+  try {
+    if (bytes == nullptr) return GDN_FAIL(GDN_ERR_NULL);
+    gdn::Accept pp;
+    GDN_TRY(check_accept(p, vocab, tree != 0, &pp));
+    *bytes = gdn::accept_workspace_bytes(pp);
+    return GDN_OK;
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+gdn_status gdn_draft_accept(const gdn_problem* p, int32_t vocab, const int32_t* parent,
+                            const int32_t* tokens, const void* target, const void* draft,
+                            const float* uniform, int32_t* accepted, int32_t* length,
+                            int32_t* next_token, void* ws, size_t ws_bytes, void* stream) {
+  GDN_ENTRY();
+  try {
+    gdn::Accept pp;
+    GDN_TRY(check_accept(p, vocab, parent != nullptr, &pp));
+    GDN_TRY(opt(parent));
+    GDN_TRY(need(tokens, pp.n));
+    GDN_TRY(need(target, 1));
+    GDN_TRY(opt(draft));
+    GDN_TRY(need(uniform, 1));
+    GDN_TRY(need(accepted, 1));
+    GDN_TRY(need(length, 1));
+    GDN_TRY(need(next_token, 1));
+    const size_t need_ws = gdn::accept_workspace_bytes(pp);
+    if (need_ws > 0 && (ws == nullptr || ws_bytes < need_ws)) return GDN_FAIL(GDN_ERR_WORKSPACE);
+    GDN_TRY(opt(ws));
+    const hipError_t e =
+        g_fail_launch.load()  // test hook
+            ? hipErrorLaunchFailure
+            : gdn::launch_accept(pp, parent, tokens, target, draft, uniform, accepted, length,
+                                 next_token, ws, static_cast<hipStream_t>(stream));
+    if (log_on())
+      fprintf(stderr, "gdn: %s: trees=%d nodes=%d vocab=%d io=%s%s%s -> %s\n", t_entry, pp.trees,
+              pp.n, pp.V, dtype_name(pp.io), pp.cu_seqlens ? " (varlen)" : "",
+              pp.tree ? " tree" : " chain", hipGetErrorName(e));
+    return e == hipSuccess ? GDN_OK : GDN_FAIL(GDN_ERR_HIP);
+  } catch (...) {
+    return GDN_FAIL(GDN_ERR_HIP);
+  }
+}
+
+}  // extern "C"

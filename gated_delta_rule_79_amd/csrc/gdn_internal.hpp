@@ -151,4 +151,80 @@ hipError_t launch_group_norm_bwd(const GroupNorm& p, const void* x, const void* 
                                  const float* b, const void* dy, void* dx, void* dz, float* dw,
                                  float* db, void* ws, hipStream_t s);
 
+// Selective state space scan (gdn_scan.hip).
+constexpr int kScanTile = 16;  // seg_chunks counts these tokens
+struct Scan {
+  int B, T, H, dk, dv;        // H heads of dv channels, dk states a channel
+  int hb;                     // groups of heads that share b and c rows
+  int nseq;                   // number of independent sequences (B or packed)
+  bool varlen;
+  const int32_t* cu_seqlens;  // device
+  int io;                     // gdn_dtype
+  int seg_req;                // gdn_problem::seg_chunks
+  bool softplus;
+};
+struct ScanIn {
+  const void *x, *dt;
+  const float* a;
+  const void *b, *c;
+  const float *d, *bias;
+  const void* z;
+  const float* s0;
+};
+struct ScanGrad {
+  void *dx, *ddt;
+  float* da;
+  void *db, *dc;
+  float *dd, *dbias;
+  void* dz;
+  float* ds0;
+};
+// whether every launch of a call fits the grid
+bool scan_fits(const Scan& p);
+size_t scan_fwd_workspace_bytes(const Scan& p);
+hipError_t launch_scan_fwd(const Scan& p, const ScanIn& in, void* y, float* s_final, void* ws,
+                           hipStream_t s);
+size_t scan_bwd_workspace_bytes(const Scan& p);
+hipError_t launch_scan_bwd(const Scan& p, const ScanIn& in, const void* dy, const float* ds_final,
+                           const ScanGrad& out, void* ws, hipStream_t s);
+hipError_t launch_scan_step(const Scan& p, const ScanIn& in, float* state, void* y,
+                            hipStream_t s);
+
+// Short causal convolution with a carried history (gdn_conv.hip).
+struct ShortConv {
+  int B, T;
+  int ch;                     // channels of a row
+  int width;                  // taps of a channel
+  int nseq;                   // number of independent sequences (B or packed)
+  bool varlen;
+  const int32_t* cu_seqlens;  // device
+  int io;                     // gdn_dtype
+  int act;                    // gdn_act
+};
+bool short_conv_fits(const ShortConv& p, bool bwd);
+hipError_t launch_short_conv_fwd(const ShortConv& p, const void* x, const float* taps,
+                                 const float* bias, const void* s0, void* y, void* s_final,
+                                 hipStream_t s);
+size_t short_conv_bwd_workspace_bytes(const ShortConv& p);
+hipError_t launch_short_conv_bwd(const ShortConv& p, const void* x, const float* taps,
+                                 const float* bias, const void* s0, const void* dy,
+                                 const void* ds_final, void* dx, float* dtaps, float* dbias,
+                                 void* ds0, void* ws, hipStream_t s);
+hipError_t launch_short_conv_step(const ShortConv& p, const void* x, const float* taps,
+                                  const float* bias, void* state, void* y, hipStream_t s);
+
+// Acceptance of drafted tokens (gdn_accept.hip).
+struct Accept {
+  int trees, n;               // n: nodes of each, packed: of all
+  int V;                      // vocabulary
+  const int32_t* cu_seqlens;  // device, null: dense
+  int io;                     // gdn_dtype of the probabilities
+  bool tree;                  // parents are given (else chains)
+};
+size_t accept_workspace_bytes(const Accept& p);
+hipError_t launch_accept(const Accept& p, const int32_t* parent, const int32_t* tokens,
+                         const void* target, const void* draft, const float* u,
+                         int32_t* accepted, int32_t* length, int32_t* next, void* ws,
+                         hipStream_t s);
+
 }  // namespace gdn

@@ -1,0 +1,1328 @@
+// Selective state space scan: every channel j of the H heads carries dk
+// values,
+//
+//   delta_t = softplus(dt_t + bias)            (or dt_t + bias)
+//   S_t[n]  = e^{delta_t a[n]} S_{t-1}[n] + delta_t x_t b_t[n]
+//   y_t     = (sum_n c_t[n] S_t[n] + d x_t) * silu(z_t)
+//
+// with b, c rows shared by all channels of a group (H / hb heads), its
+// backward and its single-token step.
+//
+// A lane owns one channel and NS of its states, in registers for a whole walk
+// over the tokens; a wave owns 64 channels of one group, so that the b and c
+// values are the same for all its lanes and arrive as scalars.  More than NS
+// states are shared out over WS waves of the workgroup, whose sums over n meet
+// in LDS.  There is no product of two shared matrices here (the decay differs
+// in every channel and state), so nothing for the matrix cores: the vector
+// unit's exponential, two multiplications and two multiply-adds for every
+// token, channel and state bound the walks.
+//
+// Few or long sequences are cut into segments walked by workgroups of their
+// own: one launch walks every segment from zero and leaves its last state and
+// the sum of its delta (the segment's decay is e^{a sum}); one chains them;
+// one walks the outputs from the states chained.  Packed sequences are cut
+// on the grid of all tokens, whatever their bounds: a walk goes from run to
+// run of one sequence and takes up each sequence's own initial state, so all
+// workgroups have the same number of tokens and the host need not know the
+// lengths.
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "gdn_device.hpp"
+#include "gdn_internal.hpp"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2eLow = 1.92596303e-8f;  // log2(e) - kLog2e
+constexpr float kLn2 = 0.69314718055994530942f;
+
+#define GDN_CONST __attribute__((address_space(4)))
+
+// ------------------------------------------------------------- functions ---
+
+// e^{-x} for x >= 0: the part of x log2(e) that its product loses goes back in
+__device__ inline float exp_neg(float x) {
+  x = x > 104.f ? 104.f : x;  // (a NaN stays)
+  const float t = -x * kLog2e;
+  const float low = fmaf(-x, kLog2e, -t) - x * kLog2eLow;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e * kLn2, low, e);
+}
+
+// softplus(v) = max(v, 0) + log(1 + e^{-|v|}), the logarithm as
+// 2 artanh(u / (2 + u)) with u = e^{-|v|} <= 1: the series in s^2 <= 1/9 ends
+// below 2^-24 after eight terms, and a small u keeps all its bits.
+__device__ inline float softplus(float v) {
+  const float u = exp_neg(fabsf(v));
+  const float s = u * __builtin_amdgcn_rcpf(2.f + u), q = s * s;
+  float p = 1.f / 15.f;
+  p = fmaf(p, q, 1.f / 13.f);
+  p = fmaf(p, q, 1.f / 11.f);
+  p = fmaf(p, q, 1.f / 9.f);
+  p = fmaf(p, q, 1.f / 7.f);
+  p = fmaf(p, q, 1.f / 5.f);
+  p = fmaf(p, q, 1.f / 3.f);
+  p = fmaf(p, q, 1.f);
+  return (v > 0.f ? v : 0.f) + 2.f * s * p;
+}
+
+__device__ inline float sigmoid(float v) {
+  const float u = exp_neg(fabsf(v)), r = __builtin_amdgcn_rcpf(1.f + u);
+  return v >= 0.f ? r : u * r;
+}
+
+// ------------------------------------------------------------------ sizes ---
+
+struct Args {
+  int64_t T;          // tokens of a dense sequence, or of the packed row
+  int D, Dg, nb;      // channels, channels of a group, 64-channel blocks of a group
+  int units;          // nb times the groups
+  int ublocks;        // workgroups of a segment
+  int dk, dv, hb;
+  int S, L;           // segments of a sequence (packed: of all), their tokens
+  int nseq;
+  int softplus;
+  const int32_t* cu;
+  const void *x, *dt, *b, *c, *z, *dy;
+  const float *a, *d, *bias, *s0, *ds;
+  void *y, *dx, *ddt, *dz;
+  float *sf, *ds0;
+  // workspace
+  int* cut;           // [segments] the state behind the segment does not see its front
+  float* h;           // [segments][D dk] state behind a segment; after the chaining, in front
+  float* sum;         // [segments][D] sum of delta
+  int* cutr;          // the same from the last token back
+  float* g;
+  float *mark, *msum; // [tokens / kTile][D dk], [..][D]: states inside segments
+  float* part;        // [tokens][units][WS][2][NS] shares of db, dc
+  float *pa, *pd, *pb;  // [segments][D dk], [segments][WS][D] twice
+};
+
+// A segment's tokens, counted over all sequences.
+struct Span {
+  int64_t lo, hi;
+  int at;             // slot
+  int chain;          // dense: the sequence
+  bool first, last;   // of its sequence (packed: of all)
+};
+
+__device__ inline Span span_of(const Args& A, int at) {
+  Span s;
+  s.at = at;
+  s.chain = at / A.S;
+  const int k = at - s.chain * A.S;
+  s.first = k == 0;
+  s.last = k == A.S - 1;
+  const int64_t base = s.chain * A.T, from = static_cast<int64_t>(k) * A.L;
+  s.lo = base + (from < A.T ? from : A.T);
+  s.hi = base + (s.last || from + A.L > A.T ? A.T : from + A.L);
+  return s;
+}
+
+__device__ inline int64_t bound(const Args& A, int n) {
+  return reinterpret_cast<const GDN_CONST int32_t*>(reinterpret_cast<uintptr_t>(A.cu))[n];
+}
+
+// smallest n with cu[n] >= t, A.nseq + 1 if there is none
+__device__ inline int lower(const Args& A, int64_t t) {
+  int lo = 0, hi = A.nseq + 1;
+  while (lo < hi) {
+    const int m = (lo + hi) >> 1;
+    if (bound(A, m) >= t) hi = m;
+    else lo = m + 1;
+  }
+  return lo;
+}
+
+// The tokens of one sequence in a segment.
+struct Run {
+  int seq;
+  int64_t lo, hi;
+  bool cont;   // they continue the segment in front
+  bool ends;   // the sequence ends with them
+};
+
+// The runs of a segment: index 0 is what continues the segment in front (if
+// there is such), 1 .. count are the sequences that begin here, empty ones
+// among them.  Bounds outside the segment or out of order give runs inside it.
+struct Runs {
+  int n0, count;
+  bool cont;
+};
+
+__device__ inline Runs runs_of(const Args& A, const Span& s) {
+  Runs r;
+  if (A.cu == nullptr) {
+    r.n0 = s.chain;
+    r.count = s.first ? 1 : 0;
+    r.cont = !s.first;
+    return r;
+  }
+  r.n0 = lower(A, s.lo);
+  // (nothing lies in front of the first segment, whatever the bounds say)
+  r.cont = !s.first && r.n0 > 0 && r.n0 <= A.nseq && bound(A, r.n0) > s.lo;
+  const int end = s.last ? A.nseq : min(lower(A, s.hi), A.nseq);
+  r.count = max(end - r.n0, 0);
+  return r;
+}
+
+__device__ inline Run run_at(const Args& A, const Span& s, const Runs& r, int i) {
+  Run t;
+  t.cont = i == 0;
+  if (A.cu == nullptr) {
+    t.seq = s.chain;
+    t.lo = s.lo;
+    t.hi = s.hi;
+    t.ends = s.last;
+    return t;
+  }
+  t.seq = r.n0 + i - 1;
+  const int64_t b = bound(A, t.seq), e = bound(A, t.seq + 1);
+  t.lo = i == 0 || b < s.lo ? s.lo : b > s.hi ? s.hi : b;
+  t.hi = e < t.lo ? t.lo : e > s.hi ? s.hi : e;
+  t.ends = s.last || e <= s.hi;  // (nor anything behind the last)
+  return t;
+}
+
+// ------------------------------------------------------------------ lanes ---
+
+// Memory through buffer descriptors: a row's place is a scalar, a lane's the
+// same 32-bit byte offset in every row, and what lies past the descriptor's
+// bytes (rows behind a run, lanes without a channel) is read as zero and not
+// written.
+constexpr uint32_t kNowhere = 0x80000000u;
+
+__device__ inline __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes),
+                                           0x00027000);
+}
+
+// What a lane keeps of its channel.
+template <int NS>
+struct Lane {
+  int unit, grp;      // channel block, group
+  int n0, left;       // first state of the wave, states from it on
+  int ch;             // channel (of the last one where the lane has none)
+  bool live;
+  uint32_t row;       // bytes in front of the channel in a row of x
+  uint32_t state;     // bytes in front of (n0, channel) in a [H, dk, dv] state
+  float a2[NS];       // a log2(e)
+  float bias, d;
+};
+
+template <int NS, bool PAD>
+__device__ inline void load_state(const Args& A, const Lane<NS>& l, const float* p, float* h) {
+  const auto b = buffer(p, 4u * A.D * A.dk);
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+    h[i] = !PAD || i < l.left
+               ? __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, l.state, 4 * i * A.dv, 0))
+               : 0.f;
+}
+template <int NS, bool PAD>
+__device__ inline void store_state(const Args& A, const Lane<NS>& l, float* p, const float* h) {
+  const auto b = buffer(p, 4u * A.D * A.dk);
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+    if (!PAD || i < l.left)
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(h[i]), b, l.state, 4 * i * A.dv, 0);
+}
+
+template <typename IO, int NS, int WS, bool PAD>
+__device__ inline Lane<NS> lane_of(const Args& A) {
+  Lane<NS> l;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int unit = blockIdx.x % A.ublocks * (kWaves / WS) + wave / WS;
+  l.unit = min(unit, A.units - 1);
+  l.grp = l.unit / A.nb;
+  const int j = (l.unit - l.grp * A.nb) * 64 + lane;
+  l.live = unit < A.units && j < A.Dg;
+  l.ch = l.grp * A.Dg + min(j, A.Dg - 1);
+  l.n0 = (wave % WS) * NS;
+  l.left = A.dk - l.n0;
+  const int head = l.ch / A.dv;
+  l.row = l.live ? l.ch * io<IO>::bytes : kNowhere;
+  l.state = l.live ? 4u * (head * A.dk * A.dv + l.ch - head * A.dv + l.n0 * A.dv) : kNowhere;
+  load_state<NS, PAD>(A, l, A.a, l.a2);
+#pragma unroll
+  for (int i = 0; i < NS; ++i) l.a2[i] *= kLog2e;
+  l.bias = A.bias != nullptr ? A.bias[l.ch] : 0.f;
+  l.d = A.d != nullptr ? A.d[l.ch] : 0.f;
+  return l;
+}
+
+// N values of a token's b or c row, the same for all lanes and so scalars;
+// they stay packed until they are used.  left: states from the first of them
+// to the row's end; those past it are zeros.
+template <typename IO, int N, bool PAD>
+struct Row {
+  uint32_t w[N * io<IO>::bytes / 4];
+  // from: the wave's part of the row
+  __device__ inline void load(uintptr_t from, int left) {
+#pragma unroll
+    for (int q = 0; q < N; q += 4) {
+      const int n = !PAD || q < left ? q : left - 4;
+      const GDN_CONST uint32_t* s =
+          reinterpret_cast<const GDN_CONST uint32_t*>(from + n * io<IO>::bytes);
+#pragma unroll
+      for (int i = 0; i < io<IO>::bytes; ++i)
+        w[q * io<IO>::bytes / 4 + i] = PAD && q >= left ? 0 : s[i];
+    }
+  }
+  __device__ inline float operator[](int n) const {
+    if constexpr (io<IO>::bytes == 4) return __uint_as_float(w[n]);
+    return __uint_as_float(n & 1 ? w[n >> 1] & 0xffff0000u : w[n >> 1] << 16);
+  }
+  // Unpacks anew from here on (kept unpacked, a row takes a register a value).
+  __device__ inline void pack() {
+#pragma unroll
+    for (auto& x : w) asm volatile("" : "+s"(x));
+  }
+  // The loads are there when this returns: what is loaded next is not waited
+  // for together with them (scalar loads end in any order, so the wait for
+  // one is a wait for all).
+  __device__ inline void arrive() const {
+    asm volatile("" ::"s"(w[0]));
+    __builtin_amdgcn_sched_barrier(0);
+  }
+};
+
+// Values of a wave's channels in U tokens, as stored; left: tokens of the run
+// from the first of them (rows past it are zeros).
+template <typename IO, int U>
+struct Rows {
+  uint32_t v[U];
+  __device__ inline void load(const Args& A, const void* p, int64_t tok, int left, uint32_t row) {
+    const uint32_t bytes = A.D * io<IO>::bytes;
+    const int most = max(min(left, U), 0);
+    const auto b = buffer(static_cast<const char*>(p) + tok * bytes, most * bytes);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // (a scalar offset past the descriptor's end is not relied on)
+      const uint32_t at = min(u, most) * bytes;
+      if constexpr (io<IO>::bytes == 2) v[u] = __builtin_amdgcn_raw_buffer_load_b16(b, row, at, 0);
+      else v[u] = __builtin_amdgcn_raw_buffer_load_b32(b, row, at, 0);
+    }
+  }
+  __device__ inline float operator[](int u) const {
+    return __uint_as_float(io<IO>::bytes == 2 ? v[u] << 16 : v[u]);
+  }
+};
+// The rows of a run from token tok on, to be written.
+template <typename IO, int U>
+struct RowsOut {
+  __amdgpu_buffer_rsrc_t b;
+  int most;
+  uint32_t bytes;
+  __device__ inline RowsOut(const Args& A, void* p, int64_t tok, int left)
+      : most(min(left, U)), bytes(A.D * io<IO>::bytes) {
+    b = buffer(static_cast<char*>(p) + tok * bytes, most * bytes);
+  }
+  __device__ inline void store(int u, uint32_t row, float v) const {
+    const uint32_t at = min(u, most) * bytes;
+    if constexpr (io<IO>::bytes == 2)
+      __builtin_amdgcn_raw_buffer_store_b16(
+          __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)), b, row, at, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), b, row, at, 0);
+  }
+};
+
+template <typename IO>
+__device__ inline float load_x(const void* p, const Args& A, int64_t tok, int ch) {
+  return io<IO>::load(static_cast<const char*>(p) + tok * A.D * io<IO>::bytes, ch);
+}
+template <typename IO>
+__device__ inline void store_x(void* p, const Args& A, int64_t tok, int ch, float v) {
+  io<IO>::store(static_cast<char*>(p) + tok * A.D * io<IO>::bytes, ch, v);
+}
+
+__device__ inline float step_of(const Args& A, float dt, float bias) {
+  return A.softplus ? softplus(dt + bias) : dt + bias;
+}
+
+__device__ inline float decay(float delta, float a2) {
+  return __builtin_amdgcn_exp2f(delta * a2);
+}
+
+// Where the wave's part of a token's row of b or c begins, and the bytes from
+// one token's to the next.
+template <typename IO, int NS>
+__device__ inline uintptr_t row_of(const Args& A, const Lane<NS>& l, const void* p, int64_t tok) {
+  return reinterpret_cast<uintptr_t>(p) + ((tok * A.hb + l.grp) * A.dk + l.n0) * io<IO>::bytes;
+}
+template <typename IO>
+__device__ inline int row_step(const Args& A) {
+  return A.hb * A.dk * io<IO>::bytes;
+}
+
+// The state a run starts from.
+template <int NS, bool PAD>
+__device__ inline void enter(const Args& A, const Lane<NS>& l, const Span& s, const Run& r,
+                             float* h) {
+  const int64_t size = static_cast<int64_t>(A.D) * A.dk;
+  if (r.cont) {
+    load_state<NS, PAD>(A, l, A.h + s.at * size, h);
+  } else if (A.s0 != nullptr) {
+    load_state<NS, PAD>(A, l, A.s0 + r.seq * size, h);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) h[i] = 0.f;
+  }
+}
+
+// Walks a run in groups of four tokens, the next group's rows and the next
+// token's b on their way: f(t, left, x, u, delta, b) for token u of the group
+// at t.  Tokens past the run have x = delta = 0, which leaves a state as it is.
+template <typename IO, int NS, bool PAD, typename F>
+__device__ inline void walk(const Args& A, const Lane<NS>& l, const Run& r, F f) {
+  constexpr int U = 4;
+  Rows<IO, U> x, dt;
+  Row<IO, NS, PAD> next;
+  int left = static_cast<int>(r.hi - r.lo);
+  x.load(A, A.x, r.lo, left, l.row);
+  dt.load(A, A.dt, r.lo, left, l.row);
+  uintptr_t from = row_of<IO>(A, l, A.b, r.lo);
+  const int step = row_step<IO>(A);
+  if (left > 0) next.load(from, l.left);
+  for (int64_t t = r.lo; left > 0; t += U, left -= U, from += U * step) {
+    const Rows<IO, U> xs = x, dts = dt;
+    x.load(A, A.x, t + U, left - U, l.row);
+    dt.load(A, A.dt, t + U, left - U, l.row);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const Row<IO, NS, PAD> b = next;
+      b.arrive();
+      next.load(from + min(u + 1, left - 1) * step, l.left);
+      const float delta = u < left ? step_of(A, dts[u], l.bias) : 0.f;
+      f(t, left, xs, u, delta, b);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+// --------------------------------------------------- segments' own states ---
+
+// State behind a segment: from its last run, walked from its sequence's
+// initial state or, where it continues the segment in front, from zero.
+template <typename IO, int NS, bool PAD>
+__global__ __launch_bounds__(kThreads) void scan_local_kernel(Args A, int WS) {
+  const int k = blockIdx.x / A.ublocks;
+  const Span s = span_of(A, k + k / (A.S - 1));  // (no last segment of a sequence)
+  const Runs rs = runs_of(A, s);
+  Lane<NS> l = WS == 1 ? lane_of<IO, NS, 1, PAD>(A)
+               : WS == 2 ? lane_of<IO, NS, 2, PAD>(A) : lane_of<IO, NS, 4, PAD>(A);
+  const int64_t size = static_cast<int64_t>(A.D) * A.dk;
+  int i = rs.count;
+  Run r{};
+  for (; i >= (rs.cont ? 0 : 1); --i) {
+    r = run_at(A, s, rs, i);
+    if (r.hi > r.lo) break;
+  }
+  float h[NS], sum = 0.f;
+#pragma unroll
+  for (int n = 0; n < NS; ++n) h[n] = 0.f;
+  const bool none = i < (rs.cont ? 0 : 1);
+  if (!none) {
+    if (!r.cont) enter<NS, PAD>(A, l, s, r, h);
+    walk<IO, NS, PAD>(A, l, r, [&](int64_t, int, const Rows<IO, 4>& x, int u, float delta,
+                                   const Row<IO, NS, PAD>& b) {
+      const float dx = delta * x[u];
+      sum += delta;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) h[n] = fmaf(decay(delta, l.a2[n]), h[n], dx * b[n]);
+    });
+  }
+  store_state<NS, PAD>(A, l, A.h + s.at * size, h);
+  if (l.live && l.n0 == 0) A.sum[static_cast<int64_t>(s.at) * A.D + l.ch] = sum;
+  if (blockIdx.x % A.ublocks == 0 && threadIdx.x == 0) A.cut[s.at] = none || !r.cont;
+}
+
+// Chains the segments' states: every one is replaced by the state in front of
+// its segment.  One thread a channel and state; eight segments in flight.
+__global__ __launch_bounds__(256) void scan_chain_kernel(Args A) {
+  const int64_t size = static_cast<int64_t>(A.D) * A.dk;
+  const unsigned blocks = (size + 255) / 256;
+  const int64_t e = static_cast<int64_t>(blockIdx.x % blocks) * 256 + threadIdx.x;
+  if (e >= size) return;
+  const int head = static_cast<int>(e / (A.dk * A.dv));
+  const int ch = head * A.dv + static_cast<int>(e % A.dv);
+  const float a2 = A.a[e] * kLog2e;
+  const int64_t at = static_cast<int64_t>(blockIdx.x / blocks) * A.S;
+  float* h = A.h + at * size + e;
+  const float* sum = A.sum + at * A.D + ch;
+  const int* cut = A.cut + at;
+  float state = 0.f;
+  constexpr int U = 8;
+  for (int k = 0; k < A.S; k += U) {
+    float v[U], q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = min(k + u, A.S - 2);  // (the last segment's is not there)
+      v[u] = h[j * size];
+      q[u] = sum[static_cast<int64_t>(j) * A.D];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k + u >= A.S) break;
+      h[(k + u) * size] = state;
+      if (k + u < A.S - 1) state = cut[k + u] ? v[u] : fmaf(decay(q[u], a2), state, v[u]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- outputs ---
+
+// The walk of the outputs.  WS > 1: every U tokens the waves of a channel
+// block leave their sums over n in LDS and share the rows out.
+template <typename IO, int NS, int WS, bool PAD, bool GATE>
+__global__ __launch_bounds__(kThreads) void scan_out_kernel(Args A) {
+  constexpr int U = 4;
+  const Span s = span_of(A, blockIdx.x / A.ublocks);
+  const Runs rs = runs_of(A, s);
+  const Lane<NS> l = lane_of<IO, NS, WS, PAD>(A);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t size = static_cast<int64_t>(A.D) * A.dk;
+  __shared__ float meet[WS > 1 ? kWaves : 1][WS > 1 ? U : 1][64];
+  for (int i = rs.cont ? 0 : 1; i <= rs.count; ++i) {
+    const Run r = run_at(A, s, rs, i);
+    float h[NS];
+    enter<NS, PAD>(A, l, s, r, h);
+    Rows<IO, U> x, dt, z{};
+    Row<IO, NS, PAD> nextb, nextc;
+    int left = static_cast<int>(r.hi - r.lo);
+    x.load(A, A.x, r.lo, left, l.row);
+    dt.load(A, A.dt, r.lo, left, l.row);
+    if constexpr (GATE) z.load(A, A.z, r.lo, left, l.row);
+    uintptr_t fromb = row_of<IO>(A, l, A.b, r.lo), fromc = row_of<IO>(A, l, A.c, r.lo);
+    const int step = row_step<IO>(A);
+    if (left > 0) {
+      nextb.load(fromb, l.left);
+      nextc.load(fromc, l.left);
+    }
+    for (int64_t t = r.lo; left > 0; t += U, left -= U, fromb += U * step, fromc += U * step) {
+      const Rows<IO, U> xs = x, dts = dt, zs = z;
+      float y[U];
+      x.load(A, A.x, t + U, left - U, l.row);
+      dt.load(A, A.dt, t + U, left - U, l.row);
+      if constexpr (GATE) z.load(A, A.z, t + U, left - U, l.row);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const Row<IO, NS, PAD> b = nextb, c = nextc;
+        b.arrive();
+        const int at = min(u + 1, left - 1) * step;
+        nextb.load(fromb + at, l.left);
+        nextc.load(fromc + at, l.left);
+        const float delta = u < left ? step_of(A, dts[u], l.bias) : 0.f, dx = delta * xs[u];
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          h[n] = fmaf(decay(delta, l.a2[n]), h[n], dx * b[n]);
+          sum[n & 3] = fmaf(c[n], h[n], sum[n & 3]);
+        }
+        y[u] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (WS > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < U; ++u) meet[wave][u][lane] = y[u];
+        __syncthreads();
+      }
+      const RowsOut<IO, U> out(A, A.y, t, left);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (WS > 1 && u % WS != wave % WS) continue;
+        float v = y[u];
+        if constexpr (WS > 1) {
+          v = meet[wave - wave % WS][u][lane];
+#pragma unroll
+          for (int k = 1; k < WS; ++k) v += meet[wave - wave % WS + k][u][lane];
+        }
+        v = fmaf(l.d, xs[u], v);
+        if constexpr (GATE) v *= zs[u] * sigmoid(zs[u]);
+        out.store(u, l.row, v);
+      }
+    }
+    if (r.ends && A.sf != nullptr) store_state<NS, PAD>(A, l, A.sf + r.seq * size, h);
+  }
+}
+
+// --------------------------------------------------------------- backward ---
+//
+// With dy_t the gradient of y_t in front of its gate and g_t that of S_t,
+//
+//   g_t[n] = c_t[n] dy_t + e^{delta_{t+1} a[n]} g_{t+1}[n]      (+ ds_final)
+//   dc_t[n] = sum_j dy_t S_t[n],          db_t[n] = sum_j g_t[n] delta_t x_t
+//   dx_t = delta_t sum_n g_t[n] b_t[n] + d dy_t
+//   ddelta_t = sum_n g_t[n] (x_t b_t[n] + a[n] e^{delta_t a[n]} S_{t-1}[n])
+//   da[n] = sum_t delta_t g_t[n] e^{delta_t a[n]} S_{t-1}[n]
+//
+// (j: the channels of a group).  The states are formed again: the walk of the
+// segments leaves one for every tile of kScanTile tokens (from zero where the
+// segment continues another; e^{a sum} of the state in front of the segment
+// is added when it is read).  The gradient walk goes over the tiles from the
+// last one back; a tile's states at every fourth token go to LDS, four
+// tokens' decays and decayed states stay in registers.
+
+// As scan_local_kernel, over all runs: besides the segment's state its tiles'
+// states, and what its first run makes of the gradient behind it.
+template <typename IO, int NS, bool PAD, bool GATE>
+__global__ __launch_bounds__(kThreads) void scan_marks_kernel(Args A, int WS) {
+  const Span s = span_of(A, blockIdx.x / A.ublocks);
+  const Runs rs = runs_of(A, s);
+  const Lane<NS> l = WS == 1 ? lane_of<IO, NS, 1, PAD>(A)
+                     : WS == 2 ? lane_of<IO, NS, 2, PAD>(A) : lane_of<IO, NS, 4, PAD>(A);
+  const int64_t size = static_cast<int64_t>(A.D) * A.dk;
+  float h[NS], g[NS], sum = 0.f, sumr = 0.f;
+#pragma unroll
+  for (int n = 0; n < NS; ++n) h[n] = g[n] = 0.f;
+  bool cut = true, cutr = true;
+  for (int i = rs.cont ? 0 : 1; i <= rs.count; ++i) {
+    const Run r = run_at(A, s, rs, i);
+    if (r.hi <= r.lo) continue;
+    cut = !r.cont;
+    sum = 0.f;
+    if (r.cont) {
+#pragma unroll
+      for (int n = 0; n < NS; ++n) h[n] = 0.f;
+    } else {
+      enter<NS, PAD>(A, l, s, r, h);
+    }
+    float front[NS];  // decay from the run's start (only where it continues one)
+#pragma unroll
+    for (int n = 0; n < NS; ++n) front[n] = 1.f;
+    auto mark = [&](int64_t t) {
+      if (t == r.lo || (t - r.lo) % kScanTile != 0) return;
+      const int64_t slot = t / kScanTile;
+      store_state<NS, PAD>(A, l, A.mark + slot * size, h);
+      if (l.live && l.n0 == 0) A.msum[slot * A.D + l.ch] = sum;
+    };
+    if (r.cont) {
+      constexpr int U = 4;
+      Rows<IO, U> dy, z{};
+      Row<IO, NS, PAD> next;
+      const int all = static_cast<int>(r.hi - r.lo);
+      dy.load(A, A.dy, r.lo, all, l.row);
+      if constexpr (GATE) z.load(A, A.z, r.lo, all, l.row);
+      const int step = row_step<IO>(A);
+      next.load(row_of<IO>(A, l, A.c, r.lo), l.left);
+      Rows<IO, U> dys, zs{};
+      walk<IO, NS, PAD>(A, l, r, [&](int64_t t, int left, const Rows<IO, U>& x, int u,
+                                     float delta, const Row<IO, NS, PAD>& b) {
+        if (u == 0) {
+          mark(t);
+          dys = dy;
+          zs = z;
+          dy.load(A, A.dy, t + U, left - U, l.row);
+          if constexpr (GATE) z.load(A, A.z, t + U, left - U, l.row);
+        }
+        const Row<IO, NS, PAD> c = next;
+        next.load(row_of<IO>(A, l, A.c, t) + min(u + 1, left - 1) * step, l.left);
+        const float dx = delta * x[u];
+        const float v = GATE ? dys[u] * zs[u] * sigmoid(zs[u]) : dys[u];
+        sum += delta;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const float e = decay(delta, l.a2[n]);
+          h[n] = fmaf(e, h[n], dx * b[n]);
+          front[n] *= e;
+          g[n] = fmaf(front[n], c[n] * v, g[n]);
+        }
+      });
+    } else {
+      walk<IO, NS, PAD>(A, l, r, [&](int64_t t, int, const Rows<IO, 4>& x, int u, float delta,
+                                     const Row<IO, NS, PAD>& b) {
+        if (u == 0) mark(t);
+        const float dx = delta * x[u];
+        sum += delta;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) h[n] = fmaf(decay(delta, l.a2[n]), h[n], dx * b[n]);
+      });
+    }
+    if (r.cont) {
+      cutr = r.ends;
+      sumr = sum;
+      if (r.ends && A.ds != nullptr) {
+        float v[NS];
+        load_state<NS, PAD>(A, l, A.ds + r.seq * size, v);
+#pragma unroll
+        for (int n = 0; n < NS; ++n) g[n] = fmaf(front[n], v[n], g[n]);
+      }
+    }
+  }
+  if (A.S == 1) return;
+  store_state<NS, PAD>(A, l, A.h + s.at * size, h);
+  store_state<NS, PAD>(A, l, A.g + s.at * size, g);
+  // (one run over the whole segment, or both directions are cut)
+  if (l.live && l.n0 == 0) A.sum[static_cast<int64_t>(s.at) * A.D + l.ch] = cut ? sumr : sum;
+  if (blockIdx.x % A.ublocks == 0 && threadIdx.x == 0) {
+    A.cut[s.at] = cut;
+    A.cutr[s.at] = cutr;
+  }
+}
+
+// Chains the segments' gradients from the last back: every one is replaced by
+// the gradient of the state behind its segment.
+__global__ __launch_bounds__(256) void scan_chain_back_kernel(Args A) {
+  const int64_t size = static_cast<int64_t>(A.D) * A.dk;
+  const unsigned blocks = (size + 255) / 256;
+  const int64_t e = static_cast<int64_t>(blockIdx.x % blocks) * 256 + threadIdx.x;
+  if (e >= size) return;
+  const int head = static_cast<int>(e / (A.dk * A.dv));
+  const int ch = head * A.dv + static_cast<int>(e % A.dv);
+  const float a2 = A.a[e] * kLog2e;
+  const int64_t at = static_cast<int64_t>(blockIdx.x / blocks) * A.S;
+  float* g = A.g + at * size + e;
+  const float* sum = A.sum + at * A.D + ch;
+  const int* cut = A.cutr + at;
+  float grad = 0.f;
+  constexpr int U = 8;
+  for (int k = A.S - 1; k >= 0; k -= U) {
+    float v[U], q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = max(k - u, 0);
+      v[u] = g[j * size];
+      q[u] = sum[static_cast<int64_t>(j) * A.D];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k - u < 0) break;
+      g[(k - u) * size] = grad;
+      grad = cut[k - u] ? v[u] : fmaf(decay(q[u], a2), grad, v[u]);
+    }
+  }
+}
+
+template <int CTRL>
+__device__ inline float lane_of_other(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+
+// Sums over lanes of two values at once: each half of the lanes goes on with
+// one of them.  Lanes 32 apart, 16 apart, then within a row of 16 by the lane
+// bit BIT (the partner differs in that bit, and in lower ones, which later
+// steps add up).
+__device__ inline float fold32(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false,
+                                                  false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ inline float fold16(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false,
+                                                  false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+template <int BIT>
+__device__ inline float fold(float a, float b) {
+  constexpr int CTRL = BIT == 8 ? 0x128 : BIT == 4 ? 0x141 : BIT == 2 ? 0x1b : 0xb1;
+  const bool up = threadIdx.x & BIT;
+  const float keep = up ? b : a, send = up ? a : b;
+  return keep + lane_of_other<CTRL>(send);
+}
+
+// The gradient walk.
+template <typename IO, int NS, int WS, bool PAD, bool GATE>
+__global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(Args A) {
+  constexpr int U = 4, Q = kScanTile / U, N = NS < 8 ? NS : 8;
+  __shared__ floatx4 marks[kWaves][Q][NS / 4][64];
+  __shared__ float meet[WS > 1 ? kWaves : 1][WS > 1 ? U : 1][3][64];
+  const Span s = span_of(A, blockIdx.x / A.ublocks);
+  const Runs rs = runs_of(A, s);
+  const Lane<NS> l = lane_of<IO, NS, WS, PAD>(A);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool real = blockIdx.x % A.ublocks * (kWaves / WS) + wave / WS < A.units;
+  const int64_t size = static_cast<int64_t>(A.D) * A.dk;
+  const int step = row_step<IO>(A);
+  float da[NS], dd = 0.f, dbias = 0.f;
+#pragma unroll
+  for (int n = 0; n < NS; ++n) da[n] = 0.f;
+
+  for (int i = rs.count; i >= (rs.cont ? 0 : 1); --i) {
+    const Run r = run_at(A, s, rs, i);
+    float g[NS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) g[n] = 0.f;
+    if (!r.ends) load_state<NS, PAD>(A, l, A.g + s.at * size, g);
+    else if (A.ds != nullptr) load_state<NS, PAD>(A, l, A.ds + r.seq * size, g);
+
+    const int tiles = static_cast<int>((r.hi - r.lo + kScanTile - 1) / kScanTile);
+    for (int k = tiles - 1; k >= 0; --k) {
+      const int64_t t0 = r.lo + k * kScanTile;
+      const int count = static_cast<int>(r.hi - t0 < kScanTile ? r.hi - t0 : kScanTile);
+      const int blocks = (count + U - 1) / U;
+      {
+        // the tile's states at every fourth token
+        float h[NS];
+        if (k == 0) {
+          enter<NS, PAD>(A, l, s, r, h);
+        } else {
+          const int64_t slot = t0 / kScanTile;
+          load_state<NS, PAD>(A, l, A.mark + slot * size, h);
+          if (r.cont) {
+            const float sum = A.msum[slot * A.D + l.ch];
+            float f[NS];
+            enter<NS, PAD>(A, l, s, r, f);
+#pragma unroll
+            for (int n = 0; n < NS; ++n) h[n] = fmaf(decay(sum, l.a2[n]), f[n], h[n]);
+          }
+        }
+        for (int q = 0;; ++q) {
+#pragma unroll
+          for (int n = 0; n < NS; n += 4)
+            marks[wave][q][n / 4][lane] = floatx4{h[n], h[n + 1], h[n + 2], h[n + 3]};
+          if (q + 1 >= blocks) break;
+          const int64_t t = t0 + q * U;
+          Rows<IO, U> x, dt;
+          x.load(A, A.x, t, U, l.row);
+          dt.load(A, A.dt, t, U, l.row);
+          Row<IO, NS, PAD> next;
+          const uintptr_t from = row_of<IO>(A, l, A.b, t);
+          next.load(from, l.left);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const Row<IO, NS, PAD> b = next;
+            b.arrive();
+            next.load(from + min(u + 1, U - 1) * step, l.left);
+            const float delta = step_of(A, dt[u], l.bias), dx = delta * x[u];
+#pragma unroll
+            for (int n = 0; n < NS; ++n) h[n] = fmaf(decay(delta, l.a2[n]), h[n], dx * b[n]);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      }
+      for (int q = blocks - 1; q >= 0; --q) {
+        // rows past the run are its last one's, with delta = x = dy = 0: the
+        // state and its gradient pass through them unchanged
+        const int64_t t = t0 + q * U;
+        const int left = static_cast<int>(r.hi - t < U ? r.hi - t : U);
+        Rows<IO, U> x, pre, dout, z{};
+        x.load(A, A.x, t, left, l.row);
+        pre.load(A, A.dt, t, left, l.row);
+        dout.load(A, A.dy, t, left, l.row);
+        if constexpr (GATE) z.load(A, A.z, t, left, l.row);
+        const uintptr_t fromb = row_of<IO>(A, l, A.b, t), fromc = row_of<IO>(A, l, A.c, t);
+        float delta[U], dx[U], dy[U], gb[U], ga[U], ys[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          delta[u] = u < left ? step_of(A, pre[u], l.bias) : 0.f;
+          dx[u] = delta[u] * x[u];
+          dy[u] = GATE ? dout[u] * z[u] * sigmoid(z[u]) : dout[u];
+          gb[u] = ga[u] = ys[u] = 0.f;
+        }
+#pragma unroll
+        for (int n0 = 0; n0 < NS; n0 += N) {
+          Row<IO, N, PAD> b[U], c[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int at = min(u, left - 1) * step + n0 * io<IO>::bytes;
+            b[u].load(fromb + at, l.left - n0);
+            c[u].load(fromc + at, l.left - n0);
+          }
+          float h[N], e[U][N], f[U][N];  // decays, decayed states
+#pragma unroll
+          for (int n = 0; n < N; n += 4) {
+            const floatx4 v = marks[wave][q][(n0 + n) / 4][lane];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) h[n + m] = v[m];
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+              e[u][n] = decay(delta[u], l.a2[n0 + n]);
+              f[u][n] = e[u][n] * h[n];
+              h[n] = fmaf(dx[u], b[u][n], f[u][n]);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) b[u].pack();
+          float fold5[2][N], fold4[2][N];
+#pragma unroll
+          for (int u = U - 1; u >= 0; --u) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+              float& gn = g[n0 + n];
+              gn = fmaf(c[u][n], dy[u], gn);
+              const float st = fmaf(dx[u], b[u][n], f[u][n]);
+              fold5[u & 1][n] = fold32(gn * dx[u], st * dy[u]);
+              if constexpr (GATE) ys[u] = fmaf(c[u][n], st, ys[u]);
+              gb[u] = fmaf(b[u][n], gn, gb[u]);
+              const float w = gn * f[u][n];
+              da[n0 + n] = fmaf(delta[u], w, da[n0 + n]);
+              ga[u] = fmaf(l.a2[n0 + n], w, ga[u]);
+              gn *= e[u][n];
+            }
+            if ((u & 1) == 0) {
+#pragma unroll
+              for (int n = 0; n < N; ++n) fold4[u >> 1][n] = fold16(fold5[0][n], fold5[1][n]);
+            }
+          }
+          // (kept here: sums that only the outputs use are else formed there,
+          // from operands kept until then)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            asm volatile("" : "+v"(gb[u]), "+v"(ga[u]));
+            if constexpr (GATE) asm volatile("" : "+v"(ys[u]));
+          }
+          // lane bits: which of db, dc; the token of the block (low bit first); the state
+          float v[N], sum;
+#pragma unroll
+          for (int n = 0; n < N; ++n) v[n] = fold<8>(fold4[0][n], fold4[1][n]);
+          int n = lane & 7;
+          bool own = real;
+          if constexpr (N == 8) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) v[m] = fold<4>(v[m], v[m + 4]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) v[m] = fold<2>(v[m], v[m + 2]);
+            sum = fold<1>(v[0], v[1]);
+          } else {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) v[m] = fold<4>(v[m], v[m + 2]);
+            sum = fold<2>(v[0], v[1]);
+            sum += lane_of_other<0xb1>(sum);
+            n = (lane >> 1) & 3;
+            own = own && (lane & 1) == 0;
+          }
+          const int at = ((lane >> 4) & 1) + ((lane >> 3) & 1) * 2;
+          if (own && at < left)
+            A.part[(((t + at) * A.units + l.unit) * WS + wave % WS) * (2 * NS) + (lane >> 5) * NS +
+                   n0 + n] = sum;
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (WS > 1) {
+          __syncthreads();
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            meet[wave][u][0][lane] = gb[u];
+            meet[wave][u][1][lane] = ga[u];
+            if constexpr (GATE) meet[wave][u][2][lane] = ys[u];
+          }
+          __syncthreads();
+        }
+        const RowsOut<IO, U> outx(A, A.dx, t, left), outt(A, A.ddt, t, left);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (WS > 1 && u % WS != wave % WS) continue;
+          float vb = gb[u], va = ga[u], vy = ys[u];
+          if constexpr (WS > 1) {
+            vb = va = vy = 0.f;
+#pragma unroll
+            for (int w = 0; w < WS; ++w) {
+              vb += meet[wave - wave % WS + w][u][0][lane];
+              va += meet[wave - wave % WS + w][u][1][lane];
+              if constexpr (GATE) vy += meet[wave - wave % WS + w][u][2][lane];
+            }
+          }
+          float v = fmaf(x[u], vb, kLn2 * va);
+          if (A.softplus) v *= sigmoid(pre[u] + l.bias);
+          dd = fmaf(dy[u], x[u], dd);
+          dbias += u < left ? v : 0.f;
+          outx.store(u, l.row, fmaf(l.d, dy[u], delta[u] * vb));
+          outt.store(u, l.row, v);
+          if constexpr (GATE) {
+            const float sg = sigmoid(z[u]);
+            RowsOut<IO, U>(A, A.dz, t, left)
+                .store(u, l.row,
+                       dout[u] * fmaf(l.d, x[u], vy) * (sg * (1.f + z[u] * (1.f - sg))));
+          }
+        }
+      }
+    }
+    if (!r.cont && A.ds0 != nullptr) store_state<NS, PAD>(A, l, A.ds0 + r.seq * size, g);
+  }
+  store_state<NS, PAD>(A, l, A.pa + s.at * size, da);
+  if (l.live) {
+    const int64_t row = static_cast<int64_t>(s.at) * WS + wave % WS;
+    A.pd[row * A.D + l.ch] = dd;
+    A.pb[row * A.D + l.ch] = dbias;
+  }
+}
+
+// db, dc: the channel blocks' shares of every token, group and state.
+template <typename IO>
+__global__ __launch_bounds__(256) void scan_bc_kernel(Args A, int64_t tokens, int NS, int WS,
+                                                      void* db, void* dc) {
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int per = 2 * A.dk;
+  const int64_t row = e / per;  // token and group
+  if (row >= tokens * A.hb) return;
+  const int k = static_cast<int>(e - row * per), n = k % A.dk, two = k / A.dk;
+  const float* p = A.part + (row * A.nb * WS + n / NS) * (2 * NS) + two * NS + n % NS;
+  float s = 0.f;
+  for (int u = 0; u < A.nb; ++u) s += p[static_cast<int64_t>(u) * WS * 2 * NS];
+  io<IO>::store(two ? dc : db, row * A.dk + n, s);
+}
+
+// da, dd, dt_bias: the rows of shares of each column added in a fixed order.
+__global__ __launch_bounds__(256) void scan_sum_kernel(const float* part, int64_t rows,
+                                                       int64_t cols, float* out) {
+  const int lc = threadIdx.x & 15, run = threadIdx.x >> 4;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 16 + lc;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < cols) {
+    for (int64_t k = run; k < rows; k += 64) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (k + 16 * u < rows) s[u] += part[(k + 16 * u) * cols + c];
+    }
+  }
+  __shared__ float t[16][17];
+  t[run][lc] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (run != 0 || c >= cols) return;
+  float v = t[0][lc];
+#pragma unroll
+  for (int k = 1; k < 16; ++k) v += t[k][lc];
+  out[c] = v;
+}
+
+// ------------------------------------------------------------------- step ---
+
+// One token of every sequence: a thread owns V adjacent channels of one head
+// and reads and writes each of their states once; memory bounds it.
+template <typename IO, int V>
+__global__ __launch_bounds__(256) void scan_step_kernel(Args A, int per) {
+  typedef float vec __attribute__((ext_vector_type(V)));
+  const int ch = (blockIdx.x * 256 + threadIdx.x) * V;
+  if (ch >= A.D) return;
+  const int head = ch / A.dv, grp = ch / A.Dg;
+  const int state = head * A.dk * A.dv + ch - head * A.dv;
+  const int64_t size = static_cast<int64_t>(A.D) * A.dk;
+  const int end = min((static_cast<int>(blockIdx.y) + 1) * per, A.nseq);
+  for (int q = blockIdx.y * per; q < end; ++q) {
+    float* p = A.sf + q * size + state;
+    float delta[V], dx[V], x[V], y[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x[v] = load_x<IO>(A.x, A, q, ch + v);
+      delta[v] = step_of(A, load_x<IO>(A.dt, A, q, ch + v), A.bias ? A.bias[ch + v] : 0.f);
+      dx[v] = delta[v] * x[v];
+      y[v] = 0.f;
+    }
+    const int64_t row = (static_cast<int64_t>(q) * A.hb + grp) * A.dk;
+    for (int n = 0; n < A.dk; n += 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float b = io<IO>::load(A.b, row + n + i), c = io<IO>::load(A.c, row + n + i);
+        vec h = *reinterpret_cast<const vec*>(p + (n + i) * A.dv);
+        const vec a = *reinterpret_cast<const vec*>(A.a + state + (n + i) * A.dv);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float w = fmaf(decay(delta[v], a[v] * kLog2e), h[v], dx[v] * b);
+          h[v] = w;
+          y[v] = fmaf(c, w, y[v]);
+        }
+        *reinterpret_cast<vec*>(p + (n + i) * A.dv) = h;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float o = y[v] + (A.d ? A.d[ch + v] * x[v] : 0.f);
+      if (A.z != nullptr) {
+        const float z = load_x<IO>(A.z, A, q, ch + v);
+        o *= z * sigmoid(z);
+      }
+      store_x<IO>(A.y, A, q, ch + v, o);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- plan ---
+
+struct Plan {
+  int ns, ws;       // states a lane, waves for a channel's states
+  bool pad;
+  int chains;       // sequences (packed: 1)
+  int64_t len;      // tokens of a chain
+  int units;        // channel blocks
+  int S, L;
+  int64_t segs;     // chains * S
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+Plan plan_scan(const Scan& p) {
+  Plan q;
+  q.ns = p.dk <= 4 ? 4 : p.dk <= 8 ? 8 : 16;
+  q.ws = p.dk <= 16 ? 1 : p.dk <= 32 ? 2 : 4;
+  q.pad = p.dk != q.ns * q.ws;
+  q.chains = p.varlen ? 1 : p.B;
+  q.len = p.T;
+  const int64_t D = static_cast<int64_t>(p.H) * p.dv, Dg = D / p.hb;
+  q.units = static_cast<int>(p.hb * ceil_div(Dg, 64));
+  int64_t L;
+  if (p.seg_req < 0) {
+    L = q.len;
+  } else if (p.seg_req > 0) {
+    L = static_cast<int64_t>(std::min(p.seg_req, 1 << 20)) * kScanTile;
+  } else {
+    const int64_t waves = static_cast<int64_t>(q.chains) * q.units * q.ws;
+    const int64_t want = std::max<int64_t>(1, ceil_div(2048, waves));  // segments of a chain
+    L = std::max<int64_t>(ceil_div(q.len, want),
+                          static_cast<int64_t>(std::sqrt(static_cast<double>(q.len))));
+    L = std::max<int64_t>(ceil_div(L, kScanTile) * kScanTile, kScanTile);
+  }
+  if (L >= q.len) L = std::max<int64_t>(q.len, 1);
+  q.L = static_cast<int>(L);
+  q.S = static_cast<int>(std::max<int64_t>(1, ceil_div(q.len, L)));
+  q.segs = static_cast<int64_t>(q.chains) * q.S;
+  return q;
+}
+
+size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Carve {  // pieces of a workspace, or their total when base is null
+  char* base;
+  size_t used;
+  template <typename T>
+  T* take(int64_t n) {
+    T* p = reinterpret_cast<T*>(base + used);
+    used += al256(static_cast<size_t>(n) * sizeof(T));
+    return p;
+  }
+};
+
+size_t carve_fwd(const Scan& p, const Plan& q, char* ws, Args* A) {
+  if (q.S == 1) return 0;
+  const int64_t D = static_cast<int64_t>(p.H) * p.dv;
+  Carve c{ws, 0};
+  A->cut = c.take<int>(q.segs);
+  A->h = c.take<float>(q.segs * D * p.dk);
+  A->sum = c.take<float>(q.segs * D);
+  return c.used;
+}
+
+size_t carve_bwd(const Scan& p, const Plan& q, char* ws, Args* A) {
+  const int64_t D = static_cast<int64_t>(p.H) * p.dv, size = D * p.dk;
+  const int64_t tokens = static_cast<int64_t>(p.B) * p.T;
+  Carve c{ws, 0};
+  if (q.S > 1) {
+    A->cut = c.take<int>(q.segs);
+    A->cutr = c.take<int>(q.segs);
+    A->h = c.take<float>(q.segs * size);
+    A->g = c.take<float>(q.segs * size);
+    A->sum = c.take<float>(q.segs * D);
+  }
+  const int64_t marks = tokens / kScanTile + 1;
+  A->mark = c.take<float>(marks * size);
+  A->msum = c.take<float>(marks * D);
+  A->part = c.take<float>(tokens * q.units * q.ws * 2 * q.ns);
+  A->pa = c.take<float>(q.segs * size);
+  A->pd = c.take<float>(q.segs * q.ws * D);
+  A->pb = c.take<float>(q.segs * q.ws * D);
+  return c.used;
+}
+
+Args make_args(const Scan& p, const Plan& q, const ScanIn& in) {
+  Args A{};
+  A.x = in.x;
+  A.dt = in.dt;
+  A.a = in.a;
+  A.b = in.b;
+  A.c = in.c;
+  A.d = in.d;
+  A.bias = in.bias;
+  A.z = in.z;
+  A.s0 = in.s0;
+  A.T = q.len;
+  A.D = p.H * p.dv;
+  A.Dg = A.D / p.hb;
+  A.nb = (A.Dg + 63) / 64;
+  A.units = q.units;
+  A.ublocks = static_cast<int>(ceil_div(q.units, kWaves / q.ws));
+  A.dk = p.dk;
+  A.dv = p.dv;
+  A.hb = p.hb;
+  A.S = q.S;
+  A.L = q.L;
+  A.nseq = p.nseq;
+  A.softplus = p.softplus ? 1 : 0;
+  A.cu = p.varlen ? p.cu_seqlens : nullptr;
+  return A;
+}
+
+template <typename IO, int NS, bool PAD>
+void launch_local(const Args& A, const Plan& q, int64_t segs, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(A.ublocks * segs));
+  hipLaunchKernelGGL((scan_local_kernel<IO, NS, PAD>), grid, dim3(kThreads), 0, s, A, q.ws);
+}
+
+template <typename IO, int NS, int WS, bool PAD, bool GATE>
+void launch_out(const Args& A, const Plan& q, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(A.ublocks * q.segs));
+  hipLaunchKernelGGL((scan_out_kernel<IO, NS, WS, PAD, GATE>), grid, dim3(kThreads), 0, s, A);
+}
+
+void launch_sum(const float* part, int64_t rows, int64_t cols, float* out, hipStream_t s) {
+  if (out == nullptr) return;
+  hipLaunchKernelGGL(scan_sum_kernel, dim3(static_cast<unsigned>(ceil_div(cols, 16))), dim3(256),
+                     0, s, part, rows, cols, out);
+}
+
+// Calls f<NS, WS, PAD, GATE> of a plan.
+template <typename F>
+void with_plan(const Plan& q, bool gate, F f) {
+  using std::integral_constant;
+  const integral_constant<int, 1> one;
+  auto all = [&](auto ns, auto ws, auto pad) {
+    if (gate) f(ns, ws, pad, std::true_type{});
+    else f(ns, ws, pad, std::false_type{});
+  };
+  auto pad = [&](auto ns, auto ws) {
+    if (q.pad) all(ns, ws, std::true_type{});
+    else all(ns, ws, std::false_type{});
+  };
+  if (q.ns == 4) return all(integral_constant<int, 4>{}, one, std::false_type{});
+  if (q.ns == 8) return all(integral_constant<int, 8>{}, one, std::false_type{});
+  if (q.ws == 1) return pad(integral_constant<int, 16>{}, one);
+  if (q.ws == 2) return pad(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  return pad(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+}
+
+template <typename IO>
+hipError_t scan_fwd(const Plan& q, const Args& A, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  if (q.S > 1) {
+    {
+      StageScope scope(GDN_STAGE_FWD_TRANS, s);
+      with_plan(q, false, [&](auto ns, auto, auto pad, auto) {
+        launch_local<IO, ns, pad>(A, q, static_cast<int64_t>(q.chains) * (q.S - 1), s);
+      });
+      e = hipGetLastError();
+    }
+    if (e != hipSuccess) return e;
+    {
+      StageScope scope(GDN_STAGE_FWD_COMBINE, s);
+      const int64_t blocks = ceil_div(static_cast<int64_t>(A.D) * A.dk, 256);
+      const dim3 grid(static_cast<unsigned>(blocks * q.chains));
+      hipLaunchKernelGGL(scan_chain_kernel, grid, dim3(256), 0, s, A);
+      e = hipGetLastError();
+    }
+    if (e != hipSuccess) return e;
+  }
+  StageScope scope(GDN_STAGE_FWD_SCAN, s);
+  with_plan(q, A.z != nullptr, [&](auto ns, auto ws, auto pad, auto gate) {
+    launch_out<IO, ns, ws, pad, gate>(A, q, s);
+  });
+  return hipGetLastError();
+}
+
+template <typename IO>
+hipError_t scan_bwd(const Plan& q, const Args& A, int64_t tokens, const ScanGrad& out,
+                    hipStream_t s) {
+  const int64_t size = static_cast<int64_t>(A.D) * A.dk;
+  hipError_t e;
+  {
+    StageScope scope(GDN_STAGE_BWD_STATES, s);
+    with_plan(q, A.z != nullptr, [&](auto ns, auto, auto pad, auto gate) {
+      hipLaunchKernelGGL((scan_marks_kernel<IO, ns, pad, gate>),
+                         dim3(static_cast<unsigned>(A.ublocks * q.segs)), dim3(kThreads), 0, s, A,
+                         q.ws);
+    });
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess) return e;
+  if (q.S > 1) {
+    StageScope scope(GDN_STAGE_BWD_SCAN, s);
+    const dim3 grid(static_cast<unsigned>(ceil_div(size, 256) * q.chains));
+    hipLaunchKernelGGL(scan_chain_kernel, grid, dim3(256), 0, s, A);
+    hipLaunchKernelGGL(scan_chain_back_kernel, grid, dim3(256), 0, s, A);
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess) return e;
+  StageScope scope(GDN_STAGE_BWD_GRAD, s);
+  with_plan(q, A.z != nullptr, [&](auto ns, auto ws, auto pad, auto gate) {
+    hipLaunchKernelGGL((scan_grad_kernel<IO, ns, ws, pad, gate>),
+                       dim3(static_cast<unsigned>(A.ublocks * q.segs)), dim3(kThreads), 0, s, A);
+  });
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (tokens > 0)
+    hipLaunchKernelGGL((scan_bc_kernel<IO>),
+                       dim3(static_cast<unsigned>(ceil_div(tokens * A.hb * 2 * A.dk, 256))),
+                       dim3(256), 0, s, A, tokens, q.ns, q.ws, out.db, out.dc);
+  launch_sum(A.pa, q.segs, size, out.da, s);
+  launch_sum(A.pd, q.segs * q.ws, A.D, out.dd, s);
+  launch_sum(A.pb, q.segs * q.ws, A.D, out.dbias, s);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool scan_fits(const Scan& p) {
+  // every launch below 2^32 threads
+  const Plan q = plan_scan(p);
+  const int64_t most = (int64_t(1) << 32) / kThreads - 1;
+  const int64_t state = ceil_div(static_cast<int64_t>(p.H) * p.dv * p.dk, 256);
+  const int64_t rows = static_cast<int64_t>(p.B) * p.T;
+  return q.segs <= most / std::max<int64_t>(ceil_div(q.units, kWaves / q.ws), state) &&
+         rows <= most * 256 / (2 * p.dk) / p.hb;
+}
+
+size_t scan_fwd_workspace_bytes(const Scan& p) {
+  Args A{};
+  return carve_fwd(p, plan_scan(p), nullptr, &A);
+}
+
+hipError_t launch_scan_fwd(const Scan& p, const ScanIn& in, void* y, float* s_final, void* ws,
+                           hipStream_t s) {
+  const Plan q = plan_scan(p);
+  Args A = make_args(p, q, in);
+  carve_fwd(p, q, static_cast<char*>(ws), &A);
+  A.y = y;
+  A.sf = s_final;
+  return p.io == GDN_BF16 ? scan_fwd<bf16_t>(q, A, s) : scan_fwd<f32_t>(q, A, s);
+}
+
+size_t scan_bwd_workspace_bytes(const Scan& p) {
+  Args A{};
+  return carve_bwd(p, plan_scan(p), nullptr, &A);
+}
+
+hipError_t launch_scan_bwd(const Scan& p, const ScanIn& in, const void* dy, const float* ds_final,
+                           const ScanGrad& out, void* ws, hipStream_t s) {
+  const Plan q = plan_scan(p);
+  Args A = make_args(p, q, in);
+  carve_bwd(p, q, static_cast<char*>(ws), &A);
+  A.dy = dy;
+  A.ds = ds_final;
+  A.dx = out.dx;
+  A.ddt = out.ddt;
+  A.dz = out.dz;
+  A.ds0 = out.ds0;
+  const int64_t tokens = static_cast<int64_t>(p.B) * p.T;
+  return p.io == GDN_BF16 ? scan_bwd<bf16_t>(q, A, tokens, out, s)
+                          : scan_bwd<f32_t>(q, A, tokens, out, s);
+}
+
+hipError_t launch_scan_step(const Scan& p, const ScanIn& in, float* state, void* y,
+                            hipStream_t s) {
+  Args A = make_args(p, plan_scan(p), in);
+  A.y = y;
+  A.sf = state;
+  const int V = p.dv % 4 == 0 ? 4 : 1;
+  const int64_t blocks = ceil_div(A.D / V, 256);
+  const int per = static_cast<int>(std::max<int64_t>(1, blocks * p.nseq / 2048));
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(ceil_div(p.nseq, per)));
+  StageScope scope(GDN_STAGE_DECODE, s);
+  auto go = [&](auto io_tag) {
+    using IO = decltype(io_tag);
+    if (V == 4) hipLaunchKernelGGL((scan_step_kernel<IO, 4>), grid, dim3(256), 0, s, A, per);
+    else hipLaunchKernelGGL((scan_step_kernel<IO, 1>), grid, dim3(256), 0, s, A, per);
+  };
+  if (p.io == GDN_BF16) go(bf16_t{});
+  else go(f32_t{});
+  return hipGetLastError();
+}
+
+}  // namespace gdn

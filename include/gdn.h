@@ -501,6 +501,136 @@ gdn_status gdn_group_norm_bwd(const gdn_problem* p, int32_t d, int32_t act, int3
                               void* dz, float* dw, float* db, void* ws, size_t ws_bytes,
                               void* stream);
 
+/* Selective state space scan: a state of dk values for each of the dv
+ * channels of every head,
+ *   delta_t = softplus(dt_t + dt_bias)      (softplus != 0; else dt_t + dt_bias)
+ *   S_t[n, j] = exp(delta_t[j] a[n, j]) S_{t-1}[n, j] + delta_t[j] x_t[j] b_t[n]
+ *   y_t[j] = (sum_n c_t[n] S_t[n, j] + d[j] x_t[j]) * silu(z_t[j])
+ * the recurrence whose decay and write depend on the token, the channel and
+ * the state, next to the matrix-valued ones above.
+ *   p         : B, T, H, dk, dv, nseq, cu_seqlens, io_dtype and seg_chunks as
+ *               in the chunked calls (seg_chunks counts 16 tokens; packed
+ *               sequences are cut on the grid of all tokens; < 0 walks a
+ *               packed batch as one); gate must be GDN_GATE_NONE; chunk and
+ *               gate_dtype are ignored.  dk: a multiple of 4 up to 64; dv >= 1;
+ *               H dv <= 2^22 (else GDN_ERR_UNSUPPORTED).
+ *   hb        : rows of b and c of a token; head h reads row h / (H / hb).
+ *               hb in 1 .. H dividing H, else GDN_ERR_SHAPE.
+ *   x, dt, z, y : [B, T, H, dv] io_dtype; z NULL = no gate.
+ *   b, c      : [B, T, hb, dk] io_dtype.
+ *   a         : [H, dk, dv] fp32 (laid out as a state), finite, normally < 0.
+ *   d, dt_bias : [H, dv] fp32, each may be NULL (zeros).
+ *   s0, s_final : [nseq, H, dk, dv] fp32 or NULL, as in gdn_chunk_fwd.
+ *   ws        : at least gdn_selective_scan_fwd_workspace bytes; calls that
+ *               overlap in time (streams, captured graphs) need one each.
+ * All arithmetic is fp32, the state too.  Rows of packed tensors behind
+ * cu_seqlens[nseq] are neither read nor written.  A NaN or infinity in a
+ * token stays in its sequence.  Deterministic.  Errors as gdn_chunk_fwd;
+ * GDN_ERR_SHAPE where a launch would take 2^32 threads. */
+gdn_status gdn_selective_scan_fwd_workspace(const gdn_problem* p, int32_t hb, size_t* bytes);
+gdn_status gdn_selective_scan_fwd(const gdn_problem* p, int32_t hb, int32_t softplus,
+                                  const void* x, const void* dt, const float* a, const void* b,
+                                  const void* c, const float* d, const float* dt_bias,
+                                  const void* z, const float* s0, void* y, float* s_final,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/* Backward of gdn_selective_scan_fwd: gradients of <dy, y> + <ds_final,
+ * s_final> with respect to every input, the states formed again inside.
+ *   dx, ddt, dz [B, T, H, dv] and db, dc [B, T, hb, dk] in io_dtype (dz only
+ *   with z); da [H, dk, dv], dd, ddt_bias [H, dv] and ds0 [nseq, H, dk, dv]
+ *   fp32; dd, ddt_bias and ds0 may be NULL to skip them, ds_final NULL = zeros.
+ * Sums over tokens and channels run in a fixed order (deterministic). */
+gdn_status gdn_selective_scan_bwd_workspace(const gdn_problem* p, int32_t hb, size_t* bytes);
+gdn_status gdn_selective_scan_bwd(const gdn_problem* p, int32_t hb, int32_t softplus,
+                                  const void* x, const void* dt, const float* a, const void* b,
+                                  const void* c, const float* d, const float* dt_bias,
+                                  const void* z, const float* s0, const void* dy,
+                                  const float* ds_final, void* dx, void* ddt, float* da, void* db,
+                                  void* dc, float* dd, float* ddt_bias, void* dz, float* ds0,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/* One token per sequence of the same rule (B = N sequences), state updated
+ * in place; each state element is read once and written once.  x, dt, z, y
+ * [N, H, dv]; b, c [N, hb, dk]; state [N, H, dk, dv] fp32.  T, chunk, nseq,
+ * cu_seqlens and seg_chunks of the problem are ignored. */
+gdn_status gdn_selective_scan_step(const gdn_problem* p, int32_t hb, int32_t softplus,
+                                   const void* x, const void* dt, const float* a, const void* b,
+                                   const void* c, const float* d, const float* dt_bias,
+                                   const void* z, float* state, void* y, void* stream);
+
+/* Short causal depthwise convolution with a carried history: the step in
+ * front of the scan, and of a block's q, k, v paths where a sequence is
+ * resumed or decoded (gdn_prologue_fwd starts every sequence from nothing).
+ *   y[t, h, c] = act(bias[h, c] + sum_{j < width} taps[h, c, j] x[t - j, h, c])
+ * where the inputs in front of a sequence's first token are its history.
+ *   p         : B, T, H, dv, nseq, cu_seqlens and io_dtype are used: x, y
+ *               [B, T, H, dv], dv >= 1, H dv <= 2^22.
+ *   width     : 1 .. 8 (else GDN_ERR_UNSUPPORTED).   act : gdn_act.
+ *   taps      : [H, dv, width] fp32.   bias : [H, dv] fp32 or NULL.
+ *   s0, s_final : [nseq, width - 1, H, dv] io_dtype, a sequence's last
+ *               width - 1 inputs, oldest first; s0 NULL = zeros, s_final NULL
+ *               to skip it.  s_final must not be s0.
+ * Rows behind cu_seqlens[nseq] are neither read nor written. */
+gdn_status gdn_short_conv_fwd(const gdn_problem* p, int32_t width, int32_t act, const void* x,
+                              const float* taps, const float* bias, const void* s0, void* y,
+                              void* s_final, void* stream);
+
+/* Backward of gdn_short_conv_fwd: gradients of <dy, y> + <ds_final, s_final>.
+ * dx and ds0 in io_dtype, dtaps and dbias fp32 (overwritten; dbias and ds0
+ * may be NULL to skip them, ds_final NULL = zeros).  Sums over tokens run in
+ * a fixed order (deterministic). */
+gdn_status gdn_short_conv_bwd_workspace(const gdn_problem* p, int32_t width, size_t* bytes);
+gdn_status gdn_short_conv_bwd(const gdn_problem* p, int32_t width, int32_t act, const void* x,
+                              const float* taps, const float* bias, const void* s0,
+                              const void* dy, const void* ds_final, void* dx, float* dtaps,
+                              float* dbias, void* ds0, void* ws, size_t ws_bytes, void* stream);
+
+/* One token per sequence (B = N sequences): x, y [N, H, dv]; state
+ * [N, width - 1, H, dv] io_dtype, moved up by the token in place (may be NULL
+ * for width 1).  y may be x. */
+gdn_status gdn_short_conv_step(const gdn_problem* p, int32_t width, int32_t act, const void* x,
+                               const float* taps, const float* bias, void* state, void* y,
+                               void* stream);
+
+/* Acceptance of drafted tokens against the target's probabilities, from given
+ * uniform numbers: what decides between gdn_tree_verify and gdn_tree_commit
+ * (speculative sampling; the next tokens are distributed as the target's).
+ * The walk starts at a sequence's root and tries the children of where it
+ * stands in index order, r the target's row there, Z = 1, q the draft's:
+ *   child i of token x is accepted when u[i] q(x) Z < r(x), and the walk goes
+ *   on from it; else r <- max(r / Z - q, 0), Z <- sum r (r and Z stay where
+ *   nothing would be left).
+ * With no child left the next token is the first whose running sum of r
+ * exceeds u[last] sum(r), or the last with r > 0 where rounding leaves none.
+ *   p         : B trees of T nodes, T <= 64 (else GDN_ERR_SHAPE), or nseq
+ *               trees packed by cu_seqlens (B == 1; of more than 64 nodes the
+ *               first 64 are tried, and the answer is unspecified); io_dtype
+ *               is that of the probabilities; the rest is ignored.
+ *   vocab     : 1 .. 2^28.
+ *   parent    : device int32 as in gdn_tree_verify, or NULL for chains (node
+ *               i continues node i - 1).
+ *   tokens    : device int32, [B, T] or [nodes]; a token outside [0, vocab)
+ *               is not tried (and ends a chain).
+ *   target    : [B, T + 1, vocab] or [nodes + nseq, vocab]: row 0 of a tree
+ *               holds the probabilities behind the committed tokens, row
+ *               i + 1 those behind node i.  Values that are NaN count as 0.
+ *   draft     : the draft's, laid out the same (rows of nodes without
+ *               children are not read), or NULL: q is 1 at the drafted token.
+ *   uniform   : [B, T + 1] or [nodes + nseq] fp32 in [0, 1): one for each
+ *               node, then the last for the next token.
+ *   accepted  : int32 [trees], the last accepted node or -1 (what
+ *               gdn_tree_commit takes);  length : accepted nodes;
+ *   next_token : the token behind them.
+ *   ws        : at least gdn_draft_accept_workspace bytes (tree: parent is
+ *               given).
+ * Sums are 64 bits.  Deterministic. */
+gdn_status gdn_draft_accept_workspace(const gdn_problem* p, int32_t vocab, int32_t tree,
+                                      size_t* bytes);
+gdn_status gdn_draft_accept(const gdn_problem* p, int32_t vocab, const int32_t* parent,
+                            const int32_t* tokens, const void* target, const void* draft,
+                            const float* uniform, int32_t* accepted, int32_t* length,
+                            int32_t* next_token, void* ws, size_t ws_bytes, void* stream);
+
 /* Stage timing, for benchmarks and profiling.  While enabled, every kernel
  * the library enqueues is bracketed by a pair of HIP events recorded on the
  * same stream.  gdn_profile_read waits for the recorded events, writes the

@@ -59,3 +59,11 @@ from .linattn_oracle import (  # noqa: F401
     group_norm_fwd,
     group_norm_bwd,
 )
+from .scan_oracle import (  # noqa: F401
+    scan_delta,
+    scan_fwd,
+    scan_bwd,
+    conv_fwd,
+    conv_bwd,
+    accept,
+)

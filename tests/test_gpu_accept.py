@@ -1,0 +1,260 @@
+"""Draft acceptance on the GPU against the fp64 oracle: whole numbers, equal.
+
+Both sides sum in 64 bits in orders of their own, so a decision could differ
+only where a uniform number lies within 2^-40 of a border: seeds are fixed and
+none does."""
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_79_amd as gdn
+import oracle
+from gpu_util import Padded, log
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def make(sizes, V, dtype, tree, drawn=True, seed=1, far=0.5, peak=2.0):
+    """Packed trees of the given sizes: drafts from the draft's rows."""
+    g = torch.Generator().manual_seed(seed)
+    rows = sum(sizes) + len(sizes)
+    logits = torch.randn(rows, V, generator=g) * peak
+    q = torch.softmax(logits, -1).to(dtype)
+    p = torch.softmax(logits + far * torch.randn(rows, V, generator=g), -1).to(dtype)
+    tokens, parent, row = [], [], 0
+    for n in sizes:
+        par = [i - 1 if not tree else int(torch.randint(-1, i, (1,), generator=g)) if i else -1
+               for i in range(n)]
+        parent += par
+        for k in par:
+            src = q[row + k + 1].float()
+            tokens.append(int(torch.multinomial(src if drawn else src.square(), 1, generator=g)))
+        row += n + 1
+    return dict(tokens=torch.tensor(tokens, dtype=torch.int32), target=p,
+                draft=q if drawn else None, uniform=torch.rand(rows, generator=g),
+                parent=torch.tensor(parent, dtype=torch.int32) if tree else None)
+
+
+def reference(d, sizes):
+    f = lambda t: None if t is None else t.double().numpy()  # noqa: E731
+    p, q, u = f(d["target"]), f(d["draft"]), d["uniform"].numpy()
+    out, node = [], 0
+    for m, n in enumerate(sizes):
+        row = slice(node + m, node + m + n + 1)
+        at = slice(node, node + n)
+        out.append(oracle.accept(d["tokens"].numpy()[at], p[row], None if q is None else q[row],
+                                 u[row], None if d["parent"] is None else d["parent"].numpy()[at]))
+        node += n
+    return np.array(out).T
+
+
+def run(d, sizes, packed):
+    g = {k: None if t is None else t.cuda() for k, t in d.items()}
+    if packed:
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32, device="cuda")
+        out = gdn.draft_accept(g["tokens"], g["target"], g["draft"], g["uniform"], g["parent"], cu)
+    else:
+        B, n = len(sizes), sizes[0]
+        lead = lambda t, k: None if t is None else t.view(B, k, *t.shape[1:])  # noqa: E731
+        out = gdn.draft_accept(lead(g["tokens"], n), lead(g["target"], n + 1),
+                               lead(g["draft"], n + 1), lead(g["uniform"], n + 1),
+                               lead(g["parent"], n))
+    torch.cuda.synchronize()
+    return np.stack([t.cpu().numpy() for t in out])
+
+
+def check(d, sizes, packed=True):
+    want, got = reference(d, sizes), run(d, sizes, packed)
+    log(f"    accepted {want[1].mean():.2f} of {np.mean(sizes):.2f}")
+    assert np.array_equal(got, want), np.nonzero(got != want)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("drawn", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [1, 3, 100, 257, 2048, 5001, 32000])
+def test_packed_batches(gpu_lib, V, dtype, drawn, tree):
+    log(f"[accept] V {V} {dtype} drawn {drawn} tree {tree}")
+    sizes = [0, 5, 1, 16, 0, 3, 64, 8] if V < 5000 else [4, 0, 16]
+    check(make(sizes, V, dtype, tree, drawn), sizes)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("B,n,V", [(1, 0, 50), (1, 1, 131072), (3, 8, 70001), (40, 6, 512),
+                                   (300, 3, 128)])
+def test_dense_batches(gpu_lib, B, n, V, tree):
+    for dtype in (F32, BF16):
+        check(make([n] * B, V, dtype, tree, seed=B), [n] * B, packed=False)
+
+
+@pytest.mark.parametrize("far,seed", [(0.0, 1), (0.05, 2), (2.0, 3), (6.0, 4)])
+def test_near_and_far_drafts(gpu_lib, far, seed):
+    # drafts of the target's own rows are all accepted; of far ones few are
+    for tree in (False, True):
+        sizes = [12] * 20
+        d = make(sizes, 300, F32, tree, far=far, seed=seed, peak=3.0)
+        check(d, sizes)
+        if far == 0.0:
+            got = run(d, sizes, True)
+            assert tree or (got[1] == 12).all()
+
+
+def test_many_rejected_siblings(gpu_lib):
+    # a star: every child of the root may be rejected, one residual after another
+    sizes = [40] * 30
+    d = make(sizes, 64, F32, True, far=4.0, seed=9)
+    d["parent"][:] = -1
+    for m in range(30):
+        row = torch.softmax(torch.randn(64, generator=torch.Generator().manual_seed(m)) * 2, 0)
+        d["tokens"][m * 40:(m + 1) * 40] = torch.multinomial(
+            d["draft"][m * 41], 40, replacement=True,
+            generator=torch.Generator().manual_seed(m)).int()
+        d["target"][m * 41] = row
+    check(d, sizes)
+    d["draft"] = None  # and the same token again and again
+    check(d, sizes)
+
+
+def test_numbers_at_the_ends(gpu_lib):
+    sizes = [6] * 8
+    for u in (0.0, 1.0 - 2.0 ** -24):
+        for tree in (False, True):
+            d = make(sizes, 700, F32, tree, seed=11)
+            d["uniform"][:] = u
+            check(d, sizes)
+
+
+def test_nothing_left_keeps_the_row(gpu_lib):
+    # target below draft everywhere it is tried: nothing would be left
+    V = 40
+    for tree in (False, True):
+        d = make([2], V, F32, tree, seed=3)
+        d["target"][:] = d["draft"] * 0.5
+        d["uniform"][:2] = 0.9
+        check(d, [2])
+    # a row of zeros draws the last token
+    d["target"][:] = 0.0
+    assert run(d, [2], True)[2, 0] == V - 1
+
+
+def test_sparse_rows_and_nan(gpu_lib):
+    V = 9000
+    for tree in (False, True):
+        d = make([3] * 6, V, F32, tree, seed=5)
+        keep = torch.zeros(V, dtype=torch.bool)
+        keep[[0, 17, 4096, 8999]] = True
+        d["target"] = torch.where(keep, d["target"], 0.0)
+        d["target"] /= d["target"].sum(-1, keepdim=True)
+        check(d, [3] * 6)
+        e = {k: None if t is None else t.clone() for k, t in d.items()}
+        e["target"][:, 100] = float("nan")  # counts nothing
+        assert np.array_equal(run(e, [3] * 6, True), run(d, [3] * 6, True))
+
+
+def test_tokens_that_are_none(gpu_lib):
+    for tree in (False, True):
+        d = make([8] * 10, 90, F32, tree, far=0.1, seed=6)
+        d["tokens"][3::8] = -1
+        d["tokens"][6::8] = 90
+        check(d, [8] * 10)
+
+
+def test_parents_out_of_range_are_the_root(gpu_lib):
+    d = make([5] * 6, 60, F32, True, seed=8)
+    d["parent"][2::5] = 7
+    d["parent"][3::5] = -9
+    d["parent"][4::5] = 4
+    check(d, [5] * 6)
+
+
+def test_bounds_out_of_order_stay_in_range(gpu_lib):
+    d = make([5] * 4, 3000, F32, True)
+    g = {k: t.cuda() for k, t in d.items()}
+    for cu in ([0, 30, 10, 99, -4], [20, 20, 0, 7, 1000]):
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        for parent in (None, g["parent"]):
+            out = [Padded((4,), torch.int32) for _ in range(3)]
+            gdn.draft_accept(g["tokens"], g["target"], g["draft"], g["uniform"], parent, c,
+                             out=[o.t for o in out])
+            torch.cuda.synchronize()
+            for o in out:
+                o.check("out")
+
+
+def test_captured_and_replayed(gpu_lib):
+    sizes = [7] * 9
+    sets = [make(sizes, 5000, F32, True, seed=s) for s in range(4)]
+    g = {k: t.cuda() for k, t in sets[0].items()}
+    cu = torch.arange(0, 64, 7, dtype=torch.int32, device="cuda")
+    for parent in (None, g["parent"]):
+        work = lambda: gdn.draft_accept(g["tokens"], g["target"], g["draft"],  # noqa: E731
+                                        g["uniform"], parent, cu)
+        work()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = work()
+        for d in sets:
+            for k in g:
+                g[k].copy_(d[k])
+            graph.replay()
+            torch.cuda.synchronize()
+            e = dict(d, parent=None if parent is None else d["parent"])
+            assert np.array_equal(np.stack([t.cpu().numpy() for t in out]), reference(e, sizes))
+
+
+def test_two_streams_at_once(gpu_lib):
+    sets = [make([9] * 5, 40000, F32, False, seed=s) for s in (1, 2)]
+    gs = [{k: None if t is None else t.cuda() for k, t in d.items()} for d in sets]
+    cu = torch.arange(0, 46, 9, dtype=torch.int32, device="cuda")
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        out = []
+        for g, s in zip(gs, streams):
+            with torch.cuda.stream(s):
+                out.append(gdn.draft_accept(g["tokens"], g["target"], g["draft"], g["uniform"],
+                                            None, cu))
+        torch.cuda.synchronize()
+        for o, d in zip(out, sets):
+            assert np.array_equal(np.stack([t.cpu().numpy() for t in o]), reference(d, [9] * 5))
+
+
+def test_offsets_past_four_gigabytes(gpu_lib):
+    # the last tree's rows lie past 2^32 bytes
+    V, n, B = 131072, 64, 132
+    d = make([n], V, F32, False, far=0.02, seed=2)
+    target = torch.zeros(B, n + 1, V, device="cuda")
+    assert target.numel() * 4 > 1 << 32
+    target[-1] = d["target"].cuda()
+    draft = torch.zeros_like(target)
+    draft[-1] = d["draft"].cuda()
+    tokens = torch.zeros(B, n, dtype=torch.int32, device="cuda")
+    tokens[-1] = d["tokens"].cuda()
+    u = torch.zeros(B, n + 1, device="cuda")
+    u[-1] = d["uniform"].cuda()
+    for parent in (None, torch.arange(-1, n - 1, dtype=torch.int32, device="cuda").repeat(B, 1)):
+        out = gdn.draft_accept(tokens, target, draft, u, parent)
+        assert [int(t[-1]) for t in out] == list(reference(d, [n])[:, 0])
+
+
+def test_refusals(gpu_lib):
+    d = make([4] * 2, 50, F32, False)
+    g = dict(tokens=d["tokens"].view(2, 4).cuda(), target=d["target"].view(2, 5, 50).cuda(),
+             draft=d["draft"].view(2, 5, 50).cuda(), uniform=d["uniform"].view(2, 5).cuda())
+    bad = [dict(tokens=g["tokens"].long()), dict(tokens=g["tokens"].cpu()),
+           dict(target=g["target"][:, :4].contiguous()), dict(draft=g["draft"].to(BF16)),
+           dict(uniform=g["uniform"].double()), dict(parent=g["tokens"][:1]),
+           dict(target=g["target"].double(), draft=None), dict(target=g["target"].transpose(0, 1)),
+           dict(cu_seqlens=torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")),
+           dict(out=[g["tokens"][:, 0]] * 3)]
+    for kw in bad:
+        with pytest.raises((ValueError, TypeError, gdn.GdnError)):
+            gdn.draft_accept(**{**g, **kw})
+    big = torch.zeros(1, 65, dtype=torch.int32, device="cuda")
+    with pytest.raises(gdn.GdnError):
+        gdn.draft_accept(big, torch.zeros(1, 66, 8, device="cuda"), None,
+                         torch.zeros(1, 66, device="cuda"))
