@@ -37,45 +37,38 @@ namespace gdn {
 
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
+// Waves of a workgroup whose channel blocks take ws waves each.
+constexpr int waves_of(int ws) { return ws > 4 ? ws : 4; }
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLog2eLow = 1.92596303e-8f;  // log2(e) - kLog2e
 constexpr float kLn2 = 0.69314718055994530942f;
 
 #define GDN_CONST __attribute__((address_space(4)))
 
 // ------------------------------------------------------------- functions ---
 
-// e^{-x} for x >= 0: the part of x log2(e) that its product loses goes back in
-__device__ inline float exp_neg(float x) {
-  x = x > 104.f ? 104.f : x;  // (a NaN stays)
-  const float t = -x * kLog2e;
-  const float low = fmaf(-x, kLog2e, -t) - x * kLog2eLow;
+// e^x; what the product x log2(e) loses goes back in (a large |x| ends at
+// infinity or zero by itself)
+__device__ inline float exp_full(float x) {
+  const float t = x * kLog2e;
   const float e = __builtin_amdgcn_exp2f(t);
-  return fmaf(e * kLn2, low, e);
+  return fmaf(e * kLn2, fmaf(x, kLog2e, -t), e);
 }
 
-// softplus(v) = max(v, 0) + log(1 + e^{-|v|}), the logarithm as
-// 2 artanh(u / (2 + u)) with u = e^{-|v|} <= 1: the series in s^2 <= 1/9 ends
-// below 2^-24 after eight terms, and a small u keeps all its bits.
+// softplus(v) = max(v, 0) + log(1 + u), u = e^{-|v|}: w = 1 + u is off by
+// d = u - (w - 1), log(w + d) = log(w) + d to 2^-25 of the result.
 __device__ inline float softplus(float v) {
-  const float u = exp_neg(fabsf(v));
-  const float s = u * __builtin_amdgcn_rcpf(2.f + u), q = s * s;
-  float p = 1.f / 15.f;
-  p = fmaf(p, q, 1.f / 13.f);
-  p = fmaf(p, q, 1.f / 11.f);
-  p = fmaf(p, q, 1.f / 9.f);
-  p = fmaf(p, q, 1.f / 7.f);
-  p = fmaf(p, q, 1.f / 5.f);
-  p = fmaf(p, q, 1.f / 3.f);
-  p = fmaf(p, q, 1.f);
-  return (v > 0.f ? v : 0.f) + 2.f * s * p;
+  const float x = -fabsf(v), u = x < -104.f ? 0.f : exp_full(x);
+  const float w = 1.f + u;
+  return (v > 0.f ? v : 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), u - (w - 1.f));
 }
 
+// bf16 rows take the exponential as it is (its error, |v| 2^-24, is far below
+// their rounding)
+template <typename IO>
 __device__ inline float sigmoid(float v) {
-  const float u = exp_neg(fabsf(v)), r = __builtin_amdgcn_rcpf(1.f + u);
-  return v >= 0.f ? r : u * r;
+  const float e = io<IO>::bytes == 2 ? __builtin_amdgcn_exp2f(-v * kLog2e)
+                                     : v < -87.f ? INFINITY : v > 104.f ? 0.f : exp_full(-v);
+  return __builtin_amdgcn_rcpf(1.f + e);
 }
 
 // ------------------------------------------------------------------ sizes ---
@@ -235,11 +228,11 @@ __device__ inline void store_state(const Args& A, const Lane<NS>& l, float* p, c
       __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(h[i]), b, l.state, 4 * i * A.dv, 0);
 }
 
-template <typename IO, int NS, int WS, bool PAD>
-__device__ inline Lane<NS> lane_of(const Args& A) {
+template <typename IO, int NS, bool PAD>
+__device__ inline Lane<NS> lane_of(const Args& A, int WS) {
   Lane<NS> l;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int unit = blockIdx.x % A.ublocks * (kWaves / WS) + wave / WS;
+  const int unit = blockIdx.x % A.ublocks * (waves_of(WS) / WS) + wave / WS;
   l.unit = min(unit, A.units - 1);
   l.grp = l.unit / A.nb;
   const int j = (l.unit - l.grp * A.nb) * 64 + lane;
@@ -413,12 +406,11 @@ __device__ inline void walk(const Args& A, const Lane<NS>& l, const Run& r, F f)
 // State behind a segment: from its last run, walked from its sequence's
 // initial state or, where it continues the segment in front, from zero.
 template <typename IO, int NS, bool PAD>
-__global__ __launch_bounds__(kThreads) void scan_local_kernel(Args A, int WS) {
+__global__ __launch_bounds__(512) void scan_local_kernel(Args A, int WS) {
   const int k = blockIdx.x / A.ublocks;
   const Span s = span_of(A, k + k / (A.S - 1));  // (no last segment of a sequence)
   const Runs rs = runs_of(A, s);
-  Lane<NS> l = WS == 1 ? lane_of<IO, NS, 1, PAD>(A)
-               : WS == 2 ? lane_of<IO, NS, 2, PAD>(A) : lane_of<IO, NS, 4, PAD>(A);
+  const Lane<NS> l = lane_of<IO, NS, PAD>(A, WS);
   const int64_t size = static_cast<int64_t>(A.D) * A.dk;
   int i = rs.count;
   Run r{};
@@ -445,35 +437,65 @@ __global__ __launch_bounds__(kThreads) void scan_local_kernel(Args A, int WS) {
   if (blockIdx.x % A.ublocks == 0 && threadIdx.x == 0) A.cut[s.at] = none || !r.cont;
 }
 
-// Chains the segments' states: every one is replaced by the state in front of
-// its segment.  One thread a channel and state; eight segments in flight.
-__global__ __launch_bounds__(256) void scan_chain_kernel(Args A) {
-  const int64_t size = static_cast<int64_t>(A.D) * A.dk;
-  const unsigned blocks = (size + 255) / 256;
-  const int64_t e = static_cast<int64_t>(blockIdx.x % blocks) * 256 + threadIdx.x;
-  if (e >= size) return;
+// Chains the segments' states, every one replaced by the state in front of its
+// segment, and (second half of the grid) the gradients, every one replaced by
+// the gradient of the state behind its segment.  A wave chains a share of the
+// segments of 64 channels and states, the shares meet in LDS, and every wave
+// goes over its own again: 128 segments of 65536 values 9 us, 20 us walked by
+// one thread a value.
+constexpr int kChainWaves = 16;
+__global__ __launch_bounds__(64 * kChainWaves) void scan_chain_kernel(Args A, int64_t blocks) {
+  constexpr int U = 8;
+  __shared__ float decays[kChainWaves][64], values[kChainWaves][64];
+  const int64_t size = static_cast<int64_t>(A.D) * A.dk, wide = (size + 63) / 64;
+  const bool back = blockIdx.x >= blocks;
+  const int64_t block = blockIdx.x - (back ? blocks : 0);
+  const int64_t chain = block / wide, at = chain * A.S;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t e = min((block - chain * wide) * 64 + lane, size - 1);  // (the last one again)
   const int head = static_cast<int>(e / (A.dk * A.dv));
   const int ch = head * A.dv + static_cast<int>(e % A.dv);
   const float a2 = A.a[e] * kLog2e;
-  const int64_t at = static_cast<int64_t>(blockIdx.x / blocks) * A.S;
-  float* h = A.h + at * size + e;
+  float* h = (back ? A.g : A.h) + at * size + e;
   const float* sum = A.sum + at * A.D + ch;
-  const int* cut = A.cut + at;
-  float state = 0.f;
-  constexpr int U = 8;
-  for (int k = 0; k < A.S; k += U) {
-    float v[U], q[U];
+  const int* cut = (back ? A.cutr : A.cut) + at;
+  // segment of the i-th place in the order of the chain; the last place's own
+  // state is not asked for (and the forward's not there)
+  const int last = A.S - 1;
+  auto place = [&](int i) { return back ? last - i : i; };
+  const int share = (A.S + kChainWaves - 1) / kChainWaves;
+  const int lo = min(wave * share, A.S), hi = min(lo + share, A.S);
+  float v[U], p[U];
+  auto load = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = min(k + u, A.S - 2);  // (the last segment's is not there)
-      v[u] = h[j * size];
-      q[u] = sum[static_cast<int64_t>(j) * A.D];
+      const int k = place(min(i0 + u, max(last - 1, 0)));
+      v[u] = h[k * size];
+      p[u] = cut[k] ? 0.f : decay(sum[static_cast<int64_t>(k) * A.D], a2);
     }
+  };
+  float all = 1.f, state = 0.f;
+  for (int i = lo; i < hi; i += U) {
+    load(i);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (k + u >= A.S) break;
-      h[(k + u) * size] = state;
-      if (k + u < A.S - 1) state = cut[k + u] ? v[u] : fmaf(decay(q[u], a2), state, v[u]);
+      if (i + u >= hi) break;
+      all *= p[u];
+      state = fmaf(p[u], state, v[u]);
+    }
+  }
+  decays[wave][lane] = all;
+  values[wave][lane] = state;
+  __syncthreads();
+  state = 0.f;
+  for (int w = 0; w < wave; ++w) state = fmaf(decays[w][lane], state, values[w][lane]);
+  for (int i = lo; i < hi; i += U) {
+    if (share > U) load(i);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u >= hi) break;
+      if ((block - chain * wide) * 64 + lane < size) h[place(i + u) * size] = state;
+      state = fmaf(p[u], state, v[u]);
     }
   }
 }
@@ -483,14 +505,14 @@ __global__ __launch_bounds__(256) void scan_chain_kernel(Args A) {
 // The walk of the outputs.  WS > 1: every U tokens the waves of a channel
 // block leave their sums over n in LDS and share the rows out.
 template <typename IO, int NS, int WS, bool PAD, bool GATE>
-__global__ __launch_bounds__(kThreads) void scan_out_kernel(Args A) {
+__global__ __launch_bounds__(64 * waves_of(WS)) void scan_out_kernel(Args A) {
   constexpr int U = 4;
   const Span s = span_of(A, blockIdx.x / A.ublocks);
   const Runs rs = runs_of(A, s);
-  const Lane<NS> l = lane_of<IO, NS, WS, PAD>(A);
+  const Lane<NS> l = lane_of<IO, NS, PAD>(A, WS);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t size = static_cast<int64_t>(A.D) * A.dk;
-  __shared__ float meet[WS > 1 ? kWaves : 1][WS > 1 ? U : 1][64];
+  __shared__ float meet[WS > 1 ? waves_of(WS) : 1][WS > 1 ? U : 1][64];
   for (int i = rs.cont ? 0 : 1; i <= rs.count; ++i) {
     const Run r = run_at(A, s, rs, i);
     float h[NS];
@@ -547,7 +569,7 @@ __global__ __launch_bounds__(kThreads) void scan_out_kernel(Args A) {
           for (int k = 1; k < WS; ++k) v += meet[wave - wave % WS + k][u][lane];
         }
         v = fmaf(l.d, xs[u], v);
-        if constexpr (GATE) v *= zs[u] * sigmoid(zs[u]);
+        if constexpr (GATE) v *= zs[u] * sigmoid<IO>(zs[u]);
         out.store(u, l.row, v);
       }
     }
@@ -575,11 +597,10 @@ __global__ __launch_bounds__(kThreads) void scan_out_kernel(Args A) {
 // As scan_local_kernel, over all runs: besides the segment's state its tiles'
 // states, and what its first run makes of the gradient behind it.
 template <typename IO, int NS, bool PAD, bool GATE>
-__global__ __launch_bounds__(kThreads) void scan_marks_kernel(Args A, int WS) {
+__global__ __launch_bounds__(512) void scan_marks_kernel(Args A, int WS) {
   const Span s = span_of(A, blockIdx.x / A.ublocks);
   const Runs rs = runs_of(A, s);
-  const Lane<NS> l = WS == 1 ? lane_of<IO, NS, 1, PAD>(A)
-                     : WS == 2 ? lane_of<IO, NS, 2, PAD>(A) : lane_of<IO, NS, 4, PAD>(A);
+  const Lane<NS> l = lane_of<IO, NS, PAD>(A, WS);
   const int64_t size = static_cast<int64_t>(A.D) * A.dk;
   float h[NS], g[NS], sum = 0.f, sumr = 0.f;
 #pragma unroll
@@ -627,7 +648,7 @@ __global__ __launch_bounds__(kThreads) void scan_marks_kernel(Args A, int WS) {
         const Row<IO, NS, PAD> c = next;
         next.load(row_of<IO>(A, l, A.c, t) + min(u + 1, left - 1) * step, l.left);
         const float dx = delta * x[u];
-        const float v = GATE ? dys[u] * zs[u] * sigmoid(zs[u]) : dys[u];
+        const float v = GATE ? dys[u] * zs[u] * sigmoid<IO>(zs[u]) : dys[u];
         sum += delta;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
@@ -669,39 +690,6 @@ __global__ __launch_bounds__(kThreads) void scan_marks_kernel(Args A, int WS) {
   }
 }
 
-// Chains the segments' gradients from the last back: every one is replaced by
-// the gradient of the state behind its segment.
-__global__ __launch_bounds__(256) void scan_chain_back_kernel(Args A) {
-  const int64_t size = static_cast<int64_t>(A.D) * A.dk;
-  const unsigned blocks = (size + 255) / 256;
-  const int64_t e = static_cast<int64_t>(blockIdx.x % blocks) * 256 + threadIdx.x;
-  if (e >= size) return;
-  const int head = static_cast<int>(e / (A.dk * A.dv));
-  const int ch = head * A.dv + static_cast<int>(e % A.dv);
-  const float a2 = A.a[e] * kLog2e;
-  const int64_t at = static_cast<int64_t>(blockIdx.x / blocks) * A.S;
-  float* g = A.g + at * size + e;
-  const float* sum = A.sum + at * A.D + ch;
-  const int* cut = A.cutr + at;
-  float grad = 0.f;
-  constexpr int U = 8;
-  for (int k = A.S - 1; k >= 0; k -= U) {
-    float v[U], q[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = max(k - u, 0);
-      v[u] = g[j * size];
-      q[u] = sum[static_cast<int64_t>(j) * A.D];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (k - u < 0) break;
-      g[(k - u) * size] = grad;
-      grad = cut[k - u] ? v[u] : fmaf(decay(q[u], a2), grad, v[u]);
-    }
-  }
-}
-
 template <int CTRL>
 __device__ inline float lane_of_other(float x) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
@@ -710,7 +698,9 @@ __device__ inline float lane_of_other(float x) {
 // Sums over lanes of two values at once: each half of the lanes goes on with
 // one of them.  Lanes 32 apart, 16 apart, then within a row of 16 by the lane
 // bit BIT (the partner differs in that bit, and in lower ones, which later
-// steps add up).
+// steps add up).  (The matrix cores can add lanes up too, as products with unit
+// vectors; their fp32 products take the vector unit's time: the gradient walk
+// of 16384 tokens of 4096 channels went from 1000 to 1390 us.)
 __device__ inline float fold32(float a, float b) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false,
                                                   false);
@@ -731,15 +721,15 @@ __device__ inline float fold(float a, float b) {
 
 // The gradient walk.
 template <typename IO, int NS, int WS, bool PAD, bool GATE>
-__global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(Args A) {
-  constexpr int U = 4, Q = kScanTile / U, N = NS < 8 ? NS : 8;
-  __shared__ floatx4 marks[kWaves][Q][NS / 4][64];
-  __shared__ float meet[WS > 1 ? kWaves : 1][WS > 1 ? U : 1][3][64];
+__global__ __launch_bounds__(64 * waves_of(WS), 2) void scan_grad_kernel(Args A) {
+  constexpr int U = 4, Q = kScanTile / U, N = PAD || NS < 8 ? 4 : 8;
+  __shared__ floatx4 marks[waves_of(WS)][Q][NS / 4][64];
+  __shared__ float meet[WS > 1 ? waves_of(WS) : 1][WS > 1 ? U : 1][3][64];
   const Span s = span_of(A, blockIdx.x / A.ublocks);
   const Runs rs = runs_of(A, s);
-  const Lane<NS> l = lane_of<IO, NS, WS, PAD>(A);
+  const Lane<NS> l = lane_of<IO, NS, PAD>(A, WS);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool real = blockIdx.x % A.ublocks * (kWaves / WS) + wave / WS < A.units;
+  const bool real = blockIdx.x % A.ublocks * (waves_of(WS) / WS) + wave / WS < A.units;
   const int64_t size = static_cast<int64_t>(A.D) * A.dk;
   const int step = row_step<IO>(A);
   float da[NS], dd = 0.f, dbias = 0.f;
@@ -755,6 +745,17 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(Args A) {
     else if (A.ds != nullptr) load_state<NS, PAD>(A, l, A.ds + r.seq * size, g);
 
     const int tiles = static_cast<int>((r.hi - r.lo + kScanTile - 1) / kScanTile);
+    Rows<IO, U> next[4];  // the rows of the next block: x, dt, dy, z
+    auto rows = [&](int64_t t, int left) {
+      next[0].load(A, A.x, t, left, l.row);
+      next[1].load(A, A.dt, t, left, l.row);
+      next[2].load(A, A.dy, t, left, l.row);
+      if constexpr (GATE) next[3].load(A, A.z, t, left, l.row);
+    };
+    if (tiles > 0) {
+      const int64_t t = r.lo + (r.hi - r.lo - 1) / U * U;
+      rows(t, static_cast<int>(r.hi - t));
+    }
     for (int k = tiles - 1; k >= 0; --k) {
       const int64_t t0 = r.lo + k * kScanTile;
       const int count = static_cast<int>(r.hi - t0 < kScanTile ? r.hi - t0 : kScanTile);
@@ -775,15 +776,20 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(Args A) {
             for (int n = 0; n < NS; ++n) h[n] = fmaf(decay(sum, l.a2[n]), f[n], h[n]);
           }
         }
-        for (int q = 0;; ++q) {
+        Rows<IO, U> wx[Q - 1], wdt[Q - 1];
+#pragma unroll
+        for (int q = 0; q < Q - 1; ++q) {
+          wx[q].load(A, A.x, t0 + q * U, count - (q + 1) * U > 0 ? U : 0, l.row);
+          wdt[q].load(A, A.dt, t0 + q * U, count - (q + 1) * U > 0 ? U : 0, l.row);
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
 #pragma unroll
           for (int n = 0; n < NS; n += 4)
             marks[wave][q][n / 4][lane] = floatx4{h[n], h[n + 1], h[n + 2], h[n + 3]};
           if (q + 1 >= blocks) break;
           const int64_t t = t0 + q * U;
-          Rows<IO, U> x, dt;
-          x.load(A, A.x, t, U, l.row);
-          dt.load(A, A.dt, t, U, l.row);
+          const Rows<IO, U>&x = wx[q < Q - 1 ? q : 0], &dt = wdt[q < Q - 1 ? q : 0];
           Row<IO, NS, PAD> next;
           const uintptr_t from = row_of<IO>(A, l, A.b, t);
           next.load(from, l.left);
@@ -804,18 +810,20 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(Args A) {
         // state and its gradient pass through them unchanged
         const int64_t t = t0 + q * U;
         const int left = static_cast<int>(r.hi - t < U ? r.hi - t : U);
-        Rows<IO, U> x, pre, dout, z{};
-        x.load(A, A.x, t, left, l.row);
-        pre.load(A, A.dt, t, left, l.row);
-        dout.load(A, A.dy, t, left, l.row);
-        if constexpr (GATE) z.load(A, A.z, t, left, l.row);
+        const Rows<IO, U> x = next[0], pre = next[1], dout = next[2], z = next[GATE ? 3 : 0];
+        rows(t - U, t > r.lo ? U : 0);  // (the block in front is a whole one)
         const uintptr_t fromb = row_of<IO>(A, l, A.b, t), fromc = row_of<IO>(A, l, A.c, t);
-        float delta[U], dx[U], dy[U], gb[U], ga[U], ys[U];
+        float delta[U], dx[U], dy[U], slope[U], gb[U], ga[U], ys[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           delta[u] = u < left ? step_of(A, pre[u], l.bias) : 0.f;
           dx[u] = delta[u] * x[u];
-          dy[u] = GATE ? dout[u] * z[u] * sigmoid(z[u]) : dout[u];
+          dy[u] = dout[u];
+          if constexpr (GATE) {
+            const float sg = sigmoid<IO>(z[u]);
+            dy[u] *= z[u] * sg;
+            slope[u] = dout[u] * (sg * (1.f + z[u] * (1.f - sg)));
+          }
           gb[u] = ga[u] = ys[u] = 0.f;
         }
 #pragma unroll
@@ -924,17 +932,13 @@ __global__ __launch_bounds__(kThreads, 2) void scan_grad_kernel(Args A) {
             }
           }
           float v = fmaf(x[u], vb, kLn2 * va);
-          if (A.softplus) v *= sigmoid(pre[u] + l.bias);
+          if (A.softplus) v *= sigmoid<IO>(pre[u] + l.bias);
           dd = fmaf(dy[u], x[u], dd);
           dbias += u < left ? v : 0.f;
           outx.store(u, l.row, fmaf(l.d, dy[u], delta[u] * vb));
           outt.store(u, l.row, v);
-          if constexpr (GATE) {
-            const float sg = sigmoid(z[u]);
-            RowsOut<IO, U>(A, A.dz, t, left)
-                .store(u, l.row,
-                       dout[u] * fmaf(l.d, x[u], vy) * (sg * (1.f + z[u] * (1.f - sg))));
-          }
+          if constexpr (GATE)
+            RowsOut<IO, U>(A, A.dz, t, left).store(u, l.row, slope[u] * fmaf(l.d, x[u], vy));
         }
       }
     }
@@ -989,51 +993,81 @@ __global__ __launch_bounds__(256) void scan_sum_kernel(const float* part, int64_
 // ------------------------------------------------------------------- step ---
 
 // One token of every sequence: a thread owns V adjacent channels of one head
-// and reads and writes each of their states once; memory bounds it.
+// and reads and writes each of their states once, sixteen of them (and their
+// rates) in flight at a time; memory bounds it.
 template <typename IO, int V>
-__global__ __launch_bounds__(256) void scan_step_kernel(Args A, int per) {
+__device__ inline void load_row(const void* p, int64_t at, float* x) {
+  if constexpr (V == 1) {
+    x[0] = io<IO>::load(p, at);
+  } else if constexpr (io<IO>::bytes == 2) {
+    typedef __bf16 vec __attribute__((ext_vector_type(V)));
+    const vec v = *reinterpret_cast<const vec*>(static_cast<const __bf16*>(p) + at);
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = static_cast<float>(v[e]);
+  } else {
+    typedef float vec __attribute__((ext_vector_type(V)));
+    const vec v = *reinterpret_cast<const vec*>(static_cast<const float*>(p) + at);
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = v[e];
+  }
+}
+
+template <typename IO, int V>
+__global__ __launch_bounds__(256) void scan_step_kernel(Args A, int64_t threads) {
   typedef float vec __attribute__((ext_vector_type(V)));
-  const int ch = (blockIdx.x * 256 + threadIdx.x) * V;
-  if (ch >= A.D) return;
+  constexpr int N = 16;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (id >= threads) return;
+  const int row = A.D / V;  // threads of a sequence
+  const int64_t q = id / row;
+  const int ch = static_cast<int>(id - q * row) * V;
   const int head = ch / A.dv, grp = ch / A.Dg;
   const int state = head * A.dk * A.dv + ch - head * A.dv;
-  const int64_t size = static_cast<int64_t>(A.D) * A.dk;
-  const int end = min((static_cast<int>(blockIdx.y) + 1) * per, A.nseq);
-  for (int q = blockIdx.y * per; q < end; ++q) {
-    float* p = A.sf + q * size + state;
-    float delta[V], dx[V], x[V], y[V];
+  float* p = A.sf + q * A.D * A.dk + state;
+  const float* rate = A.a + state;
+  const int64_t bc = (q * A.hb + grp) * A.dk;
+  float x[V], z[V], delta[V], dx[V], y[V];
+  load_row<IO, V>(A.x, q * A.D + ch, x);
+  load_row<IO, V>(A.dt, q * A.D + ch, delta);
+  if (A.z != nullptr) load_row<IO, V>(A.z, q * A.D + ch, z);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      x[v] = load_x<IO>(A.x, A, q, ch + v);
-      delta[v] = step_of(A, load_x<IO>(A.dt, A, q, ch + v), A.bias ? A.bias[ch + v] : 0.f);
-      dx[v] = delta[v] * x[v];
-      y[v] = 0.f;
+  for (int v = 0; v < V; ++v) y[v] = A.d ? A.d[ch + v] * x[v] : 0.f;
+  for (int n0 = 0; n0 < A.dk; n0 += N) {
+    vec h[N], a[N];
+    float b[N], c[N];
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const int n = min(n0 + i, A.dk - 4);  // (the last ones again, not used)
+      load_row<IO, 4>(A.b, bc + n, b + i);
+      load_row<IO, 4>(A.c, bc + n, c + i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        h[i + k] = *reinterpret_cast<const vec*>(p + (n + k) * A.dv);
+        a[i + k] = *reinterpret_cast<const vec*>(rate + (n + k) * A.dv);
+      }
     }
-    const int64_t row = (static_cast<int64_t>(q) * A.hb + grp) * A.dk;
-    for (int n = 0; n < A.dk; n += 4) {
+    if (n0 == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float b = io<IO>::load(A.b, row + n + i), c = io<IO>::load(A.c, row + n + i);
-        vec h = *reinterpret_cast<const vec*>(p + (n + i) * A.dv);
-        const vec a = *reinterpret_cast<const vec*>(A.a + state + (n + i) * A.dv);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float w = fmaf(decay(delta[v], a[v] * kLog2e), h[v], dx[v] * b);
-          h[v] = w;
-          y[v] = fmaf(c, w, y[v]);
-        }
-        *reinterpret_cast<vec*>(p + (n + i) * A.dv) = h;
+      for (int v = 0; v < V; ++v) {
+        delta[v] = step_of(A, delta[v], A.bias ? A.bias[ch + v] : 0.f);
+        dx[v] = delta[v] * x[v];
       }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float o = y[v] + (A.d ? A.d[ch + v] * x[v] : 0.f);
-      if (A.z != nullptr) {
-        const float z = load_x<IO>(A.z, A, q, ch + v);
-        o *= z * sigmoid(z);
+    for (int i = 0; i < N; ++i) {
+      if (n0 + i >= A.dk) break;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        h[i][v] = fmaf(decay(delta[v], a[i][v] * kLog2e), h[i][v], dx[v] * b[i]);
+        y[v] = fmaf(c[i], h[i][v], y[v]);
       }
-      store_x<IO>(A.y, A, q, ch + v, o);
+      *reinterpret_cast<vec*>(p + (n0 + i) * A.dv) = h[i];
     }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (A.z != nullptr) y[v] *= z[v] * sigmoid<IO>(z[v]);
+    store_x<IO>(A.y, A, q, ch + v, y[v]);
   }
 }
 
@@ -1053,13 +1087,20 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 Plan plan_scan(const Scan& p) {
   Plan q;
-  q.ns = p.dk <= 4 ? 4 : p.dk <= 8 ? 8 : 16;
-  q.ws = p.dk <= 16 ? 1 : p.dk <= 32 ? 2 : 4;
-  q.pad = p.dk != q.ns * q.ws;
   q.chains = p.varlen ? 1 : p.B;
   q.len = p.T;
   const int64_t D = static_cast<int64_t>(p.H) * p.dv, Dg = D / p.hb;
   q.units = static_cast<int>(p.hb * ceil_div(Dg, 64));
+  q.ns = p.dk <= 4 ? 4 : p.dk <= 8 ? 8 : 16;
+  auto split = [&] {
+    q.ws = 1;
+    while (q.ws * q.ns < p.dk) q.ws *= 2;
+  };
+  split();
+  // Segments: eight waves a SIMD to choose from hide the loads (16384 tokens
+  // of 4096 channels: 574 us with two, 490 with four, 456), but not below
+  // half the square root of the tokens, where the chaining takes over; no cut
+  // where one walk takes less than three launches.
   int64_t L;
   if (p.seg_req < 0) {
     L = q.len;
@@ -1067,15 +1108,23 @@ Plan plan_scan(const Scan& p) {
     L = static_cast<int64_t>(std::min(p.seg_req, 1 << 20)) * kScanTile;
   } else {
     const int64_t waves = static_cast<int64_t>(q.chains) * q.units * q.ws;
-    const int64_t want = std::max<int64_t>(1, ceil_div(2048, waves));  // segments of a chain
+    const int64_t want = std::max<int64_t>(1, ceil_div(8192, waves));  // segments of a chain
     L = std::max<int64_t>(ceil_div(q.len, want),
-                          static_cast<int64_t>(std::sqrt(static_cast<double>(q.len))));
+                          static_cast<int64_t>(0.5 * std::sqrt(static_cast<double>(q.len))));
     L = std::max<int64_t>(ceil_div(L, kScanTile) * kScanTile, kScanTile);
+    if (q.len <= 96) L = q.len;
   }
   if (L >= q.len) L = std::max<int64_t>(q.len, 1);
   q.L = static_cast<int>(L);
   q.S = static_cast<int>(std::max<int64_t>(1, ceil_div(q.len, L)));
   q.segs = static_cast<int64_t>(q.chains) * q.S;
+  // Few waves: a channel's states are shared out over more of them, so that
+  // a token takes less time.
+  while (q.ns > 4 && q.ws < 8 && q.segs * q.units * q.ws < 512) {
+    q.ns /= 2;
+    split();
+  }
+  q.pad = q.ns < 16 || p.dk != q.ns * q.ws;
   return q;
 }
 
@@ -1139,7 +1188,7 @@ Args make_args(const Scan& p, const Plan& q, const ScanIn& in) {
   A.Dg = A.D / p.hb;
   A.nb = (A.Dg + 63) / 64;
   A.units = q.units;
-  A.ublocks = static_cast<int>(ceil_div(q.units, kWaves / q.ws));
+  A.ublocks = static_cast<int>(ceil_div(q.units, waves_of(q.ws) / q.ws));
   A.dk = p.dk;
   A.dv = p.dv;
   A.hb = p.hb;
@@ -1154,13 +1203,21 @@ Args make_args(const Scan& p, const Plan& q, const ScanIn& in) {
 template <typename IO, int NS, bool PAD>
 void launch_local(const Args& A, const Plan& q, int64_t segs, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(A.ublocks * segs));
-  hipLaunchKernelGGL((scan_local_kernel<IO, NS, PAD>), grid, dim3(kThreads), 0, s, A, q.ws);
+  hipLaunchKernelGGL((scan_local_kernel<IO, NS, PAD>), grid, dim3(64 * waves_of(q.ws)), 0, s, A,
+                     q.ws);
 }
 
 template <typename IO, int NS, int WS, bool PAD, bool GATE>
 void launch_out(const Args& A, const Plan& q, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(A.ublocks * q.segs));
-  hipLaunchKernelGGL((scan_out_kernel<IO, NS, WS, PAD, GATE>), grid, dim3(kThreads), 0, s, A);
+  hipLaunchKernelGGL((scan_out_kernel<IO, NS, WS, PAD, GATE>), grid, dim3(64 * waves_of(WS)), 0,
+                     s, A);
+}
+
+void launch_chain(const Args& A, const Plan& q, int ways, hipStream_t s) {
+  const int64_t blocks = ceil_div(static_cast<int64_t>(A.D) * A.dk, 64) * q.chains;
+  hipLaunchKernelGGL(scan_chain_kernel, dim3(static_cast<unsigned>(ways * blocks)),
+                     dim3(64 * kChainWaves), 0, s, A, blocks);
 }
 
 void launch_sum(const float* part, int64_t rows, int64_t cols, float* out, hipStream_t s) {
@@ -1169,24 +1226,32 @@ void launch_sum(const float* part, int64_t rows, int64_t cols, float* out, hipSt
                      0, s, part, rows, cols, out);
 }
 
-// Calls f<NS, WS, PAD, GATE> of a plan.
+// Calls f<NS, WS, PAD, GATE> of a plan (fewer than 16 states a lane are always
+// taken for padded: their scalars are not what bounds them).
 template <typename F>
 void with_plan(const Plan& q, bool gate, F f) {
   using std::integral_constant;
-  const integral_constant<int, 1> one;
   auto all = [&](auto ns, auto ws, auto pad) {
     if (gate) f(ns, ws, pad, std::true_type{});
     else f(ns, ws, pad, std::false_type{});
   };
-  auto pad = [&](auto ns, auto ws) {
-    if (q.pad) all(ns, ws, std::true_type{});
-    else all(ns, ws, std::false_type{});
+  auto pads = [&](auto ns, auto ws) {
+    if constexpr (ns == 16) {
+      if (!q.pad) return all(ns, ws, std::false_type{});
+    }
+    all(ns, ws, std::true_type{});
   };
-  if (q.ns == 4) return all(integral_constant<int, 4>{}, one, std::false_type{});
-  if (q.ns == 8) return all(integral_constant<int, 8>{}, one, std::false_type{});
-  if (q.ws == 1) return pad(integral_constant<int, 16>{}, one);
-  if (q.ws == 2) return pad(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  return pad(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  auto waves = [&](auto ns) {
+    if (q.ws == 1) return pads(ns, integral_constant<int, 1>{});
+    if (q.ws == 2) return pads(ns, integral_constant<int, 2>{});
+    if constexpr (ns < 16) {
+      if (q.ws == 8) return pads(ns, integral_constant<int, 8>{});
+    }
+    pads(ns, integral_constant<int, 4>{});
+  };
+  if (q.ns == 4) return waves(integral_constant<int, 4>{});
+  if (q.ns == 8) return waves(integral_constant<int, 8>{});
+  waves(integral_constant<int, 16>{});
 }
 
 template <typename IO>
@@ -1203,9 +1268,7 @@ hipError_t scan_fwd(const Plan& q, const Args& A, hipStream_t s) {
     if (e != hipSuccess) return e;
     {
       StageScope scope(GDN_STAGE_FWD_COMBINE, s);
-      const int64_t blocks = ceil_div(static_cast<int64_t>(A.D) * A.dk, 256);
-      const dim3 grid(static_cast<unsigned>(blocks * q.chains));
-      hipLaunchKernelGGL(scan_chain_kernel, grid, dim3(256), 0, s, A);
+      launch_chain(A, q, 1, s);
       e = hipGetLastError();
     }
     if (e != hipSuccess) return e;
@@ -1226,24 +1289,23 @@ hipError_t scan_bwd(const Plan& q, const Args& A, int64_t tokens, const ScanGrad
     StageScope scope(GDN_STAGE_BWD_STATES, s);
     with_plan(q, A.z != nullptr, [&](auto ns, auto, auto pad, auto gate) {
       hipLaunchKernelGGL((scan_marks_kernel<IO, ns, pad, gate>),
-                         dim3(static_cast<unsigned>(A.ublocks * q.segs)), dim3(kThreads), 0, s, A,
-                         q.ws);
+                         dim3(static_cast<unsigned>(A.ublocks * q.segs)),
+                         dim3(64 * waves_of(q.ws)), 0, s, A, q.ws);
     });
     e = hipGetLastError();
   }
   if (e != hipSuccess) return e;
   if (q.S > 1) {
     StageScope scope(GDN_STAGE_BWD_SCAN, s);
-    const dim3 grid(static_cast<unsigned>(ceil_div(size, 256) * q.chains));
-    hipLaunchKernelGGL(scan_chain_kernel, grid, dim3(256), 0, s, A);
-    hipLaunchKernelGGL(scan_chain_back_kernel, grid, dim3(256), 0, s, A);
+    launch_chain(A, q, 2, s);
     e = hipGetLastError();
   }
   if (e != hipSuccess) return e;
   StageScope scope(GDN_STAGE_BWD_GRAD, s);
   with_plan(q, A.z != nullptr, [&](auto ns, auto ws, auto pad, auto gate) {
     hipLaunchKernelGGL((scan_grad_kernel<IO, ns, ws, pad, gate>),
-                       dim3(static_cast<unsigned>(A.ublocks * q.segs)), dim3(kThreads), 0, s, A);
+                       dim3(static_cast<unsigned>(A.ublocks * q.segs)), dim3(64 * waves_of(ws)), 0,
+                       s, A);
   });
   e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -1262,11 +1324,12 @@ hipError_t scan_bwd(const Plan& q, const Args& A, int64_t tokens, const ScanGrad
 bool scan_fits(const Scan& p) {
   // every launch below 2^32 threads
   const Plan q = plan_scan(p);
-  const int64_t most = (int64_t(1) << 32) / kThreads - 1;
-  const int64_t state = ceil_div(static_cast<int64_t>(p.H) * p.dv * p.dk, 256);
+  const int64_t most = (int64_t(1) << 32) - 1;
+  const int64_t state = ceil_div(static_cast<int64_t>(p.H) * p.dv * p.dk, 64);
   const int64_t rows = static_cast<int64_t>(p.B) * p.T;
-  return q.segs <= most / std::max<int64_t>(ceil_div(q.units, kWaves / q.ws), state) &&
-         rows <= most * 256 / (2 * p.dk) / p.hb;
+  const int64_t unit = ceil_div(q.units, waves_of(q.ws) / q.ws) * 64 * waves_of(q.ws);
+  return q.segs <= most / unit && q.chains <= most / (2 * 64 * kChainWaves) / state &&
+         rows <= most / (2 * p.dk) / p.hb - 256;
 }
 
 size_t scan_fwd_workspace_bytes(const Scan& p) {
@@ -1310,15 +1373,16 @@ hipError_t launch_scan_step(const Scan& p, const ScanIn& in, float* state, void*
   Args A = make_args(p, plan_scan(p), in);
   A.y = y;
   A.sf = state;
-  const int V = p.dv % 4 == 0 ? 4 : 1;
-  const int64_t blocks = ceil_div(A.D / V, 256);
-  const int per = static_cast<int>(std::max<int64_t>(1, blocks * p.nseq / 2048));
-  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(ceil_div(p.nseq, per)));
+  // four channels a thread where that leaves threads enough to keep the memory
+  // busy, else one
+  const int V = p.dv % 4 == 0 && static_cast<int64_t>(A.D) * p.nseq >= (1 << 17) ? 4 : 1;
+  const int64_t threads = static_cast<int64_t>(A.D / V) * p.nseq;
+  const dim3 grid(static_cast<unsigned>(ceil_div(threads, 256)));
   StageScope scope(GDN_STAGE_DECODE, s);
   auto go = [&](auto io_tag) {
     using IO = decltype(io_tag);
-    if (V == 4) hipLaunchKernelGGL((scan_step_kernel<IO, 4>), grid, dim3(256), 0, s, A, per);
-    else hipLaunchKernelGGL((scan_step_kernel<IO, 1>), grid, dim3(256), 0, s, A, per);
+    if (V == 4) hipLaunchKernelGGL((scan_step_kernel<IO, 4>), grid, dim3(256), 0, s, A, threads);
+    else hipLaunchKernelGGL((scan_step_kernel<IO, 1>), grid, dim3(256), 0, s, A, threads);
   };
   if (p.io == GDN_BF16) go(bf16_t{});
   else go(f32_t{});
