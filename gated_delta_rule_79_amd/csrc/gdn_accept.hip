@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kMaxNodes = 64;
 constexpr int kWalkThreads = 1024;
+constexpr int kHeldPer = 32;  // values a thread holds: rows up to 32768 stay in the CU
 constexpr int kSlabThreads = 256;
 constexpr int kLastPer = 4;  // values a thread takes where a token is looked for
 
@@ -43,6 +44,7 @@ struct Args {
   int32_t *accepted, *length, *next;
   int slabs, slab;    // of a chain's row
   double* part;       // [trees][slabs] sums
+  int2* head;         // [trees] a chain's accepted nodes, the token that failed
 };
 
 // Where a sequence's nodes and rows lie.
@@ -75,14 +77,12 @@ struct Row {
   const int* tried;       // their tokens (certain drafts)
 
   __device__ inline double less(float pv, float qv, int x) const {
-    double w = static_cast<double>(pv);
+    double w = pv > 0.f ? pv : 0.f;  // (a NaN counts nothing)
     for (int j = 0; j < m; ++j) {
-      const double d = w * scale[j] - (q != nullptr ? static_cast<double>(qv)
-                                                    : x == tried[j] ? 1.0 : 0.0);
-      w = d;
-      if (!(w > 0.0)) w = 0.0;
+      const double by = q != nullptr ? static_cast<double>(qv) : x == tried[j] ? 1.0 : 0.0;
+      w = fmax(fma(w, scale[j], -by), 0.0);
     }
-    return w > 0.0 ? w : 0.0;  // (a NaN counts nothing)
+    return w;
   }
   __device__ inline double at(int x) const {
     return less(io<IO>::load(p, x), q != nullptr ? io<IO>::load(q, x) : 0.f, x);
@@ -138,7 +138,7 @@ __device__ inline double wave_sum(const Row<IO>& r, int lo, int hi) {
 // Scratch of a workgroup of up to 16 waves.
 struct Meet {
   double part[16];
-  int lo, hi, first, last;
+  int first, last, token;
   double before;
 };
 
@@ -157,69 +157,79 @@ __device__ inline double block_sums(const Row<IO>& r, int lo, int hi, Meet* meet
   return s;
 }
 
-// The share of `count` sums whose running sum first exceeds what is left of
-// `target`, or the last that is not empty; takes the sums in front off it.
-__device__ inline int pick(const double* part, int count, double* target) {
-  double before = 0.0, at = 0.0;
-  int last = 0;
-  for (int k = 0; k < count; ++k) {
-    if (part[k] > 0.0) last = k, at = before;
-    if (before + part[k] > *target && part[k] > 0.0) break;
-    before += part[k];
-  }
-  *target -= at;
-  return last;
-}
-
-// The token of [lo, hi) (few enough for the workgroup) at which the running
-// sum exceeds target; the last one with a part of the row if none does.
-template <typename IO>
-__device__ inline int find(const Row<IO>& r, int lo, int hi, double target, int none, Meet* meet) {
+// Of the workgroup's values v >= 0 (one a thread, in order): the first thread
+// at which the running sum exceeds *target, or the last with a value if none
+// does (0 if none has one).  Takes the sum in front of it off *target.
+__device__ inline int pick(double v, double* target, Meet* meet) {
   const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  double w[kLastPer], sum = 0.0;
-  const int at = lo + threadIdx.x * kLastPer;
-#pragma unroll
-  for (int e = 0; e < kLastPer; ++e) {
-    w[e] = at + e < hi ? r.at(at + e) : 0.0;
-    sum += w[e];
-  }
-  double run = sum;  // of the wave's lanes up to this one
+  double run = v;  // of the wave's lanes up to this one
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
-    const double v = __shfl_up(run, m, 64);
-    if (lane >= m) run += v;
+    const double o = __shfl_up(run, m, 64);
+    if (lane >= m) run += o;
   }
   __syncthreads();
   if (lane == 63) meet->part[wave] = run;
-  if (threadIdx.x == 0) meet->first = 0x7fffffff, meet->last = -1;
+  if (threadIdx.x == 0) meet->first = 0x7fffffff, meet->last = 0;
   __syncthreads();
-  double before = run - sum;
-  for (int k = 0; k < wave && k < waves; ++k) before += meet->part[k];
-#pragma unroll
-  for (int e = 0; e < kLastPer; ++e) {
-    before += w[e];
-    if (w[e] > 0.0) {
-      if (before > target) atomicMin(&meet->first, at + e);
-      atomicMax(&meet->last, at + e);
-    }
+  double front = run - v;
+  for (int k = 0; k < wave && k < waves; ++k) front += meet->part[k];
+  const int id = threadIdx.x;
+  if (v > 0.0) {
+    if (front + v > *target) atomicMin(&meet->first, id);
+    atomicMax(&meet->last, id);
   }
   __syncthreads();
-  return meet->first != 0x7fffffff ? meet->first : meet->last >= 0 ? meet->last : none;
+  const int at = meet->first != 0x7fffffff ? meet->first : meet->last;
+  if (id == at) meet->before = front;
+  __syncthreads();
+  *target -= meet->before;
+  return at;
 }
 
-// Narrows [lo, hi) to what find() takes, then finds the token.
+// The token among a thread's values w (kLastPer of them from `at` on, the
+// threads' in order) at which the running sum exceeds target; the last one with
+// a part of the row if none does.
+template <int PER>
+__device__ inline int find(const double (&w)[PER], int at, double target, int none, Meet* meet) {
+  double sum = 0.0;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) sum += w[e];
+  const int owner = pick(sum, &target, meet);
+  if (static_cast<int>(threadIdx.x) == owner) {
+    int token = none;
+    double run = 0.0;
+    for (int e = PER - 1; e >= 0; --e)
+      if (w[e] > 0.0 && token == none) token = at + e;  // the last
+    bool found = false;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      run += w[e];
+      if (!found && w[e] > 0.0 && run > target) token = at + e, found = true;
+    }
+    meet->token = token;
+  }
+  __syncthreads();
+  return meet->token;
+}
+
+// The token of [lo, hi), narrowed to what the threads hold at once.
 template <typename IO, int W>
 __device__ inline int draw(const Row<IO>& r, int lo, int hi, double target, int none, Meet* meet) {
   const int waves = blockDim.x >> 6;
   while (hi - lo > static_cast<int>(blockDim.x) * kLastPer) {
     block_sums<IO, W>(r, lo, hi, meet);
     const int each = ((hi - lo + waves - 1) / waves + W - 1) / W * W;
-    const int k = pick(meet->part, waves, &target);
-    __syncthreads();
+    const double v = static_cast<int>(threadIdx.x) < waves ? meet->part[threadIdx.x] : 0.0;
+    const int k = pick(v, &target, meet);
     lo = min(lo + k * each, hi);
     hi = min(lo + each, hi);
   }
-  return find(r, lo, hi, target, none, meet);
+  double w[kLastPer];
+  const int at = lo + threadIdx.x * kLastPer;
+#pragma unroll
+  for (int e = 0; e < kLastPer; ++e) w[e] = at + e < hi ? r.at(at + e) : 0.0;
+  return find(w, at, target, none, meet);
 }
 
 template <typename IO>
@@ -233,55 +243,238 @@ __device__ inline bool take(float u, float q, double Z, double r) {
 
 // ------------------------------------------------------------------- trees ---
 
+// A tree's nodes in LDS: every node with the target's and the draft's value of
+// its token in its parent's row, gathered at once.
+struct Nodes {
+  int parent[kMaxNodes], token[kMaxNodes], tried[kMaxNodes];
+  float p[kMaxNodes], q[kMaxNodes], u[kMaxNodes + 1];
+  double scale[kMaxNodes];
+
+  template <typename IO>
+  __device__ inline void load(const Args& A, const Tree& t) {
+    const int i = threadIdx.x;
+    if (i <= t.size) u[i] = A.u[t.row + i];
+    if (i < t.size) {
+      const int x = A.tokens[t.node + i], up = A.parent[t.node + i];
+      const int from = up >= 0 && up < i ? up : -1;
+      const bool ok = x >= 0 && x < A.V;
+      const int64_t row = t.row + from + 1;
+      parent[i] = ok ? from : -2;  // (a token that is none is no one's child)
+      token[i] = x;
+      p[i] = ok ? io<IO>::load(row_at<IO>(A.p, row, A.V), x) : 0.f;
+      q[i] = ok && A.q != nullptr ? io<IO>::load(row_at<IO>(A.q, row, A.V), x) : 1.f;
+    }
+  }
+};
+
+// Where the walk stands.
+struct Place {
+  int node, length;   // last accepted node, accepted nodes
+  int i;              // node that is tried next
+  int m;              // rejections here
+  double Z;
+  __device__ inline void move() {
+    node = i++;
+    ++length;
+    m = 0;
+    Z = 1.0;
+  }
+  // the next child from i on; false: there is none
+  __device__ inline bool child(const Nodes& nodes, const Tree& t) {
+    while (i < t.size && nodes.parent[i] != node) ++i;
+    return i < t.size;
+  }
+  __device__ inline bool accepts(const Nodes& nodes, bool drawn) const {
+    double r = nodes.p[i];
+    for (int j = 0; j < m; ++j) {
+      const double by = drawn ? static_cast<double>(nodes.q[i])
+                              : nodes.token[i] == nodes.tried[j] ? 1.0 : 0.0;
+      r = fmax(fma(r, nodes.scale[j], -by), 0.0);
+    }
+    return take(nodes.u[i], nodes.q[i], Z, r);
+  }
+  // child i is rejected; sum(k): of what k rejections leave
+  template <typename F>
+  __device__ inline void reject(Nodes& nodes, F sum) {
+    __syncthreads();  // (all have read what is written now)
+    if (threadIdx.x == 0) nodes.scale[m] = 1.0 / Z, nodes.tried[m] = nodes.token[i];
+    __syncthreads();
+    const double left = sum(m + 1);
+    if (left > 0.0) Z = left, ++m;  // else nothing would be left: the row stays
+    ++i;
+  }
+};
+
+// Rows of any length, read anew for every sum.
 template <typename IO, int W>
 __global__ __launch_bounds__(kWalkThreads) void accept_walk_kernel(Args A) {
   __shared__ Meet meet;
-  __shared__ double scale[kMaxNodes];
-  __shared__ int tried[kMaxNodes], parent[kMaxNodes], token[kMaxNodes];
-  __shared__ float u[kMaxNodes + 1];
+  __shared__ Nodes nodes;
   const Tree t = tree_at(A, blockIdx.x);
-  if (threadIdx.x < t.size) {
-    parent[threadIdx.x] = A.parent[t.node + threadIdx.x];
-    token[threadIdx.x] = A.tokens[t.node + threadIdx.x];
-  }
-  if (threadIdx.x <= t.size) u[threadIdx.x] = A.u[t.row + threadIdx.x];
+  nodes.load<IO>(A, t);
   __syncthreads();
-  int cur = -1, length = 0;
-  double Z = 1.0;
-  Row<IO> r{row_at<IO>(A.p, t.row, A.V), row_at<IO>(A.q, t.row, A.V), 0, scale, tried};
-  for (int i = 0; i < t.size; ++i) {
-    const int from = parent[i], x = token[i];
-    const bool here = (from >= 0 && from < i ? from : -1) == cur && x >= 0 && x < A.V;
-    if (!here) continue;  // (uniform)
-    const float q = r.q != nullptr ? io<IO>::load(r.q, x) : 1.f;
-    if (take(u[i], q, Z, r.at(x))) {
-      cur = i;
-      ++length;
-      Z = 1.0;
-      r.m = 0;
-      r.p = row_at<IO>(A.p, t.row + i + 1, A.V);
-      r.q = row_at<IO>(A.q, t.row + i + 1, A.V);
-      continue;
+  Place at{-1, 0, 0, 0, 1.0};
+  Row<IO> r{row_at<IO>(A.p, t.row, A.V), row_at<IO>(A.q, t.row, A.V), 0, nodes.scale, nodes.tried};
+  while (at.child(nodes, t)) {
+    if (at.accepts(nodes, A.q != nullptr)) {
+      at.move();
+      r.p = row_at<IO>(A.p, t.row + at.node + 1, A.V);
+      r.q = row_at<IO>(A.q, t.row + at.node + 1, A.V);
+    } else {
+      at.reject(nodes, [&](int k) {
+        r.m = k;
+        return block_sums<IO, W>(r, 0, A.V, &meet);
+      });
     }
-    __syncthreads();  // (all have read what is written now)
-    if (threadIdx.x == 0) scale[r.m] = 1.0 / Z, tried[r.m] = x;
-    __syncthreads();
-    ++r.m;
-    const double left = block_sums<IO, W>(r, 0, A.V, &meet);
-    if (left > 0.0) Z = left;
-    else --r.m;  // nothing would be left: the row stays
   }
-  // (the sum of a row that was rejected from is known, its shares are not kept)
-  const double sum = block_sums<IO, W>(r, 0, A.V, &meet);
-  double target = static_cast<double>(u[t.size]) * sum;
+  r.m = at.m;
+  double target = static_cast<double>(nodes.u[t.size]) * block_sums<IO, W>(r, 0, A.V, &meet);
   const int waves = kWalkThreads / 64, each = ((A.V + waves - 1) / waves + W - 1) / W * W;
-  const int k = pick(meet.part, waves, &target);
-  __syncthreads();
-  const int lo = min(k * each, A.V);
+  const double v = static_cast<int>(threadIdx.x) < waves ? meet.part[threadIdx.x] : 0.0;
+  const int lo = min(pick(v, &target, &meet) * each, A.V);
   const int next = draw<IO, W>(r, lo, min(lo + each, A.V), target, A.V - 1, &meet);
   if (threadIdx.x == 0) {
-    A.accepted[blockIdx.x] = cur;
-    A.length[blockIdx.x] = length;
+    A.accepted[blockIdx.x] = at.node;
+    A.length[blockIdx.x] = at.length;
+    A.next[blockIdx.x] = next;
+  }
+}
+
+// Rows that fit a CU, the target's in registers and the draft's in LDS: a row
+// is read once at most, and one whose first child is accepted not at all.
+template <typename IO, int W>
+__global__ __launch_bounds__(kWalkThreads) void accept_held_kernel(Args A) {
+  constexpr int C = kHeldPer / W, STEP = kWalkThreads * W, WAVES = kWalkThreads / 64;
+  typedef typename io<IO>::storage store;
+  struct Piece {  // W values as they are stored
+    uint32_t bits[W * sizeof(store) / 4];
+    __device__ inline float operator[](int e) const {
+      if constexpr (sizeof(store) == 4) return __uint_as_float(bits[e]);
+      else return __uint_as_float(e & 1 ? bits[e >> 1] & 0xffff0000u : bits[e >> 1] << 16);
+    }
+    // Taken for changed here: the 64-bit values of a whole row are else formed
+    // once for all sums and kept, more than there are registers.
+    __device__ inline void fresh() {
+      for (auto& b : bits) asm volatile("" : "+v"(b));
+    }
+  };
+  __shared__ Meet meet;
+  __shared__ Nodes nodes;
+  __shared__ double chunk[C][WAVES];
+  __shared__ Piece q[C][kWalkThreads];  // (a thread reads its own)
+  const Tree t = tree_at(A, blockIdx.x);
+  const bool drawn = A.q != nullptr;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  nodes.load<IO>(A, t);
+  __syncthreads();
+  Place at{-1, 0, 0, 0, 1.0};
+  Piece p[C];
+  const int first = threadIdx.x * W;
+  // (through a descriptor: what lies past the row, or all of it, is zero)
+  auto load = [&](const void* base, int values, auto&& set) {
+    const auto row = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<void*>(row_at<IO>(base, t.row + at.node + 1, A.V)), 0,
+        values * io<IO>::bytes, 0x00027000);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int from = (first + c * STEP) * io<IO>::bytes;
+      set(c, __builtin_bit_cast(Piece, __builtin_amdgcn_raw_buffer_load_b128(row, from, 0, 0)));
+    }
+  };
+  // piece c of the row behind k rejections
+  auto piece = [&](int c, int k, double (&w)[W]) {
+    p[c].fresh();
+#pragma unroll
+    for (int e = 0; e < W; ++e) w[e] = p[c][e] > 0.f ? p[c][e] : 0.f;  // (a NaN counts nothing)
+    if (drawn) {
+      if (k == 0) return;
+      const Piece by = q[c][threadIdx.x];
+      for (int j = 0; j < k; ++j) {
+        const double scale = nodes.scale[j];
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          w[e] = fmax(fma(w[e], scale, -static_cast<double>(by[e])), 0.0);
+      }
+    } else {
+      for (int j = 0; j < k; ++j) {
+        const double scale = nodes.scale[j];
+        const int x = nodes.tried[j] - (first + c * STEP);
+#pragma unroll
+        for (int e = 0; e < W; ++e) w[e] = fmax(fma(w[e], scale, e == x ? -1.0 : 0.0), 0.0);
+      }
+    }
+  };
+  // sums of the pieces of all threads (a piece: STEP tokens) into chunk
+  auto sums = [&](int k) {
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      double w[W], s = 0.0;
+      piece(c, k, w);
+#pragma unroll
+      for (int e = 0; e < W; ++e) s += w[e];
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+      if (lane == 0) chunk[c][wave] = s;
+    }
+    __syncthreads();
+  };
+  auto total = [&](int k) {
+    double s = 0.0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      double w[W];
+      piece(c, k, w);
+#pragma unroll
+      for (int e = 0; e < W; ++e) s += w[e];
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+    __syncthreads();
+    if (lane == 0) meet.part[wave] = s;
+    __syncthreads();
+    double left = 0.0;
+#pragma unroll
+    for (int o = 0; o < WAVES; ++o) left += meet.part[o];
+    return left;
+  };
+  bool moved;
+  do {
+    bool child = at.child(nodes, t);
+    while (child && at.accepts(nodes, drawn)) {
+      at.move();
+      child = at.child(nodes, t);
+    }
+    load(A.p, A.V, [&](int c, Piece v) { p[c] = v; });
+    if (child && drawn) load(A.q, A.V, [&](int c, Piece v) { q[c][threadIdx.x] = v; });
+    moved = false;
+    while (child && !moved) {
+      at.reject(nodes, total);
+      child = at.child(nodes, t);
+      if (child && at.accepts(nodes, drawn)) {
+        at.move();
+        moved = true;
+      }
+    }
+  } while (moved);
+  sums(at.m);
+  double mine = 0.0, sum = 0.0;
+  for (int c = 0; c < C; ++c) {
+    double v = 0.0;
+    for (int o = 0; o < WAVES; ++o) v += chunk[c][o];
+    if (c == static_cast<int>(threadIdx.x)) mine = v;
+    sum += v;
+  }
+  double target = static_cast<double>(nodes.u[t.size]) * sum;
+  const int which = pick(mine, &target, &meet);
+  double own[W];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    if (c == which) piece(c, at.m, own);  // (uniform)
+  const int next = find(own, first + which * STEP, target, A.V - 1, &meet);
+  if (threadIdx.x == 0) {
+    A.accepted[blockIdx.x] = at.node;
+    A.length[blockIdx.x] = at.length;
     A.next[blockIdx.x] = next;
   }
 }
@@ -334,38 +527,41 @@ __global__ __launch_bounds__(kSlabThreads) void accept_slab_kernel(Args A) {
   const Row<IO> r = chain_row<IO>(A, t, end, x, scale, tried);
   const int lo = min(k * A.slab, A.V), hi = min(lo + A.slab, A.V);
   const double sum = block_sums<IO, W>(r, lo, hi, &meet);
-  if (threadIdx.x == 0) A.part[static_cast<int64_t>(m) * A.slabs + k] = sum;
+  if (threadIdx.x == 0) {
+    A.part[static_cast<int64_t>(m) * A.slabs + k] = sum;
+    if (k == 0) A.head[m] = int2{end, x};
+  }
 }
 
 template <typename IO, int W>
 __global__ __launch_bounds__(kSlabThreads) void accept_chain_kernel(Args A) {
   __shared__ Meet meet;
-  __shared__ double scale[1], part[kSlabThreads];
+  __shared__ double scale[1];
   __shared__ int tried[1];
   const int m = blockIdx.x;
   const Tree t = tree_at(A, m);
-  int x;
-  const int end = chain_end<IO>(A, t, &x);
-  Row<IO> r = chain_row<IO>(A, t, end, x, scale, tried);
-  if (threadIdx.x < A.slabs)
-    part[threadIdx.x] = A.part[static_cast<int64_t>(m) * A.slabs + threadIdx.x];
-  __syncthreads();
-  double sum = 0.0;
-  for (int k = 0; k < A.slabs; ++k) sum += part[k];
+  const int2 head = A.head[m];
+  const int end = head.x;
+  const double part = static_cast<int>(threadIdx.x) < A.slabs
+                          ? A.part[static_cast<int64_t>(m) * A.slabs + threadIdx.x] : 0.0;
   const double u = A.u[t.row + t.size];
+  Row<IO> r = chain_row<IO>(A, t, end, head.y, scale, tried);
+  double sum = part;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  if ((threadIdx.x & 63) == 0) meet.part[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  sum = (meet.part[0] + meet.part[1]) + (meet.part[2] + meet.part[3]);
   int lo = 0, hi = A.V;
-  double target = 0.0;
+  double target;
   if (r.m > 0 && !(sum > 0.0)) {  // (uniform) nothing is left: the target's own row
     r.m = 0;
-    sum = block_sums<IO, W>(r, 0, A.V, &meet);
-    target = u * sum;
+    target = u * block_sums<IO, W>(r, 0, A.V, &meet);
   } else {
     target = u * sum;
-    const int k = pick(part, A.slabs, &target);
-    lo = min(k * A.slab, A.V);
+    lo = min(pick(part, &target, &meet) * A.slab, A.V);
     hi = min(lo + A.slab, A.V);
   }
-  __syncthreads();
   const int next = draw<IO, W>(r, lo, hi, target, A.V - 1, &meet);
   if (threadIdx.x == 0) {
     A.accepted[m] = end - 1;
@@ -374,20 +570,28 @@ __global__ __launch_bounds__(kSlabThreads) void accept_chain_kernel(Args A) {
   }
 }
 
-// Slabs of a chain's row: at least 2048 values, and no more of them than give
-// every CU two workgroups.
+// Slabs of a chain's row: 1024 values, which the second launch's workgroup
+// holds at once, more where there are more than 2048 workgroups or 256 slabs.
 void plan_slabs(const Accept& p, int* slabs, int* slab) {
-  const int64_t most = std::min<int64_t>(std::max<int64_t>(1, 512 / p.trees), kSlabThreads);
-  int64_t each = (p.V + most - 1) / most;
-  each = (std::max<int64_t>(each, 2048) + 7) / 8 * 8;
+  const int64_t V = p.V;
+  int64_t each = std::max<int64_t>(1024, (V * p.trees + 2047) / 2048);
+  each = (std::max(each, (V + kSlabThreads - 1) / kSlabThreads) + 7) / 8 * 8;
+  each = std::min(each, (V + 7) / 8 * 8);
   *slab = static_cast<int>(each);
-  *slabs = static_cast<int>((p.V + each - 1) / each);
+  *slabs = static_cast<int>((V + each - 1) / each);
 }
 
 template <typename IO, int W>
 hipError_t accept(const Args& A, hipStream_t s) {
   if (A.parent != nullptr) {
-    hipLaunchKernelGGL((accept_walk_kernel<IO, W>), dim3(A.trees), dim3(kWalkThreads), 0, s, A);
+    const dim3 grid(A.trees), threads(kWalkThreads);
+    if constexpr (W > 1) {
+      if (A.V <= kWalkThreads * kHeldPer) {
+        hipLaunchKernelGGL((accept_held_kernel<IO, W>), grid, threads, 0, s, A);
+        return hipGetLastError();
+      }
+    }
+    hipLaunchKernelGGL((accept_walk_kernel<IO, W>), grid, threads, 0, s, A);
     return hipGetLastError();
   }
   hipLaunchKernelGGL((accept_slab_kernel<IO, W>), dim3(A.trees * A.slabs), dim3(kSlabThreads), 0,
@@ -404,7 +608,7 @@ size_t accept_workspace_bytes(const Accept& p) {
   if (p.tree) return 0;
   int slabs, slab;
   plan_slabs(p, &slabs, &slab);
-  return static_cast<size_t>(p.trees) * slabs * sizeof(double);
+  return static_cast<size_t>(p.trees) * (slabs * sizeof(double) + sizeof(int2));
 }
 
 hipError_t launch_accept(const Accept& p, const int32_t* parent, const int32_t* tokens,
@@ -427,6 +631,7 @@ hipError_t launch_accept(const Accept& p, const int32_t* parent, const int32_t* 
   A.next = next;
   plan_slabs(p, &A.slabs, &A.slab);
   A.part = static_cast<double*>(ws);
+  A.head = reinterpret_cast<int2*>(A.part + static_cast<int64_t>(A.trees) * A.slabs);
   StageScope scope(GDN_STAGE_OTHER, s);
   // whole rows of 16-byte pieces, else one value at a time
   if (p.io == GDN_BF16)

@@ -46,9 +46,11 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 // ------------------------------------------------------------- functions ---
 
-// e^x; what the product x log2(e) loses goes back in (a large |x| ends at
-// infinity or zero by itself)
+// e^x for |x| <= 87, the ends beyond (a NaN gives one of them: its users keep
+// the NaN by themselves); what the product x log2(e) loses goes back in.  No
+// branches in these: they stand between the loads of every token.
 __device__ inline float exp_full(float x) {
+  x = __builtin_amdgcn_fmed3f(x, -87.f, 87.f);
   const float t = x * kLog2e;
   const float e = __builtin_amdgcn_exp2f(t);
   return fmaf(e * kLn2, fmaf(x, kLog2e, -t), e);
@@ -57,17 +59,15 @@ __device__ inline float exp_full(float x) {
 // softplus(v) = max(v, 0) + log(1 + u), u = e^{-|v|}: w = 1 + u is off by
 // d = u - (w - 1), log(w + d) = log(w) + d to 2^-25 of the result.
 __device__ inline float softplus(float v) {
-  const float x = -fabsf(v), u = x < -104.f ? 0.f : exp_full(x);
-  const float w = 1.f + u;
-  return (v > 0.f ? v : 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), u - (w - 1.f));
+  const float u = exp_full(-fabsf(v)), w = 1.f + u;
+  return (v < 0.f ? 0.f : v) + fmaf(kLn2, __builtin_amdgcn_logf(w), u - (w - 1.f));
 }
 
 // bf16 rows take the exponential as it is (its error, |v| 2^-24, is far below
-// their rounding)
+// their rounding).
 template <typename IO>
 __device__ inline float sigmoid(float v) {
-  const float e = io<IO>::bytes == 2 ? __builtin_amdgcn_exp2f(-v * kLog2e)
-                                     : v < -87.f ? INFINITY : v > 104.f ? 0.f : exp_full(-v);
+  const float e = io<IO>::bytes == 2 ? __builtin_amdgcn_exp2f(-v * kLog2e) : exp_full(-v);
   return __builtin_amdgcn_rcpf(1.f + e);
 }
 
@@ -257,21 +257,24 @@ __device__ inline Lane<NS> lane_of(const Args& A, int WS) {
 template <typename IO, int N, bool PAD>
 struct Row {
   uint32_t w[N * io<IO>::bytes / 4];
-  // from: the wave's part of the row
-  __device__ inline void load(uintptr_t from, int left) {
+  int left;
+  // from: the wave's part of the row (its last four states where it has fewer)
+  __device__ inline void load(uintptr_t from, int states) {
+    left = states;
 #pragma unroll
     for (int q = 0; q < N; q += 4) {
-      const int n = !PAD || q < left ? q : left - 4;
+      const int n = PAD ? min(q, states - 4) : q;
       const GDN_CONST uint32_t* s =
           reinterpret_cast<const GDN_CONST uint32_t*>(from + n * io<IO>::bytes);
 #pragma unroll
-      for (int i = 0; i < io<IO>::bytes; ++i)
-        w[q * io<IO>::bytes / 4 + i] = PAD && q >= left ? 0 : s[i];
+      for (int i = 0; i < io<IO>::bytes; ++i) w[q * io<IO>::bytes / 4 + i] = s[i];
     }
   }
   __device__ inline float operator[](int n) const {
-    if constexpr (io<IO>::bytes == 4) return __uint_as_float(w[n]);
-    return __uint_as_float(n & 1 ? w[n >> 1] & 0xffff0000u : w[n >> 1] << 16);
+    uint32_t u;
+    if constexpr (io<IO>::bytes == 4) u = w[n];
+    else u = n & 1 ? w[n >> 1] & 0xffff0000u : w[n >> 1] << 16;
+    return __uint_as_float(PAD && (n & ~3) >= left ? 0u : u);
   }
   // Unpacks anew from here on (kept unpacked, a row takes a register a value).
   __device__ inline void pack() {
@@ -338,7 +341,8 @@ __device__ inline void store_x(void* p, const Args& A, int64_t tok, int ch, floa
 }
 
 __device__ inline float step_of(const Args& A, float dt, float bias) {
-  return A.softplus ? softplus(dt + bias) : dt + bias;
+  const float v = dt + bias, s = softplus(v);
+  return A.softplus ? s : v;
 }
 
 __device__ inline float decay(float delta, float a2) {
@@ -371,33 +375,72 @@ __device__ inline void enter(const Args& A, const Lane<NS>& l, const Span& s, co
   }
 }
 
+// A run's rows of b or c, fetched ahead of their tokens: a group of U tokens at
+// once where that takes few scalars (one wait a group, which is what few waves
+// feel), else one token.
+template <typename IO, int NS, bool PAD, int U>
+struct Ahead {
+  static constexpr bool GROUP = NS * io<IO>::bytes <= 16;
+  typedef Row<IO, NS, PAD> row;
+  row next[GROUP ? U : 1], cur[GROUP ? U : 1];
+  uintptr_t from;  // the group's first row
+  int step, left;  // bytes of a row; states of the wave
+  __device__ inline void start(uintptr_t p, int row_step, int states, int tokens) {
+    from = p;
+    step = row_step;
+    left = states;
+    if (tokens > 0) fetch(0, tokens);
+  }
+  // the group from token `at` on (or that token) of those that are left
+  __device__ inline void fetch(int at, int tokens) {
+#pragma unroll
+    for (int u = 0; u < (GROUP ? U : 1); ++u) next[u].load(from + min(at + u, tokens - 1) * step, left);
+  }
+  __device__ inline void take() {
+#pragma unroll
+    for (int u = 0; u < (GROUP ? U : 1); ++u) cur[u] = next[u];
+  }
+  __device__ inline const row& operator[](int u) const { return cur[GROUP ? u : 0]; }
+  __device__ inline void group_done() { from += U * step; }
+};
+
 // Walks a run in groups of four tokens, the next group's rows and the next
 // token's b on their way: f(t, left, x, u, delta, b) for token u of the group
 // at t.  Tokens past the run have x = delta = 0, which leaves a state as it is.
 template <typename IO, int NS, bool PAD, typename F>
 __device__ inline void walk(const Args& A, const Lane<NS>& l, const Run& r, F f) {
   constexpr int U = 4;
+  typedef Ahead<IO, NS, PAD, U> ahead;
   Rows<IO, U> x, dt;
-  Row<IO, NS, PAD> next;
+  ahead b;
   int left = static_cast<int>(r.hi - r.lo);
   x.load(A, A.x, r.lo, left, l.row);
   dt.load(A, A.dt, r.lo, left, l.row);
-  uintptr_t from = row_of<IO>(A, l, A.b, r.lo);
-  const int step = row_step<IO>(A);
-  if (left > 0) next.load(from, l.left);
-  for (int64_t t = r.lo; left > 0; t += U, left -= U, from += U * step) {
+  b.start(row_of<IO>(A, l, A.b, r.lo), row_step<IO>(A), l.left, left);
+  for (int64_t t = r.lo; left > 0; t += U, left -= U) {
     const Rows<IO, U> xs = x, dts = dt;
     x.load(A, A.x, t + U, left - U, l.row);
     dt.load(A, A.dt, t + U, left - U, l.row);
+    float delta[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) delta[u] = u < left ? step_of(A, dts[u], l.bias) : 0.f;
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (ahead::GROUP) {
+      b.take();
+      b[0].arrive();
+      b.fetch(U, left);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const Row<IO, NS, PAD> b = next;
-      b.arrive();
-      next.load(from + min(u + 1, left - 1) * step, l.left);
-      const float delta = u < left ? step_of(A, dts[u], l.bias) : 0.f;
-      f(t, left, xs, u, delta, b);
+      if constexpr (!ahead::GROUP) {
+        b.take();
+        b[0].arrive();
+        b.fetch(u + 1, left);
+      }
+      f(t, left, xs, u, delta[u], b[u]);
       __builtin_amdgcn_sched_barrier(0);
     }
+    b.group_done();
   }
 }
 
@@ -518,40 +561,48 @@ __global__ __launch_bounds__(64 * waves_of(WS)) void scan_out_kernel(Args A) {
     float h[NS];
     enter<NS, PAD>(A, l, s, r, h);
     Rows<IO, U> x, dt, z{};
-    Row<IO, NS, PAD> nextb, nextc;
+    typedef Ahead<IO, NS, PAD, U> ahead;
+    ahead bs, cs;
     int left = static_cast<int>(r.hi - r.lo);
     x.load(A, A.x, r.lo, left, l.row);
     dt.load(A, A.dt, r.lo, left, l.row);
     if constexpr (GATE) z.load(A, A.z, r.lo, left, l.row);
-    uintptr_t fromb = row_of<IO>(A, l, A.b, r.lo), fromc = row_of<IO>(A, l, A.c, r.lo);
-    const int step = row_step<IO>(A);
-    if (left > 0) {
-      nextb.load(fromb, l.left);
-      nextc.load(fromc, l.left);
-    }
-    for (int64_t t = r.lo; left > 0; t += U, left -= U, fromb += U * step, fromc += U * step) {
+    bs.start(row_of<IO>(A, l, A.b, r.lo), row_step<IO>(A), l.left, left);
+    cs.start(row_of<IO>(A, l, A.c, r.lo), row_step<IO>(A), l.left, left);
+    for (int64_t t = r.lo; left > 0; t += U, left -= U) {
       const Rows<IO, U> xs = x, dts = dt, zs = z;
       float y[U];
       x.load(A, A.x, t + U, left - U, l.row);
       dt.load(A, A.dt, t + U, left - U, l.row);
       if constexpr (GATE) z.load(A, A.z, t + U, left - U, l.row);
+      auto ahead_of = [&](int at) {
+        bs.take();
+        cs.take();
+        bs[0].arrive();
+        bs.fetch(at, left);
+        cs.fetch(at, left);
+      };
+      float delta[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) delta[u] = u < left ? step_of(A, dts[u], l.bias) : 0.f;
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (ahead::GROUP) ahead_of(U);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const Row<IO, NS, PAD> b = nextb, c = nextc;
-        b.arrive();
-        const int at = min(u + 1, left - 1) * step;
-        nextb.load(fromb + at, l.left);
-        nextc.load(fromc + at, l.left);
-        const float delta = u < left ? step_of(A, dts[u], l.bias) : 0.f, dx = delta * xs[u];
+        if constexpr (!ahead::GROUP) ahead_of(u + 1);
+        const Row<IO, NS, PAD>&b = bs[u], &c = cs[u];
+        const float dx = delta[u] * xs[u];
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-          h[n] = fmaf(decay(delta, l.a2[n]), h[n], dx * b[n]);
+          h[n] = fmaf(decay(delta[u], l.a2[n]), h[n], dx * b[n]);
           sum[n & 3] = fmaf(c[n], h[n], sum[n & 3]);
         }
         y[u] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
         __builtin_amdgcn_sched_barrier(0);
       }
+      bs.group_done();
+      cs.group_done();
       if constexpr (WS > 1) {
         __syncthreads();
 #pragma unroll
@@ -628,14 +679,13 @@ __global__ __launch_bounds__(512) void scan_marks_kernel(Args A, int WS) {
     };
     if (r.cont) {
       constexpr int U = 4;
-      Rows<IO, U> dy, z{};
-      Row<IO, NS, PAD> next;
+      typedef Ahead<IO, NS, PAD, U> ahead;
+      Rows<IO, U> dy, z{}, dys, zs{};
+      ahead cs;
       const int all = static_cast<int>(r.hi - r.lo);
       dy.load(A, A.dy, r.lo, all, l.row);
       if constexpr (GATE) z.load(A, A.z, r.lo, all, l.row);
-      const int step = row_step<IO>(A);
-      next.load(row_of<IO>(A, l, A.c, r.lo), l.left);
-      Rows<IO, U> dys, zs{};
+      cs.start(row_of<IO>(A, l, A.c, r.lo), row_step<IO>(A), l.left, all);
       walk<IO, NS, PAD>(A, l, r, [&](int64_t t, int left, const Rows<IO, U>& x, int u,
                                      float delta, const Row<IO, NS, PAD>& b) {
         if (u == 0) {
@@ -645,8 +695,11 @@ __global__ __launch_bounds__(512) void scan_marks_kernel(Args A, int WS) {
           dy.load(A, A.dy, t + U, left - U, l.row);
           if constexpr (GATE) z.load(A, A.z, t + U, left - U, l.row);
         }
-        const Row<IO, NS, PAD> c = next;
-        next.load(row_of<IO>(A, l, A.c, t) + min(u + 1, left - 1) * step, l.left);
+        if (!ahead::GROUP || u == 0) {
+          cs.take();
+          cs.fetch(ahead::GROUP ? U : u + 1, left);
+        }
+        const Row<IO, NS, PAD>& c = cs[u];
         const float dx = delta * x[u];
         const float v = GATE ? dys[u] * zs[u] * sigmoid<IO>(zs[u]) : dys[u];
         sum += delta;
@@ -657,6 +710,7 @@ __global__ __launch_bounds__(512) void scan_marks_kernel(Args A, int WS) {
           front[n] *= e;
           g[n] = fmaf(front[n], c[n] * v, g[n]);
         }
+        if (u == U - 1) cs.group_done();
       });
     } else {
       walk<IO, NS, PAD>(A, l, r, [&](int64_t t, int, const Rows<IO, 4>& x, int u, float delta,
@@ -793,14 +847,18 @@ __global__ __launch_bounds__(64 * waves_of(WS), 2) void scan_grad_kernel(Args A)
           Row<IO, NS, PAD> next;
           const uintptr_t from = row_of<IO>(A, l, A.b, t);
           next.load(from, l.left);
+          float delta[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) delta[u] = step_of(A, dt[u], l.bias);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const Row<IO, NS, PAD> b = next;
             b.arrive();
             next.load(from + min(u + 1, U - 1) * step, l.left);
-            const float delta = step_of(A, dt[u], l.bias), dx = delta * x[u];
+            const float dx = delta[u] * x[u];
 #pragma unroll
-            for (int n = 0; n < NS; ++n) h[n] = fmaf(decay(delta, l.a2[n]), h[n], dx * b[n]);
+            for (int n = 0; n < NS; ++n) h[n] = fmaf(decay(delta[u], l.a2[n]), h[n], dx * b[n]);
             __builtin_amdgcn_sched_barrier(0);
           }
         }
@@ -932,7 +990,8 @@ __global__ __launch_bounds__(64 * waves_of(WS), 2) void scan_grad_kernel(Args A)
             }
           }
           float v = fmaf(x[u], vb, kLn2 * va);
-          if (A.softplus) v *= sigmoid<IO>(pre[u] + l.bias);
+          const float rise = sigmoid<IO>(pre[u] + l.bias);
+          v *= A.softplus ? rise : 1.f;
           dd = fmaf(dy[u], x[u], dd);
           dbias += u < left ? v : 0.f;
           outx.store(u, l.row, fmaf(l.d, dy[u], delta[u] * vb));
@@ -952,26 +1011,45 @@ __global__ __launch_bounds__(64 * waves_of(WS), 2) void scan_grad_kernel(Args A)
   }
 }
 
-// db, dc: the channel blocks' shares of every token, group and state.
-template <typename IO>
-__global__ __launch_bounds__(256) void scan_bc_kernel(Args A, int64_t tokens, int NS, int WS,
-                                                      void* db, void* dc) {
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int per = 2 * A.dk;
-  const int64_t row = e / per;  // token and group
-  if (row >= tokens * A.hb) return;
-  const int k = static_cast<int>(e - row * per), n = k % A.dk, two = k / A.dk;
-  const float* p = A.part + (row * A.nb * WS + n / NS) * (2 * NS) + two * NS + n % NS;
-  float s = 0.f;
-  for (int u = 0; u < A.nb; ++u) s += p[static_cast<int64_t>(u) * WS * 2 * NS];
-  io<IO>::store(two ? dc : db, row * A.dk + n, s);
-}
+// The shares of the gradient walk added in a fixed order, one launch for all:
+// db, dc (the channel blocks' of every token, group and state; a thread each),
+// then da, dd, dt_bias (rows of shares; sixteen columns a workgroup, its
+// sixteen runs of rows added up in LDS).
+struct Finish {
+  int64_t tokens;
+  int NS, WS;
+  int64_t rows;            // segments
+  unsigned first[4];       // first workgroup of each part: da, dd, dbias, the end
+  void *db, *dc;
+  float *da, *dd, *dbias;
+};
 
-// da, dd, dt_bias: the rows of shares of each column added in a fixed order.
-__global__ __launch_bounds__(256) void scan_sum_kernel(const float* part, int64_t rows,
-                                                       int64_t cols, float* out) {
+template <typename IO>
+__global__ __launch_bounds__(256) void scan_finish_kernel(Args A, Finish F) {
+  if (blockIdx.x < F.first[0]) {
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int per = 2 * A.dk;
+    const int64_t row = e / per;  // token and group
+    if (row >= F.tokens * A.hb) return;
+    const int k = static_cast<int>(e - row * per), n = k % A.dk, two = k / A.dk;
+    const int unit = F.WS * 2 * F.NS;
+    const float* p = A.part + row * A.nb * unit + n / F.NS * (2 * F.NS) + two * F.NS + n % F.NS;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < A.nb; u += 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (u + i < A.nb) s[i] += p[static_cast<int64_t>(u + i) * unit];
+    }
+    io<IO>::store(two ? F.dc : F.db, row * A.dk + n, (s[0] + s[1]) + (s[2] + s[3]));
+    return;
+  }
+  const int which = blockIdx.x < F.first[1] ? 0 : blockIdx.x < F.first[2] ? 1 : 2;
+  const float* part = which == 0 ? A.pa : which == 1 ? A.pd : A.pb;
+  float* out = which == 0 ? F.da : which == 1 ? F.dd : F.dbias;
+  const int64_t rows = which == 0 ? F.rows : F.rows * F.WS;
+  const int64_t cols = which == 0 ? static_cast<int64_t>(A.D) * A.dk : A.D;
   const int lc = threadIdx.x & 15, run = threadIdx.x >> 4;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 16 + lc;
+  const int64_t c = static_cast<int64_t>(blockIdx.x - F.first[which]) * 16 + lc;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < cols) {
     for (int64_t k = run; k < rows; k += 64) {
@@ -1124,7 +1202,7 @@ Plan plan_scan(const Scan& p) {
     q.ns /= 2;
     split();
   }
-  q.pad = q.ns < 16 || p.dk != q.ns * q.ws;
+  q.pad = p.dk != q.ns * q.ws;
   return q;
 }
 
@@ -1220,14 +1298,7 @@ void launch_chain(const Args& A, const Plan& q, int ways, hipStream_t s) {
                      dim3(64 * kChainWaves), 0, s, A, blocks);
 }
 
-void launch_sum(const float* part, int64_t rows, int64_t cols, float* out, hipStream_t s) {
-  if (out == nullptr) return;
-  hipLaunchKernelGGL(scan_sum_kernel, dim3(static_cast<unsigned>(ceil_div(cols, 16))), dim3(256),
-                     0, s, part, rows, cols, out);
-}
-
-// Calls f<NS, WS, PAD, GATE> of a plan (fewer than 16 states a lane are always
-// taken for padded: their scalars are not what bounds them).
+// Calls f<NS, WS, PAD, GATE> of a plan.
 template <typename F>
 void with_plan(const Plan& q, bool gate, F f) {
   using std::integral_constant;
@@ -1236,10 +1307,8 @@ void with_plan(const Plan& q, bool gate, F f) {
     else f(ns, ws, pad, std::false_type{});
   };
   auto pads = [&](auto ns, auto ws) {
-    if constexpr (ns == 16) {
-      if (!q.pad) return all(ns, ws, std::false_type{});
-    }
-    all(ns, ws, std::true_type{});
+    if (!q.pad) return all(ns, ws, std::false_type{});
+    if constexpr (ns * ws > 4) all(ns, ws, std::true_type{});
   };
   auto waves = [&](auto ns) {
     if (q.ws == 1) return pads(ns, integral_constant<int, 1>{});
@@ -1309,13 +1378,12 @@ hipError_t scan_bwd(const Plan& q, const Args& A, int64_t tokens, const ScanGrad
   });
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (tokens > 0)
-    hipLaunchKernelGGL((scan_bc_kernel<IO>),
-                       dim3(static_cast<unsigned>(ceil_div(tokens * A.hb * 2 * A.dk, 256))),
-                       dim3(256), 0, s, A, tokens, q.ns, q.ws, out.db, out.dc);
-  launch_sum(A.pa, q.segs, size, out.da, s);
-  launch_sum(A.pd, q.segs * q.ws, A.D, out.dd, s);
-  launch_sum(A.pb, q.segs * q.ws, A.D, out.dbias, s);
+  Finish F{tokens, q.ns, q.ws, q.segs, {}, out.db, out.dc, out.da, out.dd, out.dbias};
+  F.first[0] = static_cast<unsigned>(ceil_div(tokens * A.hb * 2 * A.dk, 256));
+  F.first[1] = F.first[0] + static_cast<unsigned>(ceil_div(size, 16));
+  F.first[2] = F.first[1] + (out.dd != nullptr ? static_cast<unsigned>(ceil_div(A.D, 16)) : 0);
+  F.first[3] = F.first[2] + (out.dbias != nullptr ? static_cast<unsigned>(ceil_div(A.D, 16)) : 0);
+  hipLaunchKernelGGL((scan_finish_kernel<IO>), dim3(F.first[3]), dim3(256), 0, s, A, F);
   return hipGetLastError();
 }
 
@@ -1329,7 +1397,8 @@ bool scan_fits(const Scan& p) {
   const int64_t rows = static_cast<int64_t>(p.B) * p.T;
   const int64_t unit = ceil_div(q.units, waves_of(q.ws) / q.ws) * 64 * waves_of(q.ws);
   return q.segs <= most / unit && q.chains <= most / (2 * 64 * kChainWaves) / state &&
-         rows <= most / (2 * p.dk) / p.hb - 256;
+         rows * p.hb * 2 * p.dk + 16 * (state * 64 + 2 * static_cast<int64_t>(p.H) * p.dv) + 1024 <=
+             most;
 }
 
 size_t scan_fwd_workspace_bytes(const Scan& p) {
