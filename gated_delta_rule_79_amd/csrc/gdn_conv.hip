@@ -155,14 +155,14 @@ struct Weights {
 #pragma unroll
     for (int i = 0; i < V * W; i += P) load_v<f32_t, P>(A.taps, c * W + i, all + i);
 #pragma unroll
-    for (int i = 0; i < V; i += P) {
-      if (A.bias != nullptr) load_v<f32_t, P>(A.bias, c + i, bias + i);
+    for (int e = 0; e < V; ++e) {
+      bias[e] = 0.f;
 #pragma unroll
-      for (int e = i; e < i + P; ++e) {
-        if (A.bias == nullptr) bias[e] = 0.f;
+      for (int j = 0; j < W; ++j) tap[j][e] = all[e * W + j];
+    }
+    if (A.bias != nullptr) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) tap[j][e] = all[e * W + j];
-      }
+      for (int i = 0; i < V; i += P) load_v<f32_t, P>(A.bias, c + i, bias + i);
     }
   }
   // p_t from the input of the token and the W - 1 in front of it, x[j] the
