@@ -766,6 +766,13 @@ def _packed(cu_seqlens, x):
     return cu_seqlens.numel() - 1
 
 
+def _apart(out, name, **inputs):
+    """Refuses an output that is one of the inputs."""
+    for other, t in inputs.items():
+        if t is not None and out is not None and out.numel() and out.data_ptr() == t.data_ptr():
+            raise ValueError(f"{name} must not be {other}")
+
+
 def _scan_problem(x, dt, a, b, c, d, dt_bias, z, cu_seqlens, seg_chunks, lead):
     """The problem of a selective-scan call, its rows of b and c, and the shape
     of its states; `lead`: dimensions in front of the heads."""
@@ -805,6 +812,8 @@ def selective_scan_fwd(x, dt, a, b, c, d=None, dt_bias=None, z=None, s0=None,
     _want(s0, "s0", states, torch.float32, x.device)
     y = _result(y, "y", x)
     sf = _states(s_final, "s_final", states, x.device, s0) if output_final_state else None
+    _apart(y, "y", x=x, dt=dt, z=z)
+    _apart(sf, "s_final", s0=s0)
     ws, nbytes = _workspace(workspace, _bytes(lib.gdn_selective_scan_fwd_workspace, p, hb),
                             x.device)
     _launch(lib.gdn_selective_scan_fwd, x.device, ctypes.byref(p), hb, int(softplus), _ptr(x),
@@ -886,14 +895,14 @@ def short_conv_fwd(x, taps, bias=None, s0=None, act: str = "silu", cu_seqlens=No
     p, width, code, hist = _conv_problem(x, taps, bias, act, cu_seqlens, 2)
     _want(s0, "s0", hist, x.dtype, x.device)
     y = _result(y, "y", x)
+    _apart(y, "y", x=x)
     if not output_final_state:
         s_final = None
     elif s_final is None:
         s_final = torch.empty(hist, dtype=x.dtype, device=x.device)
     else:
         _want(s_final, "s_final", hist, x.dtype, x.device)
-        if s0 is not None and s_final.data_ptr() == s0.data_ptr() and s0.numel():
-            raise ValueError("s_final must not be s0")
+        _apart(s_final, "s_final", s0=s0)
     _launch(lib.gdn_short_conv_fwd, x.device, ctypes.byref(p), width, code, _ptr(x), _ptr(taps),
             _ptr(bias), _ptr(s0), _ptr(y), _ptr(s_final))
     return y, s_final

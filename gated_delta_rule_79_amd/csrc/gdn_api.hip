@@ -1256,6 +1256,7 @@ gdn_status check_packing(const gdn_problem* p) {
     if (p->B != 1) return GDN_FAIL(GDN_ERR_SHAPE);
     if (p->cu_seqlens == nullptr) return GDN_FAIL(GDN_ERR_NULL);
     if ((reinterpret_cast<uintptr_t>(p->cu_seqlens) & 3u) != 0) return GDN_FAIL(GDN_ERR_ALIGN);
+    if (p->nseq > (1 << 29)) return GDN_FAIL(GDN_ERR_SHAPE);
   } else if (p->cu_seqlens != nullptr) {
     return GDN_FAIL(GDN_ERR_SHAPE);
   }
@@ -1274,6 +1275,8 @@ gdn_status check_scan(const gdn_problem* p, int32_t hb, int32_t softplus, bool s
   if (p->dk < 4 || p->dk > 64 || p->dk % 4 != 0) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
   const int64_t ch = static_cast<int64_t>(p->H) * p->dv;
   if (ch > (int64_t(1) << 22)) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
+  // (eight tokens' rows of b or c within 32 bits of bytes)
+  if (static_cast<int64_t>(hb) * p->dk > (1 << 24)) return GDN_FAIL(GDN_ERR_UNSUPPORTED);
   if (!step) GDN_TRY(check_packing(p));
   out->B = p->B;
   out->T = step ? 1 : p->T;

@@ -197,6 +197,14 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
                                            0x00027000);
 }
 
+// A rate in powers of two, kept finite so that no step at all (a token past
+// its run) leaves a state as it is; of a rate of -inf the smallest step that
+// there is leaves nothing all the same.
+__device__ inline float rate_of(float a) {
+  const float a2 = a * kLog2e;
+  return a2 < -3.4e38f ? -3.4e38f : a2;
+}
+
 // What a lane keeps of its channel.
 template <int NS>
 struct Lane {
@@ -245,7 +253,7 @@ __device__ inline Lane<NS> lane_of(const Args& A, int WS) {
   l.state = l.live ? 4u * (head * A.dk * A.dv + l.ch - head * A.dv + l.n0 * A.dv) : kNowhere;
   load_state<NS, PAD>(A, l, A.a, l.a2);
 #pragma unroll
-  for (int i = 0; i < NS; ++i) l.a2[i] *= kLog2e;
+  for (int i = 0; i < NS; ++i) l.a2[i] = rate_of(l.a2[i]);
   l.bias = A.bias != nullptr ? A.bias[l.ch] : 0.f;
   l.d = A.d != nullptr ? A.d[l.ch] : 0.f;
   return l;
@@ -498,7 +506,7 @@ __global__ __launch_bounds__(64 * kChainWaves) void scan_chain_kernel(Args A, in
   const int64_t e = min((block - chain * wide) * 64 + lane, size - 1);  // (the last one again)
   const int head = static_cast<int>(e / (A.dk * A.dv));
   const int ch = head * A.dv + static_cast<int>(e % A.dv);
-  const float a2 = A.a[e] * kLog2e;
+  const float a2 = rate_of(A.a[e]);
   float* h = (back ? A.g : A.h) + at * size + e;
   const float* sum = A.sum + at * A.D + ch;
   const int* cut = (back ? A.cutr : A.cut) + at;
@@ -508,13 +516,16 @@ __global__ __launch_bounds__(64 * kChainWaves) void scan_chain_kernel(Args A, in
   auto place = [&](int i) { return back ? last - i : i; };
   const int share = (A.S + kChainWaves - 1) / kChainWaves;
   const int lo = min(wave * share, A.S), hi = min(lo + share, A.S);
+  // A decay below zero is a cut: nothing passes it, a NaN of another sequence
+  // neither.
+  auto join = [](float p, float state, float v) { return p < 0.f ? v : fmaf(p, state, v); };
   float v[U], p[U];
   auto load = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = place(min(i0 + u, max(last - 1, 0)));
       v[u] = h[k * size];
-      p[u] = cut[k] ? 0.f : decay(sum[static_cast<int64_t>(k) * A.D], a2);
+      p[u] = cut[k] ? -1.f : decay(sum[static_cast<int64_t>(k) * A.D], a2);
     }
   };
   float all = 1.f, state = 0.f;
@@ -523,22 +534,22 @@ __global__ __launch_bounds__(64 * kChainWaves) void scan_chain_kernel(Args A, in
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i + u >= hi) break;
-      all *= p[u];
-      state = fmaf(p[u], state, v[u]);
+      all = p[u] < 0.f || all < 0.f ? -1.f : all * p[u];
+      state = join(p[u], state, v[u]);
     }
   }
   decays[wave][lane] = all;
   values[wave][lane] = state;
   __syncthreads();
   state = 0.f;
-  for (int w = 0; w < wave; ++w) state = fmaf(decays[w][lane], state, values[w][lane]);
+  for (int w = 0; w < wave; ++w) state = join(decays[w][lane], state, values[w][lane]);
   for (int i = lo; i < hi; i += U) {
     if (share > U) load(i);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i + u >= hi) break;
       if ((block - chain * wide) * 64 + lane < size) h[place(i + u) * size] = state;
-      state = fmaf(p[u], state, v[u]);
+      state = join(p[u], state, v[u]);
     }
   }
 }
@@ -1136,7 +1147,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(Args A, int64_t threads)
       if (n0 + i >= A.dk) break;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        h[i][v] = fmaf(decay(delta[v], a[i][v] * kLog2e), h[i][v], dx[v] * b[i]);
+        h[i][v] = fmaf(decay(delta[v], rate_of(a[i][v])), h[i][v], dx[v] * b[i]);
         y[v] = fmaf(c[i], h[i][v], y[v]);
       }
       *reinterpret_cast<vec*>(p + (n0 + i) * A.dv) = h[i];

@@ -513,14 +513,16 @@ gdn_status gdn_group_norm_bwd(const gdn_problem* p, int32_t d, int32_t act, int3
  *               sequences are cut on the grid of all tokens; < 0 walks a
  *               packed batch as one); gate must be GDN_GATE_NONE; chunk and
  *               gate_dtype are ignored.  dk: a multiple of 4 up to 64; dv >= 1;
- *               H dv <= 2^22 (else GDN_ERR_UNSUPPORTED).
+ *               H dv <= 2^22, hb dk <= 2^24 (else GDN_ERR_UNSUPPORTED).
  *   hb        : rows of b and c of a token; head h reads row h / (H / hb).
  *               hb in 1 .. H dividing H, else GDN_ERR_SHAPE.
  *   x, dt, z, y : [B, T, H, dv] io_dtype; z NULL = no gate.
  *   b, c      : [B, T, hb, dk] io_dtype.
- *   a         : [H, dk, dv] fp32 (laid out as a state), finite, normally < 0.
+ *   a         : [H, dk, dv] fp32 (laid out as a state), normally < 0; of a rate
+ *               of -inf no step leaves anything.
  *   d, dt_bias : [H, dv] fp32, each may be NULL (zeros).
  *   s0, s_final : [nseq, H, dk, dv] fp32 or NULL, as in gdn_chunk_fwd.
+ *   No output may overlap an input, s_final s0 neither.
  *   ws        : at least gdn_selective_scan_fwd_workspace bytes; calls that
  *               overlap in time (streams, captured graphs) need one each.
  * All arithmetic is fp32, the state too.  Rows of packed tensors behind
@@ -569,7 +571,8 @@ gdn_status gdn_selective_scan_step(const gdn_problem* p, int32_t hb, int32_t sof
  *   taps      : [H, dv, width] fp32.   bias : [H, dv] fp32 or NULL.
  *   s0, s_final : [nseq, width - 1, H, dv] io_dtype, a sequence's last
  *               width - 1 inputs, oldest first; s0 NULL = zeros, s_final NULL
- *               to skip it.  s_final must not be s0.
+ *               to skip it.
+ * No output may overlap an input: y not x, s_final not s0.
  * Rows behind cu_seqlens[nseq] are neither read nor written. */
 gdn_status gdn_short_conv_fwd(const gdn_problem* p, int32_t width, int32_t act, const void* x,
                               const float* taps, const float* bias, const void* s0, void* y,

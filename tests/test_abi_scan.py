@@ -77,6 +77,22 @@ def test_scan_problem_refusals(lib, which, kw, hb, status):
         assert need(getattr(lib, f"gdn_selective_scan_{which}_workspace"), prob(**kw), hb)[0] == status
 
 
+@pytest.mark.parametrize("which", ["fwd", "bwd", "step"])
+def test_scan_rows_of_b_and_c_are_bounded(lib, which):
+    # eight of them are addressed with 32 bits
+    p = prob(T=1, H=1 << 20, dv=1, dk=16)
+    assert scan(lib, which, p, hb=1 << 20) == HIP
+    p.dk = 20
+    assert scan(lib, which, p, hb=1 << 20) == UNSUPPORTED
+    assert scan(lib, which, p, hb=1 << 10) == HIP
+
+
+def test_sequences_are_bounded(lib):
+    p = prob(T=5, H=1, dk=4, dv=1, nseq=(1 << 29) + 1, cu_seqlens=A)
+    assert scan(lib, "fwd", p, hb=1) == SHAPE and scan(lib, "bwd", p, hb=1) == SHAPE
+    assert conv(lib, "fwd", p) == SHAPE and conv(lib, "bwd", p) == SHAPE
+
+
 PACKING = [(dict(T=-1), SHAPE), (dict(nseq=-1), SHAPE), (dict(nseq=2, B=2, cu_seqlens=A), SHAPE),
            (dict(nseq=2), NULL), (dict(cu_seqlens=A), SHAPE),
            (dict(nseq=2, cu_seqlens=A + 2), ALIGN), (dict(T=(1 << 30) + 1), SHAPE),

@@ -295,6 +295,47 @@ def test_a_bad_sequence_stays_alone(gpu_lib):
                     assert np.allclose(np64(got[8])[n], ref.bwd[8][n], rtol=1e-3, atol=1e-3)
 
 
+@pytest.mark.parametrize("token", [5, 60, 200, 399])
+def test_a_bad_sequence_passes_no_segment_of_another(gpu_lib, token):
+    # every sequence lies in several segments and ends inside one, so that the
+    # states (and, backwards, the gradients) of a bad one meet the next one's
+    # where the segments are chained
+    cu = [0, 40, 70, 300, 360, 400]
+    d = make(1, 400, 2, 1, 16, 40, F32, cu=cu)
+    ref = Reference(d, cu)
+    sick = int(np.searchsorted(cu, token, side="right")) - 1
+    for bad in (float("nan"), float("inf")):
+        e = {n: None if t is None else t.clone() for n, t in d.items()}
+        for k in ("x", "dy"):
+            e[k][0, token] = bad
+        g = gpu(e)
+        for seg in (0, 1, 2, -1):
+            y, sf = run_fwd(g, cu, seg_chunks=seg)
+            got = run_bwd(g, cu, seg_chunks=seg)
+            for n in (i for i in range(5) if i != sick):
+                lo, hi = cu[n], cu[n + 1]
+                for t, r in ((y, ref.fwd[0]), (got[0], ref.bwd[0]), (got[1], ref.bwd[1]),
+                             (got[3], ref.bwd[3]), (got[4], ref.bwd[4]), (got[7], ref.bwd[7])):
+                    assert np.allclose(np64(t)[:, lo:hi], r[:, lo:hi], rtol=1e-3, atol=1e-3)
+                assert np.allclose(np64(sf)[n], ref.fwd[1][n], rtol=1e-3, atol=1e-3)
+                assert np.allclose(np64(got[8])[n], ref.bwd[8][n], rtol=1e-3, atol=1e-3)
+
+
+def test_rates_of_minus_infinity(gpu_lib):
+    # such a state holds its token's write alone: what a rate too large for any
+    # step gives
+    for cu in (None, [0, 37, 38, 70]):
+        d = make(1 if cu else 2, 70, 2, 1, 16, 40, F32, cu=cu)
+        gone = torch.rand(d["a"].shape, generator=torch.Generator().manual_seed(8)) < 0.25
+        d["a"][gone] = -1e30
+        ref = Reference(d, cu)
+        d["a"][gone] = -float("inf")
+        g = gpu(d)
+        for seg in (0, 1, -1):
+            ref.check_fwd(F32, *run_fwd(g, cu, seg_chunks=seg))
+            ref.check_bwd(F32, run_bwd(g, cu, seg_chunks=seg))
+
+
 def test_bounds_out_of_order_stay_in_range(gpu_lib):
     d = make(1, 90, 2, 1, 16, 40, F32, cu=[0] * 6)
     g = gpu(d)
@@ -451,3 +492,12 @@ def test_refusals(gpu_lib):
     odd["a"], odd["b"], odd["c"] = odd["a"][:, :6].contiguous(), *(odd[k][..., :6].contiguous() for k in "bc")
     with pytest.raises(gdn.GdnError):
         gdn.selective_scan_fwd(*(odd[k].cuda() for k in ("x", "dt", "a", "b", "c")))
+
+
+def test_outputs_that_are_inputs_are_refused(gpu_lib):
+    g = gpu(make(1, 10, 2, 1, 16, 24, F32))
+    ins = (g["x"], g["dt"], g["a"], g["b"], g["c"])
+    for kw in (dict(y=g["x"]), dict(y=g["dt"]), dict(y=g["z"], z=g["z"]),
+               dict(s0=g["s0"], s_final=g["s0"])):
+        with pytest.raises(ValueError):
+            gdn.selective_scan_fwd(*ins, **kw)

@@ -273,3 +273,9 @@ def test_refusals(gpu_lib):
         with pytest.raises(ValueError):
             gdn.short_conv_step(d["x"][:, 0].contiguous(), d["taps"], state)
     assert _lib.load()
+
+
+def test_outputs_that_are_inputs_are_refused(gpu_lib):
+    d = {k: t.cuda() for k, t in make(2, 10, 2, 16, 4, F32).items()}
+    with pytest.raises(ValueError):
+        gdn.short_conv_fwd(d["x"], d["taps"], y=d["x"])
