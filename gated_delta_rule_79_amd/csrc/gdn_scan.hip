@@ -492,8 +492,8 @@ __global__ __launch_bounds__(512) void scan_local_kernel(Args A, int WS) {
 // segment, and (second half of the grid) the gradients, every one replaced by
 // the gradient of the state behind its segment.  A wave chains a share of the
 // segments of 64 channels and states, the shares meet in LDS, and every wave
-// goes over its own again: 128 segments of 65536 values 9 us, 20 us walked by
-// one thread a value.
+// goes over its own again: 128 segments of 65536 values take 21 us (three passes
+// of 34 MB, 4.9 TB/s).
 constexpr int kChainWaves = 16;
 __global__ __launch_bounds__(64 * kChainWaves) void scan_chain_kernel(Args A, int64_t blocks) {
   constexpr int U = 8;
@@ -654,7 +654,7 @@ __global__ __launch_bounds__(64 * waves_of(WS)) void scan_out_kernel(Args A) {
 // segment continues another; e^{a sum} of the state in front of the segment
 // is added when it is read).  The gradient walk goes over the tiles from the
 // last one back; a tile's states at every fourth token go to LDS, four
-// tokens' decays and decayed states stay in registers.
+// tokens' decays and states stay in registers.
 
 // As scan_local_kernel, over all runs: besides the segment's state its tiles'
 // states, and what its first run makes of the gradient behind it.
@@ -761,11 +761,54 @@ __device__ inline float lane_of_other(float x) {
 }
 
 // Sums over lanes of two values at once: each half of the lanes goes on with
-// one of them.  Lanes 32 apart, 16 apart, then within a row of 16 by the lane
-// bit BIT (the partner differs in that bit, and in lower ones, which later
-// steps add up).  (The matrix cores can add lanes up too, as products with unit
+// one of them.  (The matrix cores can add lanes up too, as products with unit
 // vectors; their fp32 products take the vector unit's time: the gradient walk
 // of 16384 tokens of 4096 channels went from 1000 to 1390 us.)
+//
+// Lanes 8 and 4 apart: r = a + a of the other lane, then the same of b in the
+// banks of four lanes that have the bit, an add each, where a swap of halves
+// takes two adds' time in front of its add; so these two steps, which halve
+// the most values, come first.  Both adds are written out: a masked one keeps
+// its old lanes only so, and the other would be torn up for a product that is
+// one of its operands.  These instructions and the swaps read a register two
+// states after its write at the earliest.  (The lane 4 apart differs in its
+// lower bits too, which later steps add up.)
+template <int BIT, int N>
+__device__ inline void fold_banks(const float (&a)[N], const float (&b)[N], float (&r)[N]) {
+  static_assert((BIT == 8 || BIT == 4) && (N == 8 || N == 4), "");
+#define GDN_ADD(r, a, how, banks) "v_add_f32_dpp " r ", " a ", " a " " how " row_mask:0xf bank_mask:" banks "\n"
+#define GDN_8(how, up)                                                                         \
+  asm("s_nop 1\n" GDN_ADD("%0", "%8", how, "0xf") GDN_ADD("%1", "%9", how, "0xf")              \
+          GDN_ADD("%2", "%10", how, "0xf") GDN_ADD("%3", "%11", how, "0xf")                    \
+          GDN_ADD("%4", "%12", how, "0xf") GDN_ADD("%5", "%13", how, "0xf")                    \
+          GDN_ADD("%6", "%14", how, "0xf") GDN_ADD("%7", "%15", how, "0xf")                    \
+          GDN_ADD("%0", "%16", how, up) GDN_ADD("%1", "%17", how, up)                          \
+          GDN_ADD("%2", "%18", how, up) GDN_ADD("%3", "%19", how, up)                          \
+          GDN_ADD("%4", "%20", how, up) GDN_ADD("%5", "%21", how, up)                          \
+          GDN_ADD("%6", "%22", how, up) GDN_ADD("%7", "%23", how, up) "s_nop 1"                \
+      : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]),          \
+        "=&v"(r[6]), "=&v"(r[7])                                                               \
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(a[4]), "v"(a[5]), "v"(a[6]),           \
+        "v"(a[7]), "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "v"(b[4]), "v"(b[5]),           \
+        "v"(b[6]), "v"(b[7]))
+#define GDN_4(how, up)                                                                         \
+  asm("s_nop 1\n" GDN_ADD("%0", "%4", how, "0xf") GDN_ADD("%1", "%5", how, "0xf")              \
+          GDN_ADD("%2", "%6", how, "0xf") GDN_ADD("%3", "%7", how, "0xf")                      \
+          GDN_ADD("%0", "%8", how, up) GDN_ADD("%1", "%9", how, up)                            \
+          GDN_ADD("%2", "%10", how, up) GDN_ADD("%3", "%11", how, up) "s_nop 1"                \
+      : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])                                     \
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]))
+  if constexpr (N == 8) {
+    if constexpr (BIT == 8) GDN_8("row_ror:8", "0xc");
+    else GDN_8("row_half_mirror", "0xa");
+  } else {
+    if constexpr (BIT == 8) GDN_4("row_ror:8", "0xc");
+    else GDN_4("row_half_mirror", "0xa");
+  }
+#undef GDN_4
+#undef GDN_8
+#undef GDN_ADD
+}
 __device__ inline float fold32(float a, float b) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false,
                                                   false);
@@ -776,12 +819,12 @@ __device__ inline float fold16(float a, float b) {
                                                   false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
+// Lanes 2 and 1 apart.
 template <int BIT>
 __device__ inline float fold(float a, float b) {
-  constexpr int CTRL = BIT == 8 ? 0x128 : BIT == 4 ? 0x141 : BIT == 2 ? 0x1b : 0xb1;
   const bool up = threadIdx.x & BIT;
   const float keep = up ? b : a, send = up ? a : b;
-  return keep + lane_of_other<CTRL>(send);
+  return keep + lane_of_other<BIT == 2 ? 0x1b : 0xb1>(send);
 }
 
 // The gradient walk.
@@ -904,44 +947,42 @@ __global__ __launch_bounds__(64 * waves_of(WS), 2) void scan_grad_kernel(Args A)
             b[u].load(fromb + at, l.left - n0);
             c[u].load(fromc + at, l.left - n0);
           }
-          float h[N], e[U][N], f[U][N];  // decays, decayed states
+          float e[U][N], h[U + 1][N];  // decays, states in front of and behind the tokens
 #pragma unroll
           for (int n = 0; n < N; n += 4) {
             const floatx4 v = marks[wave][q][(n0 + n) / 4][lane];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) h[n + m] = v[m];
+            for (int m = 0; m < 4; ++m) h[0][n + m] = v[m];
           }
 #pragma unroll
           for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int n = 0; n < N; ++n) {
               e[u][n] = decay(delta[u], l.a2[n0 + n]);
-              f[u][n] = e[u][n] * h[n];
-              h[n] = fmaf(dx[u], b[u][n], f[u][n]);
+              h[u + 1][n] = fmaf(e[u][n], h[u][n], dx[u] * b[u][n]);
             }
           }
 #pragma unroll
           for (int u = 0; u < U; ++u) b[u].pack();
-          float fold5[2][N], fold4[2][N];
+          float pair[2][N], four[2][N];  // of a token, of two tokens
 #pragma unroll
           for (int u = U - 1; u >= 0; --u) {
+            float vb[N], vc[N];
 #pragma unroll
             for (int n = 0; n < N; ++n) {
               float& gn = g[n0 + n];
               gn = fmaf(c[u][n], dy[u], gn);
-              const float st = fmaf(dx[u], b[u][n], f[u][n]);
-              fold5[u & 1][n] = fold32(gn * dx[u], st * dy[u]);
-              if constexpr (GATE) ys[u] = fmaf(c[u][n], st, ys[u]);
+              vb[n] = gn * dx[u];
+              vc[n] = h[u + 1][n] * dy[u];
+              if constexpr (GATE) ys[u] = fmaf(c[u][n], h[u + 1][n], ys[u]);
               gb[u] = fmaf(b[u][n], gn, gb[u]);
-              const float w = gn * f[u][n];
+              gn *= e[u][n];
+              const float w = gn * h[u][n];
               da[n0 + n] = fmaf(delta[u], w, da[n0 + n]);
               ga[u] = fmaf(l.a2[n0 + n], w, ga[u]);
-              gn *= e[u][n];
             }
-            if ((u & 1) == 0) {
-#pragma unroll
-              for (int n = 0; n < N; ++n) fold4[u >> 1][n] = fold16(fold5[0][n], fold5[1][n]);
-            }
+            fold_banks<8>(vb, vc, pair[u & 1]);
+            if ((u & 1) == 0) fold_banks<4>(pair[0], pair[1], four[u >> 1]);
           }
           // (kept here: sums that only the outputs use are else formed there,
           // from operands kept until then)
@@ -950,29 +991,30 @@ __global__ __launch_bounds__(64 * waves_of(WS), 2) void scan_grad_kernel(Args A)
             asm volatile("" : "+v"(gb[u]), "+v"(ga[u]));
             if constexpr (GATE) asm volatile("" : "+v"(ys[u]));
           }
-          // lane bits: which of db, dc; the token of the block (low bit first); the state
+          // lane bits: 8 which of db, dc; 4 and 32 the token of the block; the
+          // others the state
           float v[N], sum;
 #pragma unroll
-          for (int n = 0; n < N; ++n) v[n] = fold<8>(fold4[0][n], fold4[1][n]);
-          int n = lane & 7;
+          for (int n = 0; n < N; ++n) v[n] = fold32(four[0][n], four[1][n]);
+#pragma unroll
+          for (int n = 0; n < N / 2; ++n) v[n] = fold16(v[n], v[n + N / 2]);
+          int n = (lane >> 4) & 1;
           bool own = real;
           if constexpr (N == 8) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) v[m] = fold<4>(v[m], v[m + 4]);
-#pragma unroll
             for (int m = 0; m < 2; ++m) v[m] = fold<2>(v[m], v[m + 2]);
             sum = fold<1>(v[0], v[1]);
+            n = n * 4 + (lane & 3);
           } else {
-#pragma unroll
-            for (int m = 0; m < 2; ++m) v[m] = fold<4>(v[m], v[m + 2]);
             sum = fold<2>(v[0], v[1]);
             sum += lane_of_other<0xb1>(sum);
-            n = (lane >> 1) & 3;
+            n = n * 2 + ((lane >> 1) & 1);
             own = own && (lane & 1) == 0;
           }
-          const int at = ((lane >> 4) & 1) + ((lane >> 3) & 1) * 2;
+          const int at = ((lane >> 2) & 1) + (lane >> 5) * 2;
           if (own && at < left)
-            A.part[(((t + at) * A.units + l.unit) * WS + wave % WS) * (2 * NS) + (lane >> 5) * NS +
+            A.part[(((t + at) * A.units + l.unit) * WS + wave % WS) * (2 * NS) +
+                   ((lane >> 3) & 1) * NS +
                    n0 + n] = sum;
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -1186,10 +1228,11 @@ Plan plan_scan(const Scan& p) {
     while (q.ws * q.ns < p.dk) q.ws *= 2;
   };
   split();
-  // Segments: eight waves a SIMD to choose from hide the loads (16384 tokens
-  // of 4096 channels: 574 us with two, 490 with four, 456), but not below
-  // half the square root of the tokens, where the chaining takes over; no cut
-  // where one walk takes less than three launches.
+  // Segments: eight waves a SIMD to choose from hide the loads (forward of
+  // 16384 packed tokens of 4096 channels: 440 us with four, 429 with six, 409),
+  // but not below half the square root of the tokens, where the chaining takes
+  // over (4096 tokens of 2048 channels: 86 us from a quarter, 75 from half, 80
+  // from the whole root); no cut where one walk takes less than three launches.
   int64_t L;
   if (p.seg_req < 0) {
     L = q.len;
