@@ -14,11 +14,16 @@
 // the answers are those of any other order but for numbers that close to one.
 //
 // The rows are what has to be read: one (or two, with a draft's) of V values
-// for the next token, one more pass for every rejected sibling.  Of a chain
-// only one node is ever tried at a place, so its end is known from gathered
-// values alone: every workgroup finds it by itself and takes a slab of the
-// row, a second launch finds the token in the slabs' sums.  A tree's passes
-// depend on each other; one workgroup walks it.
+// for the next token, one more for every place with a rejection that the walk
+// leaves.  What bounds a call is a chain of waits, not their bytes: the nodes,
+// the values of their tokens, a row, its sum, and again for every row.  One
+// workgroup walks a sequence, with its row in the CU where it fits (256 trees
+// of 16 nodes over 32000 fp32 values: 40 us, of which 65 MB at the rate of a
+// copy are 13; a chain of 8: 13 us).  Longer rows, and odd ones, are read anew
+// for every sum; of a chain of such only one node is ever tried at a place, so
+// its end is known from gathered values alone: every workgroup finds it by
+// itself and takes a slab of the row, a second launch finds the token in the
+// slabs' sums.
 
 #include <algorithm>
 
@@ -241,9 +246,9 @@ __device__ inline bool take(float u, float q, double Z, double r) {
   return static_cast<double>(u) * static_cast<double>(q) * Z < r;
 }
 
-// ------------------------------------------------------------------- trees ---
+// ---------------------------------------------- one workgroup a sequence ---
 
-// A tree's nodes in LDS: every node with the target's and the draft's value of
+// A sequence's nodes in LDS: every node with the target's and the draft's value of
 // its token in its parent's row, gathered at once.
 struct Nodes {
   int parent[kMaxNodes], token[kMaxNodes], tried[kMaxNodes];
@@ -255,7 +260,7 @@ struct Nodes {
     const int i = threadIdx.x;
     if (i <= t.size) u[i] = A.u[t.row + i];
     if (i < t.size) {
-      const int x = A.tokens[t.node + i], up = A.parent[t.node + i];
+      const int x = A.tokens[t.node + i], up = A.parent != nullptr ? A.parent[t.node + i] : i - 1;
       const int from = up >= 0 && up < i ? up : -1;
       const bool ok = x >= 0 && x < A.V;
       const int64_t row = t.row + from + 1;
@@ -341,10 +346,15 @@ __global__ __launch_bounds__(kWalkThreads) void accept_walk_kernel(Args A) {
 }
 
 // Rows that fit a CU, the target's in registers and the draft's in LDS: a row
-// is read once at most, and one whose first child is accepted not at all.
+// is read once at most, and one whose first child is accepted not at all.  With
+// drawn drafts k rejections leave max(p a - q b, 0), a the product of their 1/Z
+// and b the sum of the products behind each (what is negative once stays so),
+// as much work for the last one as for the first.  A wave has adjacent tokens,
+// so that its sum alone says whether the next token is among them; it then
+// looks for it by itself.
 template <typename IO, int W>
 __global__ __launch_bounds__(kWalkThreads) void accept_held_kernel(Args A) {
-  constexpr int C = kHeldPer / W, STEP = kWalkThreads * W, WAVES = kWalkThreads / 64;
+  constexpr int C = kHeldPer / W, WAVES = kWalkThreads / 64, SPAN = 64 * W;
   typedef typename io<IO>::storage store;
   struct Piece {  // W values as they are stored
     uint32_t bits[W * sizeof(store) / 4];
@@ -358,71 +368,64 @@ __global__ __launch_bounds__(kWalkThreads) void accept_held_kernel(Args A) {
       for (auto& b : bits) asm volatile("" : "+v"(b));
     }
   };
-  __shared__ Meet meet;
   __shared__ Nodes nodes;
-  __shared__ double chunk[C][WAVES];
+  __shared__ double part[2][WAVES];  // the waves' sums, of every second row in turn
   __shared__ Piece q[C][kWalkThreads];  // (a thread reads its own)
   const Tree t = tree_at(A, blockIdx.x);
   const bool drawn = A.q != nullptr;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   nodes.load<IO>(A, t);
   __syncthreads();
   Place at{-1, 0, 0, 0, 1.0};
+  const int count = (A.V + WAVES * SPAN - 1) / (WAVES * SPAN);  // pieces of a wave that are used
+  const int first = (wave * count * 64 + lane) * W;             // token
   Piece p[C];
-  const int first = threadIdx.x * W;
-  // (through a descriptor: what lies past the row, or all of it, is zero)
-  auto load = [&](const void* base, int values, auto&& set) {
+  double scale = 1.0, less = 0.0;  // a, b of the rejections here
+  int turn = 0;
+  // (through a descriptor: what lies past the row is zero)
+  auto load = [&](const void* base, auto&& set) {
     const auto row = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<void*>(row_at<IO>(base, t.row + at.node + 1, A.V)), 0,
-        values * io<IO>::bytes, 0x00027000);
+        const_cast<void*>(row_at<IO>(base, t.row + at.node + 1, A.V)), 0, A.V * io<IO>::bytes,
+        0x00027000);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int from = (first + c * STEP) * io<IO>::bytes;
-      set(c, __builtin_bit_cast(Piece, __builtin_amdgcn_raw_buffer_load_b128(row, from, 0, 0)));
-    }
+    for (int c = 0; c < C; ++c)
+      if (c < count)
+        set(c, __builtin_bit_cast(Piece, __builtin_amdgcn_raw_buffer_load_b128(
+                                             row, (first + c * SPAN) * io<IO>::bytes, 0, 0)));
   };
   // piece c of the row behind k rejections
   auto piece = [&](int c, int k, double (&w)[W]) {
     p[c].fresh();
 #pragma unroll
     for (int e = 0; e < W; ++e) w[e] = p[c][e] > 0.f ? p[c][e] : 0.f;  // (a NaN counts nothing)
+    if (k == 0) return;
     if (drawn) {
-      if (k == 0) return;
       const Piece by = q[c][threadIdx.x];
-      for (int j = 0; j < k; ++j) {
-        const double scale = nodes.scale[j];
 #pragma unroll
-        for (int e = 0; e < W; ++e)
-          w[e] = fmax(fma(w[e], scale, -static_cast<double>(by[e])), 0.0);
-      }
+      for (int e = 0; e < W; ++e)
+        w[e] = fmax(fma(w[e], scale, -(static_cast<double>(by[e]) * less)), 0.0);
     } else {
       for (int j = 0; j < k; ++j) {
-        const double scale = nodes.scale[j];
-        const int x = nodes.tried[j] - (first + c * STEP);
+        const double s = nodes.scale[j];
+        const int x = nodes.tried[j] - (first + c * SPAN);
 #pragma unroll
-        for (int e = 0; e < W; ++e) w[e] = fmax(fma(w[e], scale, e == x ? -1.0 : 0.0), 0.0);
+        for (int e = 0; e < W; ++e) w[e] = fmax(fma(w[e], s, e == x ? -1.0 : 0.0), 0.0);
       }
     }
   };
-  // sums of the pieces of all threads (a piece: STEP tokens) into chunk
-  auto sums = [&](int k) {
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      double w[W], s = 0.0;
-      piece(c, k, w);
-#pragma unroll
-      for (int e = 0; e < W; ++e) s += w[e];
-#pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
-      if (lane == 0) chunk[c][wave] = s;
-    }
-    __syncthreads();
-  };
+  // the row's sum behind k rejections, the waves' in part[turn]
   auto total = [&](int k) {
+    if (k > 0) {
+      scale = 1.0, less = 0.0;
+      for (int j = 0; j < k; ++j) {
+        scale *= nodes.scale[j];
+        less = fma(less, nodes.scale[j], 1.0);
+      }
+    }
     double s = 0.0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
+      if (c >= count) break;
       double w[W];
       piece(c, k, w);
 #pragma unroll
@@ -430,14 +433,15 @@ __global__ __launch_bounds__(kWalkThreads) void accept_held_kernel(Args A) {
     }
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+    turn ^= 1;
+    if (lane == 0) part[turn][wave] = s;
     __syncthreads();
-    if (lane == 0) meet.part[wave] = s;
-    __syncthreads();
-    double left = 0.0;
+    double all = 0.0;
 #pragma unroll
-    for (int o = 0; o < WAVES; ++o) left += meet.part[o];
-    return left;
+    for (int o = 0; o < WAVES; ++o) all += part[turn][o];
+    return all;
   };
+  double sum;
   bool moved;
   do {
     bool child = at.child(nodes, t);
@@ -445,11 +449,17 @@ __global__ __launch_bounds__(kWalkThreads) void accept_held_kernel(Args A) {
       at.move();
       child = at.child(nodes, t);
     }
-    load(A.p, A.V, [&](int c, Piece v) { p[c] = v; });
-    if (child && drawn) load(A.q, A.V, [&](int c, Piece v) { q[c][threadIdx.x] = v; });
+    load(A.p, [&](int c, Piece v) { p[c] = v; });
+    if (child && drawn) load(A.q, [&](int c, Piece v) { q[c][threadIdx.x] = v; });
+    sum = 0.0;
     moved = false;
     while (child && !moved) {
-      at.reject(nodes, total);
+      __syncthreads();  // (all have read what is written now)
+      if (threadIdx.x == 0) nodes.scale[at.m] = 1.0 / at.Z, nodes.tried[at.m] = nodes.token[at.i];
+      __syncthreads();
+      sum = total(at.m + 1);
+      if (sum > 0.0) at.Z = sum, ++at.m;  // else nothing would be left: the row stays
+      ++at.i;
       child = at.child(nodes, t);
       if (child && at.accepts(nodes, drawn)) {
         at.move();
@@ -457,29 +467,83 @@ __global__ __launch_bounds__(kWalkThreads) void accept_held_kernel(Args A) {
       }
     }
   } while (moved);
-  sums(at.m);
-  double mine = 0.0, sum = 0.0;
-  for (int c = 0; c < C; ++c) {
-    double v = 0.0;
-    for (int o = 0; o < WAVES; ++o) v += chunk[c][o];
-    if (c == static_cast<int>(threadIdx.x)) mine = v;
-    sum += v;
-  }
-  double target = static_cast<double>(nodes.u[t.size]) * sum;
-  const int which = pick(mine, &target, &meet);
-  double own[W];
+  if (!(sum > 0.0)) sum = total(at.m);  // none tried here, or the last one left nothing
+  // the wave that has the token: the first at which the running sum exceeds the
+  // target, or the last with a part of the row
+  const double target = static_cast<double>(nodes.u[t.size]) * sum;
+  int owner = 0;
+  double front = 0.0, run = 0.0;
+  bool found = false;
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-    if (c == which) piece(c, at.m, own);  // (uniform)
-  const int next = find(own, first + which * STEP, target, A.V - 1, &meet);
-  if (threadIdx.x == 0) {
+  for (int o = 0; o < WAVES; ++o) {
+    const double v = part[turn][o];
+    if (v > 0.0 && !found) {
+      owner = o;
+      front = run;
+      found = run + v > target;
+    }
+    run += v;
+  }
+  if (wave != owner) return;
+  double own[C], upto[C];  // a lane's part of a piece, and with the lanes in front
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    own[c] = 0.0;
+    if (c < count) {
+      double w[W];
+      piece(c, at.m, w);
+#pragma unroll
+      for (int e = 0; e < W; ++e) own[c] += w[e];
+    }
+    upto[c] = own[c];
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const double o = __shfl_up(upto[c], m, 64);
+      if (lane >= m) upto[c] += o;
+    }
+  }
+  int holder = 0, which = -1;
+  double before = 0.0;
+  found = false;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const unsigned long long some = __ballot(own[c] > 0.0);
+    const unsigned long long over = __ballot(own[c] > 0.0 && front + upto[c] > target);
+    if (some != 0 && !found) {
+      found = over != 0;
+      holder = found ? __ffsll(over) - 1 : 63 - __clzll(some);
+      which = c;
+      before = front + (upto[c] - own[c]);
+    }
+    front += __shfl(upto[c], 63, 64);
+  }
+  int token = A.V - 1;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (c != which) continue;  // (uniform)
+    double w[W];
+    piece(c, at.m, w);
+    bool here = false;
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      before += w[e];
+      if (w[e] > 0.0 && !here) {
+        token = first + c * SPAN + e;
+        here = before > target;
+      }
+    }
+  }
+  if (lane == holder) {
     A.accepted[blockIdx.x] = at.node;
     A.length[blockIdx.x] = at.length;
-    A.next[blockIdx.x] = next;
+    A.next[blockIdx.x] = token;
   }
 }
 
-// ------------------------------------------------------------------ chains ---
+// -------------------------------------------------- chains of longer rows ---
 
 // Length of a chain's accepted part: every lane tries a node against the
 // target's row in front of it, the first that fails ends it.  Also whether
@@ -570,6 +634,14 @@ __global__ __launch_bounds__(kSlabThreads) void accept_chain_kernel(Args A) {
   }
 }
 
+// Rows that stay in a CU (where they are whole 16-byte pieces too).
+bool held(int64_t V) { return V <= kWalkThreads * kHeldPer; }
+
+int values_of_piece(const Accept& p) {
+  const int W = p.io == GDN_BF16 ? 8 : 4;
+  return p.V % W == 0 ? W : 1;
+}
+
 // Slabs of a chain's row: 1024 values, which the second launch's workgroup
 // holds at once, more where there are more than 2048 workgroups or 256 slabs.
 void plan_slabs(const Accept& p, int* slabs, int* slab) {
@@ -583,14 +655,16 @@ void plan_slabs(const Accept& p, int* slabs, int* slab) {
 
 template <typename IO, int W>
 hipError_t accept(const Args& A, hipStream_t s) {
-  if (A.parent != nullptr) {
-    const dim3 grid(A.trees), threads(kWalkThreads);
-    if constexpr (W > 1) {
-      if (A.V <= kWalkThreads * kHeldPer) {
-        hipLaunchKernelGGL((accept_held_kernel<IO, W>), grid, threads, 0, s, A);
-        return hipGetLastError();
-      }
+  // (Chains of rows that fit: 1 of 32000 fp32 values 15.5 us in slabs, 13.0
+  // held; 256 of them 38 and 20; 2048 of 4096 values 52 and 57.)
+  const dim3 grid(A.trees), threads(kWalkThreads);
+  if constexpr (W > 1) {
+    if (held(A.V)) {
+      hipLaunchKernelGGL((accept_held_kernel<IO, W>), grid, threads, 0, s, A);
+      return hipGetLastError();
     }
+  }
+  if (A.parent != nullptr) {
     hipLaunchKernelGGL((accept_walk_kernel<IO, W>), grid, threads, 0, s, A);
     return hipGetLastError();
   }
@@ -605,7 +679,7 @@ hipError_t accept(const Args& A, hipStream_t s) {
 }  // namespace
 
 size_t accept_workspace_bytes(const Accept& p) {
-  if (p.tree) return 0;
+  if (p.tree || (values_of_piece(p) > 1 && held(p.V))) return 0;
   int slabs, slab;
   plan_slabs(p, &slabs, &slab);
   return static_cast<size_t>(p.trees) * (slabs * sizeof(double) + sizeof(int2));
@@ -634,9 +708,9 @@ hipError_t launch_accept(const Accept& p, const int32_t* parent, const int32_t* 
   A.head = reinterpret_cast<int2*>(A.part + static_cast<int64_t>(A.trees) * A.slabs);
   StageScope scope(GDN_STAGE_OTHER, s);
   // whole rows of 16-byte pieces, else one value at a time
-  if (p.io == GDN_BF16)
-    return p.V % 8 == 0 ? accept<bf16_t, 8>(A, s) : accept<bf16_t, 1>(A, s);
-  return p.V % 4 == 0 ? accept<f32_t, 4>(A, s) : accept<f32_t, 1>(A, s);
+  const bool whole = values_of_piece(p) > 1;
+  if (p.io == GDN_BF16) return whole ? accept<bf16_t, 8>(A, s) : accept<bf16_t, 1>(A, s);
+  return whole ? accept<f32_t, 4>(A, s) : accept<f32_t, 1>(A, s);
 }
 
 }  // namespace gdn

@@ -198,8 +198,9 @@ def test_accept_refusals(lib):
     for n in ACCEPT:
         assert accept(lib, p, **{n: A + 8}) == ALIGN, n
         assert accept(lib, p, **{n: None}) == (HIP if n in ("parent", "draft") else NULL), n
-    assert accept(lib, p, parent=None, ws=None) == WORKSPACE
-    assert accept(lib, p, parent=None, short=1) == WORKSPACE
+    assert accept(lib, p, vocab=1001, parent=None, ws=None) == WORKSPACE
+    assert accept(lib, p, vocab=1 << 16, parent=None, short=1) == WORKSPACE
+    assert accept(lib, p, parent=None, ws=None) == HIP  # nor do chains of rows that fit a CU
     assert accept(lib, p, parent=None, ws=A + 8) == ALIGN
     assert accept(lib, p, ws=None) == HIP  # a tree takes none
     assert lib.gdn_draft_accept_workspace(None, 5, 0, ctypes.byref(ctypes.c_size_t(0))) == NULL

@@ -90,6 +90,24 @@ def test_dense_batches(gpu_lib, B, n, V, tree):
         check(make([n] * B, V, dtype, tree, seed=B), [n] * B, packed=False)
 
 
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [4, 8, 4096, 4104, 8191, 32760, 32768, 32776, 40000])
+def test_row_lengths(gpu_lib, V, dtype, tree):
+    # rows that end inside, at and behind what a workgroup holds
+    sizes = [3, 0, 9]
+    for drawn in (False, True):
+        check(make(sizes, V, dtype, tree, drawn, seed=V, far=3.0), sizes)
+
+
+@pytest.mark.parametrize("drawn", [False, True])
+def test_a_star_over_long_rows(gpu_lib, drawn):
+    for V in (32768, 50000):
+        d = make([64], V, F32, True, drawn, far=5.0, seed=4)
+        d["parent"][:] = -1
+        check(d, [64])
+
+
 @pytest.mark.parametrize("far,seed", [(0.0, 1), (0.05, 2), (2.0, 3), (6.0, 4)])
 def test_near_and_far_drafts(gpu_lib, far, seed):
     # drafts of the target's own rows are all accepted; of far ones few are
