@@ -9,9 +9,13 @@ The three entry points mirror ``include/gdn.h``:
   decode_step(q, k, v, beta, log_alpha, state) -> o   (state updated in place)
 
 Beside them: linear attention with a constant decay per head
-(linear_attn_fwd, linear_attn_bwd, linear_attn_decode_step) and the group
+(linear_attn_fwd, linear_attn_bwd, linear_attn_decode_step), the group
 norm of a block's output with an activation or gate (group_norm_fwd,
-group_norm_bwd).
+group_norm_bwd), the selective state space scan (selective_scan_fwd,
+selective_scan_bwd, selective_scan_step), the short convolution in front of
+it with a carried history (short_conv_fwd, short_conv_bwd, short_conv_step)
+and the acceptance of drafted tokens between tree_verify and tree_commit
+(draft_accept).
 
 Tensors are torch CUDA tensors (HIP device memory); torch is used only to
 allocate outputs / workspaces and to name the current stream.  The gate mode
@@ -35,6 +39,8 @@ __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "chunk_fwd_conv", "gdn2_chunk_fwd",
            "chunk_fwd_product", "tree_verify",
            "tree_commit", "linear_attn_fwd", "linear_attn_bwd",
            "linear_attn_decode_step", "group_norm_fwd", "group_norm_bwd",
+           "selective_scan_fwd", "selective_scan_bwd", "selective_scan_step",
+           "short_conv_fwd", "short_conv_bwd", "short_conv_step", "draft_accept",
            "FwdPlan", "GdnError",
            "abi_version", "stage_times"]
 
