@@ -705,7 +705,8 @@ hipError_t launch_accept(const Accept& p, const int32_t* parent, const int32_t* 
   A.next = next;
   plan_slabs(p, &A.slabs, &A.slab);
   A.part = static_cast<double*>(ws);
-  A.head = reinterpret_cast<int2*>(A.part + static_cast<int64_t>(A.trees) * A.slabs);
+  if (ws != nullptr)
+    A.head = reinterpret_cast<int2*>(A.part + static_cast<int64_t>(A.trees) * A.slabs);
   StageScope scope(GDN_STAGE_OTHER, s);
   // whole rows of 16-byte pieces, else one value at a time
   const bool whole = values_of_piece(p) > 1;

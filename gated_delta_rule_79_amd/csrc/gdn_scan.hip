@@ -1262,8 +1262,8 @@ Plan plan_scan(const Scan& p) {
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-struct Carve {  // pieces of a workspace, or their total when base is null
-  char* base;
+struct Carve {  // pieces of a workspace, or their total when base is 0
+  uintptr_t base;
   size_t used;
   template <typename T>
   T* take(int64_t n) {
@@ -1276,7 +1276,7 @@ struct Carve {  // pieces of a workspace, or their total when base is null
 size_t carve_fwd(const Scan& p, const Plan& q, char* ws, Args* A) {
   if (q.S == 1) return 0;
   const int64_t D = static_cast<int64_t>(p.H) * p.dv;
-  Carve c{ws, 0};
+  Carve c{reinterpret_cast<uintptr_t>(ws), 0};
   A->cut = c.take<int>(q.segs);
   A->h = c.take<float>(q.segs * D * p.dk);
   A->sum = c.take<float>(q.segs * D);
@@ -1286,7 +1286,7 @@ size_t carve_fwd(const Scan& p, const Plan& q, char* ws, Args* A) {
 size_t carve_bwd(const Scan& p, const Plan& q, char* ws, Args* A) {
   const int64_t D = static_cast<int64_t>(p.H) * p.dv, size = D * p.dk;
   const int64_t tokens = static_cast<int64_t>(p.B) * p.T;
-  Carve c{ws, 0};
+  Carve c{reinterpret_cast<uintptr_t>(ws), 0};
   if (q.S > 1) {
     A->cut = c.take<int>(q.segs);
     A->cutr = c.take<int>(q.segs);

@@ -276,3 +276,25 @@ def test_refusals(gpu_lib):
     with pytest.raises(gdn.GdnError):
         gdn.draft_accept(big, torch.zeros(1, 66, 8, device="cuda"), None,
                          torch.zeros(1, 66, device="cuda"))
+
+
+def test_captured_chains_of_long_rows(gpu_lib):
+    # two launches and a workspace inside the graph
+    sizes, V = [5, 0, 7], 40000
+    sets = [make(sizes, V, F32, False, seed=s) for s in range(3)]
+    g = {k: t.cuda() for k, t in sets[0].items() if t is not None}
+    cu = torch.tensor([0, 5, 5, 12], dtype=torch.int32, device="cuda")
+    work = lambda: gdn.draft_accept(g["tokens"], g["target"], g["draft"], g["uniform"],  # noqa: E731
+                                    None, cu)
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for d in sets + sets[:1]:
+        for k in g:
+            g[k].copy_(d[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(np.stack([t.cpu().numpy() for t in out]), reference(d, sizes))
+        work()
