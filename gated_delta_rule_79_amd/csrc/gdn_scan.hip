@@ -1065,9 +1065,10 @@ __global__ __launch_bounds__(64 * waves_of(WS), 2) void scan_grad_kernel(Args A)
 }
 
 // The shares of the gradient walk added in a fixed order, one launch for all:
-// db, dc (the channel blocks' of every token, group and state; a thread each),
-// then da, dd, dt_bias (rows of shares; sixteen columns a workgroup, its
-// sixteen runs of rows added up in LDS).
+// db, dc (the channel blocks' of every token, group and state; a thread each;
+// rows in front of the first sequence and behind the last one, of which there
+// are no shares, stay as they are), then da, dd, dt_bias (rows of shares;
+// sixteen columns a workgroup, its sixteen runs of rows added up in LDS).
 struct Finish {
   int64_t tokens;
   int NS, WS;
@@ -1084,6 +1085,7 @@ __global__ __launch_bounds__(256) void scan_finish_kernel(Args A, Finish F) {
     const int per = 2 * A.dk;
     const int64_t row = e / per;  // token and group
     if (row >= F.tokens * A.hb) return;
+    if (A.cu != nullptr && (row < bound(A, 0) * A.hb || row >= bound(A, A.nseq) * A.hb)) return;
     const int k = static_cast<int>(e - row * per), n = k % A.dk, two = k / A.dk;
     const int unit = F.WS * 2 * F.NS;
     const float* p = A.part + row * A.nb * unit + n / F.NS * (2 * F.NS) + two * F.NS + n % F.NS;

@@ -525,8 +525,8 @@ gdn_status gdn_group_norm_bwd(const gdn_problem* p, int32_t d, int32_t act, int3
  *   No output may overlap an input, s_final s0 neither.
  *   ws        : at least gdn_selective_scan_fwd_workspace bytes; calls that
  *               overlap in time (streams, captured graphs) need one each.
- * All arithmetic is fp32, the state too.  Rows of packed tensors behind
- * cu_seqlens[nseq] are neither read nor written.  A NaN or infinity in a
+ * All arithmetic is fp32, the state too.  Rows of packed tensors in front of
+ * cu_seqlens[0] and behind cu_seqlens[nseq] are neither read nor written.  A NaN or infinity in a
  * token stays in its sequence.  Deterministic.  Errors as gdn_chunk_fwd;
  * GDN_ERR_SHAPE where a launch would take 2^32 threads. */
 gdn_status gdn_selective_scan_fwd_workspace(const gdn_problem* p, int32_t hb, size_t* bytes);
@@ -541,7 +541,9 @@ gdn_status gdn_selective_scan_fwd(const gdn_problem* p, int32_t hb, int32_t soft
  *   dx, ddt, dz [B, T, H, dv] and db, dc [B, T, hb, dk] in io_dtype (dz only
  *   with z); da [H, dk, dv], dd, ddt_bias [H, dv] and ds0 [nseq, H, dk, dv]
  *   fp32; dd, ddt_bias and ds0 may be NULL to skip them, ds_final NULL = zeros.
- * Sums over tokens and channels run in a fixed order (deterministic). */
+ * Rows of dx, ddt, db, dc and dz in front of cu_seqlens[0] and behind
+ * cu_seqlens[nseq] stay as they are.  Sums over tokens and channels run in a
+ * fixed order (deterministic). */
 gdn_status gdn_selective_scan_bwd_workspace(const gdn_problem* p, int32_t hb, size_t* bytes);
 gdn_status gdn_selective_scan_bwd(const gdn_problem* p, int32_t hb, int32_t softplus,
                                   const void* x, const void* dt, const float* a, const void* b,

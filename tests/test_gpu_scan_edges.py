@@ -1,0 +1,52 @@
+"""The selective scan where its contract has edges: rows outside every
+sequence, gates and steps at the ends of their range, rates of -inf."""
+
+import ctypes
+
+import pytest
+import torch
+
+import gated_delta_rule_79_amd as gdn
+from gated_delta_rule_79_amd import _lib
+from test_gpu_scan import BF16, F32, Reference, dev_cu, gpu, make, run_fwd
+
+pytestmark = pytest.mark.gpu
+
+ROWS = ("x", "dt", "b", "c", "z", "dy")
+
+
+def bwd_into(g, cu, seg, fill):
+    """The backward's C entry point on outputs that hold `fill` and a workspace
+    of NaN."""
+    lib = _lib.load()
+    p, hb, _ = gdn._scan_problem(g["x"], g["dt"], g["a"], g["b"], g["c"], g["d"], g["dt_bias"],
+                                 g["z"], cu, seg, 2)
+    need = gdn._bytes(lib.gdn_selective_scan_bwd_workspace, p, hb)
+    ws = torch.full((need // 4,), float("nan"), device="cuda")
+    ins = [g[k] for k in ("x", "dt", "a", "b", "c", "d", "dt_bias", "z", "s0")]
+    out = [torch.full_like(t, fill) for t in ins]
+    gdn._launch(lib.gdn_selective_scan_bwd, g["x"].device, ctypes.byref(p), hb, 1,
+                *(gdn._ptr(t) for t in (*ins, g["dy"], g["ds"], *out, ws)), need)
+    torch.cuda.synchronize()
+    return out
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cu", [[0, 20, 37], [5, 20, 20, 41], [16, 16, 16]])
+def test_rows_outside_the_sequences_are_left_alone(gpu_lib, cu, dtype):
+    # in front of the first and behind the last; nothing of the workspace that
+    # no walk has written reaches them
+    d = make(1, 60, 2, 2, 16, 40, dtype, cu=cu)
+    lo, hi = cu[0], cu[-1]
+    for k in ROWS:
+        d[k][:, :lo], d[k][:, hi:] = float("nan"), float("nan")
+    inside = {k: t[:, lo:hi].contiguous() if k in ROWS else t for k, t in d.items()}
+    ref, g = Reference(inside, [n - lo for n in cu]), gpu(d)
+    rows = dict(zip((0, 1, 3, 4, 7), ("dx", "ddt", "db", "dc", "dz")))
+    for seg in (0, 1, -1):
+        y, sf = run_fwd(g, cu, seg_chunks=seg, y=torch.full_like(g["x"], 7.0))
+        grads = bwd_into(g, dev_cu(cu), seg, 7.0)
+        for name, t in (("y", y), *((rows[i], grads[i]) for i in rows)):
+            assert bool((t[:, :lo] == 7.0).all()) and bool((t[:, hi:] == 7.0).all()), (name, seg)
+        ref.check_fwd(dtype, y[:, lo:hi], sf)
+        ref.check_bwd(dtype, [t[:, lo:hi] if i in rows else t for i, t in enumerate(grads)])
