@@ -27,6 +27,7 @@
 
 #include <algorithm>
 
+#include "gdn_accept_row.hpp"
 #include "gdn_device.hpp"
 #include "gdn_internal.hpp"
 
@@ -73,26 +74,8 @@ __device__ inline Tree tree_at(const Args& A, int m) {
   return t;
 }
 
-// The row that is drawn from: the target's, less what was tried there.
 template <typename IO>
-struct Row {
-  const void *p, *q;      // the target's and the draft's row
-  int m;                  // rejected children
-  const double* scale;    // 1 / Z in front of each rejection
-  const int* tried;       // their tokens (certain drafts)
-
-  __device__ inline double less(float pv, float qv, int x) const {
-    double w = pv > 0.f ? pv : 0.f;  // (a NaN counts nothing)
-    for (int j = 0; j < m; ++j) {
-      const double by = q != nullptr ? static_cast<double>(qv) : x == tried[j] ? 1.0 : 0.0;
-      w = fmax(fma(w, scale[j], -by), 0.0);
-    }
-    return w;
-  }
-  __device__ inline double at(int x) const {
-    return less(io<IO>::load(p, x), q != nullptr ? io<IO>::load(q, x) : 0.f, x);
-  }
-};
+using Row = AcceptRow<io<IO>>;
 
 // A wave's sum of the row over [lo, hi); W: values of a load (lo a multiple).
 template <typename IO, int W>
@@ -100,7 +83,7 @@ __device__ inline double wave_sum(const Row<IO>& r, int lo, int hi) {
   constexpr int U = 4;
   const int lane = threadIdx.x & 63;
   double s[U] = {0.0, 0.0, 0.0, 0.0};
-  const bool two = r.q != nullptr && r.m > 0;
+  const bool two = r.two();
   for (int i = lo + lane * W; i < hi; i += 64 * W * U) {
     float p[U][W], q[U][W];
 #pragma unroll

@@ -4,12 +4,15 @@ Both sides sum in 64 bits in orders of their own, so a decision could differ
 only where a uniform number lies within 2^-40 of a border: seeds are fixed and
 none does."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import gated_delta_rule_79_amd as gdn
 import oracle
+from gated_delta_rule_79_amd import _lib
 from gpu_util import Padded, log
 
 pytestmark = pytest.mark.gpu
@@ -298,3 +301,33 @@ def test_captured_chains_of_long_rows(gpu_lib):
         torch.cuda.synchronize()
         assert np.array_equal(np.stack([t.cpu().numpy() for t in out]), reference(d, sizes))
         work()
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [512, 5001, 40000])
+def test_a_draft_without_its_last_row(gpu_lib, V, dtype, tree):
+    # a draft model leaves no row behind its last token: nothing is read there
+    # (tests/test_accept_row.py counts the loads), and the answers are the same
+    sizes = [3, 7]
+    for u in (0.0, None):  # all accepted, so that the walk ends behind the last node, or some
+        d = make(sizes, V, dtype, tree, far=0.3, seed=V)
+        if tree:
+            d["parent"] = torch.tensor([-1, 0, 1, -1, 0, 1, 2, 3, 4, 5], dtype=torch.int32)
+        if u is not None:
+            d["uniform"][:3], d["uniform"][4:11] = u, u
+        g = {k: None if t is None else t.cuda() for k, t in d.items()}
+        draft = g["draft"][:-1].clone()
+        cu = torch.tensor([0, 3, 10], dtype=torch.int32, device="cuda")
+        p = _lib.GdnProblem(1, 10, 1, 16, 16, 0, 2, cu.data_ptr(), gdn._dtype_code(draft))
+        need = gdn._bytes(gpu_lib.gdn_draft_accept_workspace, p, V, int(tree))
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        out = [torch.empty(2, dtype=torch.int32, device="cuda") for _ in range(3)]
+        gdn._launch(gpu_lib.gdn_draft_accept, draft.device, ctypes.byref(p), V,
+                    gdn._ptr(g["parent"]), gdn._ptr(g["tokens"]), gdn._ptr(g["target"]),
+                    draft.data_ptr(), gdn._ptr(g["uniform"]), *(t.data_ptr() for t in out),
+                    ws.data_ptr(), need)
+        torch.cuda.synchronize()
+        want = reference(d, sizes)
+        assert u is None or (want[1] == sizes).all()
+        assert np.array_equal(np.stack([t.cpu().numpy() for t in out]), want)
