@@ -712,7 +712,8 @@ __global__ __launch_bounds__(512) void scan_marks_kernel(Args A, int WS) {
         }
         const Row<IO, NS, PAD>& c = cs[u];
         const float dx = delta * x[u];
-        const float v = GATE ? dys[u] * zs[u] * sigmoid<IO>(zs[u]) : dys[u];
+        // (the gate first: of the type's lowest value it is zero, dy z infinite)
+        const float v = GATE ? dys[u] * (zs[u] * sigmoid<IO>(zs[u])) : dys[u];
         sum += delta;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {

@@ -8,7 +8,7 @@ import torch
 
 import gated_delta_rule_79_amd as gdn
 from gated_delta_rule_79_amd import _lib
-from test_gpu_scan import BF16, F32, Reference, dev_cu, gpu, make, run_fwd
+from test_gpu_scan import BF16, F32, Reference, dev_cu, gpu, make, run_bwd, run_fwd
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,26 @@ def test_rows_outside_the_sequences_are_left_alone(gpu_lib, cu, dtype):
             assert bool((t[:, :lo] == 7.0).all()) and bool((t[:, hi:] == 7.0).all()), (name, seg)
         ref.check_fwd(dtype, y[:, lo:hi], sf)
         ref.check_bwd(dtype, [t[:, lo:hi] if i in rows else t for i, t in enumerate(grads)])
+
+
+@pytest.mark.parametrize("dtype", [BF16])
+def test_gates_of_the_lowest_value(gpu_lib, dtype):
+    # silu and its slope are zero there (z times the zero of its sigmoid), and
+    # so is all that such a token gives on: as behind a gate of -1000
+    d = make(2, 37, 2, 1, 16, 40, dtype)
+    off = torch.rand(2, 37, 2, 40, generator=torch.Generator().manual_seed(5)) < 0.3
+    runs = []
+    for low in (torch.finfo(dtype).min, -1000.0):
+        d["z"] = torch.where(off, low, d["z"].float()).to(dtype)
+        g = gpu(d)
+        for seg in (1, -1):
+            y, sf = run_fwd(g, None, seg_chunks=seg)
+            grads = run_bwd(g, None, seg_chunks=seg)
+            assert not y.cpu()[off].any() and not grads[7].cpu()[off].any()
+            runs.append([y, sf, *grads])
+        one = {k: g[k][:, 0].contiguous() for k in ("x", "dt", "b", "c", "z")}
+        y = gdn.selective_scan_step(one["x"], one["dt"], g["a"], one["b"], one["c"],
+                                    g["s0"].clone(), g["d"], g["dt_bias"], one["z"])
+        assert not y.cpu()[off[:, 0]].any()
+    for a, b in zip(runs[:2], runs[2:]):
+        assert all(torch.equal(s, t) and bool(s.isfinite().all()) for s, t in zip(a, b))
