@@ -39,7 +39,7 @@ namespace {
 
 // Waves of a workgroup whose channel blocks take ws waves each.
 constexpr int waves_of(int ws) { return ws > 4 ? ws : 4; }
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596303e-8f;  // and the rest
 constexpr float kLn2 = 0.69314718055994530942f;
 
 #define GDN_CONST __attribute__((address_space(4)))
@@ -47,20 +47,21 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // ------------------------------------------------------------- functions ---
 
 // e^x for |x| <= 87, the ends beyond (a NaN gives one of them: its users keep
-// the NaN by themselves); what the product x log2(e) loses goes back in.  No
-// branches in these: they stand between the loads of every token.
+// the NaN by themselves).  What the product x log2(e) loses goes back in, by
+// its own rounding and by the constant's (without the latter e^-82 is off by
+// 19 u).  No branches in these: they stand between the loads of every token.
 __device__ inline float exp_full(float x) {
   x = __builtin_amdgcn_fmed3f(x, -87.f, 87.f);
-  const float t = x * kLog2e;
+  const float t = x * kLog2e, lost = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -t));
   const float e = __builtin_amdgcn_exp2f(t);
-  return fmaf(e * kLn2, fmaf(x, kLog2e, -t), e);
+  return fmaf(e * kLn2, lost, e);
 }
 
 // softplus(v) = max(v, 0) + log(1 + u), u = e^{-|v|}: w = 1 + u is off by
 // d = u - (w - 1), log(w + d) = log(w) + d to 2^-25 of the result.
 __device__ inline float softplus(float v) {
   const float u = exp_full(-fabsf(v)), w = 1.f + u;
-  return (v < 0.f ? 0.f : v) + fmaf(kLn2, __builtin_amdgcn_logf(w), u - (w - 1.f));
+  return __builtin_elementwise_maximum(v, 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), u - (w - 1.f));
 }
 
 // bf16 rows take the exponential as it is (its error, |v| 2^-24, is far below

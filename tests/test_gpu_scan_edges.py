@@ -3,12 +3,14 @@ sequence, gates and steps at the ends of their range, rates of -inf."""
 
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
 import gated_delta_rule_79_amd as gdn
 from gated_delta_rule_79_amd import _lib
-from test_gpu_scan import BF16, F32, Reference, dev_cu, gpu, make, run_bwd, run_fwd
+from gpu_util import log, np64
+from test_gpu_scan import BF16, F32, U, Reference, dev_cu, gpu, make, run_bwd, run_fwd
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +75,32 @@ def test_gates_of_the_lowest_value(gpu_lib, dtype):
         assert not y.cpu()[off[:, 0]].any()
     for a, b in zip(runs[:2], runs[2:]):
         assert all(torch.equal(s, t) and bool(s.isfinite().all()) for s, t in zip(a, b))
+
+
+def test_steps_over_their_whole_range(gpu_lib):
+    # one token, one state that c reads with a one: y is delta itself, off by
+    # at most 12 u of itself as the bounds of the other tests take it
+    v = torch.cat([torch.linspace(-82.9, -20.0, 3001), torch.linspace(-20.0, 20.0, 8001),
+                   torch.linspace(20.0, 90.0, 501)])
+    n = v.numel()
+    b = torch.tensor([1.0, 0.0, 0.0, 0.0]).view(1, 1, 1, 4).cuda()
+    y, _ = gdn.selective_scan_fwd(torch.ones(1, 1, 1, n, device="cuda"), v.view(1, 1, 1, n).cuda(),
+                                  torch.full((1, 4, n), -1.0, device="cuda"), b, b)
+    want = np.logaddexp(v.double().numpy(), 0.0)
+    err = np.abs(np64(y).reshape(-1) - want) / want / U
+    at = int(err.argmax())
+    log(f"    worst error {err[at]:.2f} u at {float(v[at]):.3f}")
+    assert err.max() <= 12.0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_step_that_is_nan_is_seen(gpu_lib, dtype):
+    # from its token on, in its channel; nothing in front of it
+    d = make(1, 40, 1, 1, 8, 24, dtype)
+    d["dt"][0, 13, 0, 7] = float("nan")
+    g = gpu(d)
+    for seg in (1, -1):
+        y, sf = run_fwd(g, None, seg_chunks=seg)
+        bad = y.isnan().cpu()[0, :, 0]
+        assert bool(bad[13:, 7].all()) and not bad[:13].any() and not bad[:, :7].any()
+        assert bool(sf.isnan()[0, 0, :, 7].all()) and int(sf.isnan().sum()) == 8
