@@ -46,29 +46,30 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 // ------------------------------------------------------------- functions ---
 
-// e^x for |x| <= 87, the ends beyond (a NaN gives one of them: its users keep
-// the NaN by themselves).  What the product x log2(e) loses goes back in, by
-// its own rounding and by the constant's (without the latter e^-82 is off by
-// 19 u).  No branches in these: they stand between the loads of every token.
+// e^x for |x| <= 200, 0 or infinity where that passes them.  What the product
+// x log2(e) loses goes back in, by its own rounding and by the constant's
+// (without the latter e^-82 is off by 19 u).  No branches in these: they stand
+// between the loads of every token.
 __device__ inline float exp_full(float x) {
-  x = __builtin_amdgcn_fmed3f(x, -87.f, 87.f);
   const float t = x * kLog2e, lost = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  return fmaf(e * kLn2, lost, e);
+  return __builtin_amdgcn_exp2f(t) * fmaf(lost, kLn2, 1.f);
 }
 
 // softplus(v) = max(v, 0) + log(1 + u), u = e^{-|v|}: w = 1 + u is off by
-// d = u - (w - 1), log(w + d) = log(w) + d to 2^-25 of the result.
+// d = u - (w - 1), log(w + d) = log(w) + d to 2^-25 of the result.  (Its least
+// value is e^-87; of a NaN the maximum stays.)
 __device__ inline float softplus(float v) {
-  const float u = exp_full(-fabsf(v)), w = 1.f + u;
+  const float u = exp_full(fmaxf(-fabsf(v), -87.f)), w = 1.f + u;
   return __builtin_elementwise_maximum(v, 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), u - (w - 1.f));
 }
 
 // bf16 rows take the exponential as it is (its error, |v| 2^-24, is far below
-// their rounding).
+// their rounding).  Zero from about -89 down, so that v times it is none of
+// the type's lowest value; of a NaN it is anything, its users keep the NaN.
 template <typename IO>
 __device__ inline float sigmoid(float v) {
-  const float e = io<IO>::bytes == 2 ? __builtin_amdgcn_exp2f(-v * kLog2e) : exp_full(-v);
+  const float e = io<IO>::bytes == 2 ? __builtin_amdgcn_exp2f(-v * kLog2e)
+                                     : exp_full(__builtin_amdgcn_fmed3f(-v, -200.f, 200.f));
   return __builtin_amdgcn_rcpf(1.f + e);
 }
 

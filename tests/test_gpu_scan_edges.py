@@ -54,7 +54,7 @@ def test_rows_outside_the_sequences_are_left_alone(gpu_lib, cu, dtype):
         ref.check_bwd(dtype, [t[:, lo:hi] if i in rows else t for i, t in enumerate(grads)])
 
 
-@pytest.mark.parametrize("dtype", [BF16])
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_gates_of_the_lowest_value(gpu_lib, dtype):
     # silu and its slope are zero there (z times the zero of its sigmoid), and
     # so is all that such a token gives on: as behind a gate of -1000
