@@ -56,10 +56,11 @@ __device__ inline float exp_full(float x) {
 }
 
 // softplus(v) = max(v, 0) + log(1 + u), u = e^{-|v|}: w = 1 + u is off by
-// d = u - (w - 1), log(w + d) = log(w) + d to 2^-25 of the result.  (Its least
-// value is e^-87; of a NaN the maximum stays.)
+// d = u - (w - 1), log(w + d) = log(w) + d to 2^-25 of the result.  (Of a NaN
+// the maximum stays.)  Its least value is e^-83 = 9e-37: never zero, so that
+// the least step times the lowest finite rate is a decay of zero (rate_of).
 __device__ inline float softplus(float v) {
-  const float u = exp_full(fmaxf(-fabsf(v), -87.f)), w = 1.f + u;
+  const float u = exp_full(fmaxf(-fabsf(v), -83.f)), w = 1.f + u;
   return __builtin_elementwise_maximum(v, 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), u - (w - 1.f));
 }
 
@@ -200,8 +201,9 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
 }
 
 // A rate in powers of two, kept finite so that no step at all (a token past
-// its run) leaves a state as it is; of a rate of -inf the smallest step that
-// there is leaves nothing all the same.
+// its run) leaves a state as it is.  Of a rate of -inf any step that softplus
+// gives leaves nothing all the same (9e-37 x 3.4e38 = 306 halvings); of steps
+// given without it those from 4.4e-37 up.
 __device__ inline float rate_of(float a) {
   const float a2 = a * kLog2e;
   return a2 < -3.4e38f ? -3.4e38f : a2;

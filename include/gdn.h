@@ -504,6 +504,7 @@ gdn_status gdn_group_norm_bwd(const gdn_problem* p, int32_t d, int32_t act, int3
 /* Selective state space scan: a state of dk values for each of the dv
  * channels of every head,
  *   delta_t = softplus(dt_t + dt_bias)      (softplus != 0; else dt_t + dt_bias)
+ *             (at least e^-83 = 9e-37, what softplus is at -83)
  *   S_t[n, j] = exp(delta_t[j] a[n, j]) S_{t-1}[n, j] + delta_t[j] x_t[j] b_t[n]
  *   y_t[j] = (sum_n c_t[n] S_t[n, j] + d[j] x_t[j]) * silu(z_t[j])
  * the recurrence whose decay and write depend on the token, the channel and
@@ -519,7 +520,8 @@ gdn_status gdn_group_norm_bwd(const gdn_problem* p, int32_t d, int32_t act, int3
  *   x, dt, z, y : [B, T, H, dv] io_dtype; z NULL = no gate.
  *   b, c      : [B, T, hb, dk] io_dtype.
  *   a         : [H, dk, dv] fp32 (laid out as a state), normally < 0; of a rate
- *               of -inf no step leaves anything.
+ *               of -inf no step leaves anything (softplus == 0: no step of
+ *               4.4e-37 or more; one of zero leaves all).
  *   d, dt_bias : [H, dv] fp32, each may be NULL (zeros).
  *   s0, s_final : [nseq, H, dk, dv] fp32 or NULL, as in gdn_chunk_fwd.
  *   No output may overlap an input, s_final s0 neither.

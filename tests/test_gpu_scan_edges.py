@@ -104,3 +104,42 @@ def test_a_step_that_is_nan_is_seen(gpu_lib, dtype):
         bad = y.isnan().cpu()[0, :, 0]
         assert bool(bad[13:, 7].all()) and not bad[:13].any() and not bad[:, :7].any()
         assert bool(sf.isnan()[0, 0, :, 7].all()) and int(sf.isnan().sum()) == 8
+
+
+@pytest.mark.parametrize("shift", [-60.0, -82.0, -84.0, -88.0, -120.0, -1e30])
+def test_rates_of_minus_infinity_and_hardly_a_step(gpu_lib, shift):
+    # exp(delta a) of such a rate is zero however small delta is: the oracle
+    # has a rate that even the least of them takes to zero.  (Its own steps are
+    # zero from e^-746 down, which would keep what the rate takes: it has e^-600
+    # there, both far below the bounds.)
+    for cu in (None, [0, 37, 38, 70]):
+        d = make(1 if cu else 2, 70, 2, 1, 16, 40, F32, cu=cu)
+        d["dt_bias"] = torch.full_like(d["dt_bias"], max(shift, -600.0))
+        gone = torch.rand(d["a"].shape, generator=torch.Generator().manual_seed(8)) < 0.25
+        d["a"] = d["a"].double()
+        d["a"][gone] = -1e300
+        ref = Reference(d, cu)
+        d["a"], d["dt_bias"] = d["a"].float(), torch.full_like(d["dt_bias"], shift)
+        assert bool((d["a"][gone] == -float("inf")).all())
+        g = gpu(d)
+        for seg in (0, 1, -1):
+            ref.check_fwd(F32, *run_fwd(g, cu, seg_chunks=seg))
+            ref.check_bwd(F32, run_bwd(g, cu, seg_chunks=seg))
+        one = {k: g[k][:, 0].contiguous() for k in ("x", "dt", "b", "c", "z")}
+        state = g["s0"][:one["x"].shape[0]].clone()
+        gdn.selective_scan_step(one["x"], one["dt"], g["a"], one["b"], one["c"], state, g["d"],
+                                g["dt_bias"], one["z"])
+        # (its token's write alone, delta x b with delta < 1e-25)
+        assert float(state.cpu()[:, gone].abs().max()) < 1e-22
+
+
+def test_rates_of_minus_infinity_and_steps_as_given(gpu_lib):
+    # the least step that leaves nothing, and none, which leaves all
+    H, dk, dv = 1, 4, 8
+    one = lambda v: torch.full((1, 1, H, dv), v, device="cuda")  # noqa: E731
+    b = torch.zeros(1, 1, 1, dk, device="cuda")
+    a = torch.full((H, dk, dv), -float("inf"), device="cuda")
+    s0 = torch.randn(1, H, dk, dv, generator=torch.Generator().manual_seed(1)).cuda()
+    for step, left in ((4.4e-37, 0.0), (1e-30, 0.0), (1.0, 0.0), (0.0, 1.0)):
+        _, sf = gdn.selective_scan_fwd(one(1.0), one(step), a, b, b, s0=s0, softplus=False)
+        assert torch.equal(sf, s0 * left), step
