@@ -772,11 +772,18 @@ def _packed(cu_seqlens, x):
     return cu_seqlens.numel() - 1
 
 
-def _apart(out, name, **inputs):
-    """Refuses an output that is one of the inputs."""
-    for other, t in inputs.items():
-        if t is not None and out is not None and out.numel() and out.data_ptr() == t.data_ptr():
-            raise ValueError(f"{name} must not be {other}")
+def _apart(out, name, same=(), /, **others):
+    """Refuses a caller's output that shares memory with another tensor of the
+    call; those named in ``same`` may be the output itself, whole."""
+    if out is None or out.numel() == 0:
+        return
+    lo, size = out.data_ptr(), out.numel() * out.element_size()
+    for other, t in others.items():
+        if t is None:
+            continue
+        at, n = t.data_ptr(), t.numel() * t.element_size()
+        if at < lo + size and lo < at + n and not (other in same and at == lo and n == size):
+            raise ValueError(f"{name} must not be or overlap {other}")
 
 
 def _scan_problem(x, dt, a, b, c, d, dt_bias, z, cu_seqlens, seg_chunks, lead):
@@ -816,10 +823,15 @@ def selective_scan_fwd(x, dt, a, b, c, d=None, dt_bias=None, z=None, s0=None,
     lib = _lib.load()
     p, hb, states = _scan_problem(x, dt, a, b, c, d, dt_bias, z, cu_seqlens, seg_chunks, 2)
     _want(s0, "s0", states, torch.float32, x.device)
+    if not output_final_state:
+        s_final = None
+    if y is not None or s_final is not None:
+        ins = dict(x=x, dt=dt, a=a, b=b, c=c, d=d, dt_bias=dt_bias, z=z, s0=s0,
+                   cu_seqlens=cu_seqlens)
+        _apart(y, "y", **ins)
+        _apart(s_final, "s_final", y=y, **ins)
     y = _result(y, "y", x)
     sf = _states(s_final, "s_final", states, x.device, s0) if output_final_state else None
-    _apart(y, "y", x=x, dt=dt, z=z)
-    _apart(sf, "s_final", s0=s0)
     ws, nbytes = _workspace(workspace, _bytes(lib.gdn_selective_scan_fwd_workspace, p, hb),
                             x.device)
     _launch(lib.gdn_selective_scan_fwd, x.device, ctypes.byref(p), hb, int(softplus), _ptr(x),
@@ -856,12 +868,16 @@ def selective_scan_step(x, dt, a, b, c, state, d=None, dt_bias=None, z=None,
                         softplus: bool = True, y=None):
     """One token per sequence of :func:`selective_scan_fwd`'s rule
     (gdn_selective_scan_step); ``state`` [N,H,dk,dv] fp32 is updated in place.
-    x, dt, z [N,H,dv]; b, c [N,Hb,dk].  Returns y [N,H,dv]."""
+    x, dt, z [N,H,dv]; b, c [N,Hb,dk].  Returns y [N,H,dv] (may be x, dt or z
+    itself)."""
     lib = _lib.load()
     p, hb, states = _scan_problem(x, dt, a, b, c, d, dt_bias, z, None, 0, 1)
     if state is None:
         raise ValueError("state must be given")
     _want(state, "state", states, torch.float32, x.device)
+    if y is not None:
+        _apart(y, "y", ("x", "dt", "z"), x=x, dt=dt, z=z, a=a, b=b, c=c, d=d, dt_bias=dt_bias,
+               state=state)
     y = _result(y, "y", x)
     _launch(lib.gdn_selective_scan_step, x.device, ctypes.byref(p), hb, int(softplus), _ptr(x),
             _ptr(dt), _ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(dt_bias), _ptr(z), _ptr(state),
@@ -900,15 +916,16 @@ def short_conv_fwd(x, taps, bias=None, s0=None, act: str = "silu", cu_seqlens=No
     lib = _lib.load()
     p, width, code, hist = _conv_problem(x, taps, bias, act, cu_seqlens, 2)
     _want(s0, "s0", hist, x.dtype, x.device)
-    y = _result(y, "y", x)
-    _apart(y, "y", x=x)
     if not output_final_state:
         s_final = None
-    elif s_final is None:
+    if y is not None or s_final is not None:
+        ins = dict(x=x, taps=taps, bias=bias, s0=s0, cu_seqlens=cu_seqlens)
+        _apart(y, "y", **ins)
+        _apart(s_final, "s_final", y=y, **ins)
+    y = _result(y, "y", x)
+    if output_final_state and s_final is None:
         s_final = torch.empty(hist, dtype=x.dtype, device=x.device)
-    else:
-        _want(s_final, "s_final", hist, x.dtype, x.device)
-        _apart(s_final, "s_final", s0=s0)
+    _want(s_final, "s_final", hist, x.dtype, x.device)
     _launch(lib.gdn_short_conv_fwd, x.device, ctypes.byref(p), width, code, _ptr(x), _ptr(taps),
             _ptr(bias), _ptr(s0), _ptr(y), _ptr(s_final))
     return y, s_final
@@ -945,6 +962,8 @@ def short_conv_step(x, taps, state, bias=None, act: str = "silu", y=None):
     if state is None:
         raise ValueError("state must be given")
     _want(state, "state", hist, x.dtype, x.device)
+    if y is not None:
+        _apart(y, "y", ("x",), x=x, taps=taps, state=state, bias=bias)
     y = _result(y, "y", x)
     _launch(lib.gdn_short_conv_step, x.device, ctypes.byref(p), width, code, _ptr(x), _ptr(taps),
             _ptr(bias), _ptr(state), _ptr(y))
@@ -986,10 +1005,16 @@ def draft_accept(tokens, target, draft, uniform, parent=None, cu_seqlens=None,
     if out is None:
         out = tuple(torch.empty(3, trees, dtype=torch.int32, device=device)) if trees % 4 == 0 \
             else tuple(torch.empty(trees, dtype=torch.int32, device=device) for _ in range(3))
-    for t in out:
-        _want(t, "out", (trees,), torch.int32, device)
+    else:
+        out = tuple(out)
+        if len(out) != 3 or any(t is None for t in out):
+            raise ValueError("out must hold three tensors")
+        for i, t in enumerate(out):
+            _want(t, "out", (trees,), torch.int32, device)
+            _apart(t, "out", tokens=tokens, target=target, draft=draft, uniform=uniform,
+                   parent=parent, cu_seqlens=cu_seqlens, out=out[i - 1])
     ws, nbytes = _workspace(
         workspace, _bytes(lib.gdn_draft_accept_workspace, p, V, int(parents is not None)), device)
     _launch(lib.gdn_draft_accept, device, ctypes.byref(p), V, parents, _ptr(tokens), _ptr(target),
             _ptr(draft), _ptr(uniform), *(_ptr(t) for t in out), _ptr(ws), nbytes)
-    return tuple(out)
+    return out

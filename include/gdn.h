@@ -524,7 +524,7 @@ gdn_status gdn_group_norm_bwd(const gdn_problem* p, int32_t d, int32_t act, int3
  *               4.4e-37 or more; one of zero leaves all).
  *   d, dt_bias : [H, dv] fp32, each may be NULL (zeros).
  *   s0, s_final : [nseq, H, dk, dv] fp32 or NULL, as in gdn_chunk_fwd.
- *   No output may overlap an input, s_final s0 neither.
+ *   No output may overlap an input or another output, s_final s0 neither.
  *   ws        : at least gdn_selective_scan_fwd_workspace bytes; calls that
  *               overlap in time (streams, captured graphs) need one each.
  * All arithmetic is fp32, the state too.  Rows of packed tensors in front of
@@ -557,8 +557,9 @@ gdn_status gdn_selective_scan_bwd(const gdn_problem* p, int32_t hb, int32_t soft
 
 /* One token per sequence of the same rule (B = N sequences), state updated
  * in place; each state element is read once and written once.  x, dt, z, y
- * [N, H, dv]; b, c [N, hb, dk]; state [N, H, dk, dv] fp32.  T, chunk, nseq,
- * cu_seqlens and seg_chunks of the problem are ignored. */
+ * [N, H, dv]; b, c [N, hb, dk]; state [N, H, dk, dv] fp32.  y may be x, dt or
+ * z itself; nothing else may overlap.  T, chunk, nseq, cu_seqlens and
+ * seg_chunks of the problem are ignored. */
 gdn_status gdn_selective_scan_step(const gdn_problem* p, int32_t hb, int32_t softplus,
                                    const void* x, const void* dt, const float* a, const void* b,
                                    const void* c, const float* d, const float* dt_bias,
@@ -576,7 +577,7 @@ gdn_status gdn_selective_scan_step(const gdn_problem* p, int32_t hb, int32_t sof
  *   s0, s_final : [nseq, width - 1, H, dv] io_dtype, a sequence's last
  *               width - 1 inputs, oldest first; s0 NULL = zeros, s_final NULL
  *               to skip it.
- * No output may overlap an input: y not x, s_final not s0.
+ * No output may overlap an input or the other output: y not x, s_final not s0.
  * Rows behind cu_seqlens[nseq] are neither read nor written. */
 gdn_status gdn_short_conv_fwd(const gdn_problem* p, int32_t width, int32_t act, const void* x,
                               const float* taps, const float* bias, const void* s0, void* y,
@@ -594,7 +595,7 @@ gdn_status gdn_short_conv_bwd(const gdn_problem* p, int32_t width, int32_t act, 
 
 /* One token per sequence (B = N sequences): x, y [N, H, dv]; state
  * [N, width - 1, H, dv] io_dtype, moved up by the token in place (may be NULL
- * for width 1).  y may be x. */
+ * for width 1).  y may be x itself; nothing else may overlap. */
 gdn_status gdn_short_conv_step(const gdn_problem* p, int32_t width, int32_t act, const void* x,
                                const float* taps, const float* bias, void* state, void* y,
                                void* stream);
@@ -628,6 +629,7 @@ gdn_status gdn_short_conv_step(const gdn_problem* p, int32_t width, int32_t act,
  *   accepted  : int32 [trees], the last accepted node or -1 (what
  *               gdn_tree_commit takes);  length : accepted nodes;
  *   next_token : the token behind them.
+ *   No output may overlap an input or another output.
  *   ws        : at least gdn_draft_accept_workspace bytes (tree: parent is
  *               given).
  * Sums are 64 bits.  Deterministic. */

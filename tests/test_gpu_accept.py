@@ -331,3 +331,15 @@ def test_a_draft_without_its_last_row(gpu_lib, V, dtype, tree):
         want = reference(d, sizes)
         assert u is None or (want[1] == sizes).all()
         assert np.array_equal(np.stack([t.cpu().numpy() for t in out]), want)
+
+
+def test_outputs_that_overlap_are_refused(gpu_lib):
+    d = make([1] * 4, 50, F32, False)
+    g = {k: t.cuda() for k, t in d.items() if t is not None}
+    cu = torch.arange(5, dtype=torch.int32, device="cuda")
+    t = [torch.empty(4, dtype=torch.int32, device="cuda") for _ in range(3)]
+    for out in ([g["tokens"], t[1], t[2]], [t[0], cu[1:], t[2]], [t[0], t[1], t[0]], t[:2],
+                [t[0], t[1], None]):
+        with pytest.raises(ValueError):
+            gdn.draft_accept(g["tokens"], g["target"], g["draft"], g["uniform"], cu_seqlens=cu,
+                             out=out)

@@ -143,3 +143,46 @@ def test_rates_of_minus_infinity_and_steps_as_given(gpu_lib):
     for step, left in ((4.4e-37, 0.0), (1e-30, 0.0), (1.0, 0.0), (0.0, 1.0)):
         _, sf = gdn.selective_scan_fwd(one(1.0), one(step), a, b, b, s0=s0, softplus=False)
         assert torch.equal(sf, s0 * left), step
+
+
+def test_outputs_that_overlap_are_refused(gpu_lib):
+    # also b and c, which have y's shape where each head has rows of its own,
+    # and any part of a tensor
+    H, n = 2, 16
+    g = gpu(make(1, 10, H, H, n, n, F32))
+    ins = {k: g[k] for k in ("x", "dt", "a", "b", "c")}
+    buf = torch.zeros(3 * g["x"].numel(), device="cuda")
+    size = g["x"].numel()
+    part = lambda at, like: buf[at:at + like.numel()].view(like.shape)  # noqa: E731
+    states = torch.zeros(2 * g["s0"].numel(), device="cuda")
+    shared = states[H * n:H * n + g["s0"].numel()].view(g["s0"].shape)
+    shared.copy_(g["s0"])
+    bad = [dict(y=g["b"]), dict(y=g["c"]), dict(y=g["x"]), dict(y=g["z"], z=g["z"]),
+           dict(x=part(0, g["x"]), y=part(8 * n, g["x"])),
+           dict(b=part(size, g["x"]), y=part(size - 4, g["x"])),
+           dict(s0=shared, s_final=states[:g["s0"].numel()].view(g["s0"].shape)),
+           dict(a=g["s0"][0], s_final=g["s0"]),
+           dict(y=states[:size].view(g["x"].shape), s_final=shared)]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            gdn.selective_scan_fwd(**{**ins, **kw})
+    # parts that only touch are fine
+    want, _ = gdn.selective_scan_fwd(**ins)
+    x, y = part(0, g["x"]), part(size, g["x"])
+    x.copy_(g["x"])
+    gdn.selective_scan_fwd(**{**ins, "x": x}, y=y)
+    assert torch.equal(y, want)
+    one = {k: t[:, 0].contiguous() if k != "a" else t for k, t in ins.items()}
+    for other in ("b", "c"):
+        with pytest.raises(ValueError):
+            gdn.selective_scan_step(**one, state=g["s0"].clone(), y=one[other])
+    s = g["s0"].clone()
+    with pytest.raises(ValueError):
+        gdn.selective_scan_step(**one, state=s, y=s.view(-1)[:one["x"].numel()].view(1, H, n))
+    # the step's own rows may be its output
+    z = g["z"][:, 0].contiguous()
+    want = gdn.selective_scan_step(**one, state=g["s0"].clone(), z=z)
+    for k in ("x", "dt", "z"):
+        rows = {n: t.clone() for n, t in {**one, "z": z}.items()}
+        gdn.selective_scan_step(**rows, state=g["s0"].clone(), y=rows[k])
+        assert torch.equal(rows[k], want), k

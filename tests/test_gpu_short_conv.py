@@ -279,3 +279,21 @@ def test_outputs_that_are_inputs_are_refused(gpu_lib):
     d = {k: t.cuda() for k, t in make(2, 10, 2, 16, 4, F32).items()}
     with pytest.raises(ValueError):
         gdn.short_conv_fwd(d["x"], d["taps"], y=d["x"])
+
+
+def test_outputs_that_overlap_are_refused(gpu_lib):
+    d = {k: t.cuda() for k, t in make(2, 10, 2, 16, 4, F32).items()}
+    n = d["x"].numel()
+    buf = torch.zeros(2 * n, device="cuda")
+    x = buf[:n].view(d["x"].shape)
+    kept = buf[n - 16:n - 16 + d["s0"].numel()].view(d["s0"].shape)
+    for kw in (dict(x=x, y=buf[32:n + 32].view(x.shape)), dict(x=x, s_final=kept),
+               dict(x=d["x"], s0=d["s0"], y=d["x"]),
+               dict(x=d["x"], y=buf[:n].view(x.shape), s_final=kept)):
+        with pytest.raises(ValueError):
+            gdn.short_conv_fwd(taps=d["taps"], **kw)
+    one = buf[:64].view(2, 2, 16)
+    state = torch.zeros(2, 3, 2, 16, device="cuda")
+    for kw in (dict(y=buf[16:80].view(2, 2, 16)), dict(y=state.view(-1)[:64].view(2, 2, 16))):
+        with pytest.raises(ValueError):
+            gdn.short_conv_step(one, d["taps"], state, **kw)
