@@ -786,6 +786,26 @@ def _apart(out, name, same=(), /, **others):
             raise ValueError(f"{name} must not be or overlap {other}")
 
 
+def _gradients(out, ins, **others):
+    """Gradients of ``ins``, each like its input: the caller's preallocated
+    ones, checked, or new tensors; None where the input is."""
+    if out is None:
+        return [None if t is None else torch.empty_like(t) for t in ins.values()]
+    out = list(out)
+    if len(out) != len(ins):
+        raise ValueError(f"out must have {len(ins)} entries")
+    grads = {}
+    for (name, t), o in zip(ins.items(), out):
+        if t is None and o is not None:
+            raise ValueError(f"out has a gradient of {name}, which is not given")
+        if o is not None:
+            _want(o, f"d{name}", t.shape, t.dtype, t.device)
+            _apart(o, f"d{name}", **ins, **others, **grads)
+            grads[f"d{name}"] = o
+    return [o if o is not None or t is None else torch.empty_like(t)
+            for t, o in zip(ins.values(), out)]
+
+
 def _scan_problem(x, dt, a, b, c, d, dt_bias, z, cu_seqlens, seg_chunks, lead):
     """The problem of a selective-scan call, its rows of b and c, and the shape
     of its states; `lead`: dimensions in front of the heads."""
@@ -842,10 +862,12 @@ def selective_scan_fwd(x, dt, a, b, c, d=None, dt_bias=None, z=None, s0=None,
 
 def selective_scan_bwd(x, dt, a, b, c, dy, d=None, dt_bias=None, z=None, s0=None, ds_final=None,
                        softplus: bool = True, cu_seqlens=None,
-                       workspace: Optional[torch.Tensor] = None, seg_chunks: int = 0):
+                       workspace: Optional[torch.Tensor] = None, seg_chunks: int = 0, out=None):
     """Backward of :func:`selective_scan_fwd` (gdn_selective_scan_bwd):
-    gradients of <dy, y> + <ds_final, s_final>.  Returns (dx, ddt, da, db, dc,
-    dd, ddt_bias, dz, ds0); the last four are None where their input is."""
+    gradients of <dy, y> + <ds_final, s_final>.  out: optional preallocated
+    (dx, ddt, da, db, dc, dd, ddt_bias, dz, ds0), entries may be None; rows of
+    a packed batch outside its sequences stay as they are there.  Returns
+    those; the last four are None where their input is."""
     lib = _lib.load()
     p, hb, states = _scan_problem(x, dt, a, b, c, d, dt_bias, z, cu_seqlens, seg_chunks, 2)
     _want(s0, "s0", states, torch.float32, x.device)
@@ -853,8 +875,9 @@ def selective_scan_bwd(x, dt, a, b, c, dy, d=None, dt_bias=None, z=None, s0=None
     if dy is None:
         raise ValueError("dy must be given")
     _want(dy, "dy", x.shape, x.dtype, x.device)
-    dx, ddt, da, db, dc = (torch.empty_like(t) for t in (x, dt, a, b, c))
-    dd, dbias, dz, ds0 = (None if t is None else torch.empty_like(t) for t in (d, dt_bias, z, s0))
+    ins = dict(x=x, dt=dt, a=a, b=b, c=c, d=d, dt_bias=dt_bias, z=z, s0=s0)
+    dx, ddt, da, db, dc, dd, dbias, dz, ds0 = _gradients(out, ins, dy=dy, ds_final=ds_final,
+                                                         cu_seqlens=cu_seqlens)
     ws, nbytes = _workspace(workspace, _bytes(lib.gdn_selective_scan_bwd_workspace, p, hb),
                             x.device)
     _launch(lib.gdn_selective_scan_bwd, x.device, ctypes.byref(p), hb, int(softplus), _ptr(x),
@@ -932,9 +955,10 @@ def short_conv_fwd(x, taps, bias=None, s0=None, act: str = "silu", cu_seqlens=No
 
 
 def short_conv_bwd(x, taps, dy, bias=None, s0=None, ds_final=None, act: str = "silu",
-                   cu_seqlens=None, workspace: Optional[torch.Tensor] = None):
+                   cu_seqlens=None, workspace: Optional[torch.Tensor] = None, out=None):
     """Backward of :func:`short_conv_fwd` (gdn_short_conv_bwd): gradients of
-    <dy, y> + <ds_final, s_final>.  Returns (dx, dtaps, dbias, ds0); the last
+    <dy, y> + <ds_final, s_final>.  out: optional preallocated (dx, dtaps,
+    dbias, ds0), as in :func:`selective_scan_bwd`.  Returns those; the last
     two are None where their input is."""
     lib = _lib.load()
     p, width, code, hist = _conv_problem(x, taps, bias, act, cu_seqlens, 2)
@@ -943,8 +967,8 @@ def short_conv_bwd(x, taps, dy, bias=None, s0=None, ds_final=None, act: str = "s
     if dy is None:
         raise ValueError("dy must be given")
     _want(dy, "dy", x.shape, x.dtype, x.device)
-    dx, dtaps = torch.empty_like(x), torch.empty_like(taps)
-    dbias, ds0 = (None if t is None else torch.empty_like(t) for t in (bias, s0))
+    dx, dtaps, dbias, ds0 = _gradients(out, dict(x=x, taps=taps, bias=bias, s0=s0), dy=dy,
+                                       ds_final=ds_final, cu_seqlens=cu_seqlens)
     ws, nbytes = _workspace(workspace, _bytes(lib.gdn_short_conv_bwd_workspace, p, width),
                             x.device)
     _launch(lib.gdn_short_conv_bwd, x.device, ctypes.byref(p), width, code, _ptr(x), _ptr(taps),

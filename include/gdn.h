@@ -544,8 +544,9 @@ gdn_status gdn_selective_scan_fwd(const gdn_problem* p, int32_t hb, int32_t soft
  *   with z); da [H, dk, dv], dd, ddt_bias [H, dv] and ds0 [nseq, H, dk, dv]
  *   fp32; dd, ddt_bias and ds0 may be NULL to skip them, ds_final NULL = zeros.
  * Rows of dx, ddt, db, dc and dz in front of cu_seqlens[0] and behind
- * cu_seqlens[nseq] stay as they are.  Sums over tokens and channels run in a
- * fixed order (deterministic). */
+ * cu_seqlens[nseq] stay as they are.  No output may overlap an input or
+ * another output.  Sums over tokens and channels run in a fixed order
+ * (deterministic). */
 gdn_status gdn_selective_scan_bwd_workspace(const gdn_problem* p, int32_t hb, size_t* bytes);
 gdn_status gdn_selective_scan_bwd(const gdn_problem* p, int32_t hb, int32_t softplus,
                                   const void* x, const void* dt, const float* a, const void* b,
@@ -585,8 +586,9 @@ gdn_status gdn_short_conv_fwd(const gdn_problem* p, int32_t width, int32_t act, 
 
 /* Backward of gdn_short_conv_fwd: gradients of <dy, y> + <ds_final, s_final>.
  * dx and ds0 in io_dtype, dtaps and dbias fp32 (overwritten; dbias and ds0
- * may be NULL to skip them, ds_final NULL = zeros).  Sums over tokens run in
- * a fixed order (deterministic). */
+ * may be NULL to skip them, ds_final NULL = zeros).  Rows of dx outside the
+ * sequences stay as they are; no output may overlap an input or another
+ * output.  Sums over tokens run in a fixed order (deterministic). */
 gdn_status gdn_short_conv_bwd_workspace(const gdn_problem* p, int32_t width, size_t* bytes);
 gdn_status gdn_short_conv_bwd(const gdn_problem* p, int32_t width, int32_t act, const void* x,
                               const float* taps, const float* bias, const void* s0,

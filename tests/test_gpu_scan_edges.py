@@ -186,3 +186,31 @@ def test_outputs_that_overlap_are_refused(gpu_lib):
         rows = {n: t.clone() for n, t in {**one, "z": z}.items()}
         gdn.selective_scan_step(**rows, state=g["s0"].clone(), y=rows[k])
         assert torch.equal(rows[k], want), k
+
+
+@pytest.mark.parametrize("cu", [None, [3, 20, 37]])
+def test_preallocated_gradients(gpu_lib, cu):
+    d = make(1 if cu else 2, 45, 2, 2, 16, 40, BF16, cu=cu)
+    g = gpu(d)
+    want = run_bwd(g, cu)
+    lo, hi = (0, 45) if cu is None else (cu[0], cu[-1])
+    out = [torch.full_like(t, 7.0) for t in want]
+    got = run_bwd(g, cu, out=out)
+    for i, (a, o, b) in enumerate(zip(got, out, want)):
+        assert a is o
+        if i in (0, 1, 3, 4, 7):
+            assert bool((a[:, :lo] == 7.0).all()) and bool((a[:, hi:] == 7.0).all())
+            a, b = a[:, lo:hi], b[:, lo:hi]
+        assert torch.equal(a, b), i
+    # some of them, and none of what is not there
+    part = [torch.empty_like(out[0]), *[None] * 8]
+    got = run_bwd({**g, "d": None, "z": None}, cu, out=part)
+    assert got[0] is part[0] and got[5] is None and got[7] is None
+    ins = [g[k] for k in ("x", "dt", "a", "b", "c", "dy", "d", "dt_bias", "z", "s0", "ds")]
+    for bad in (out[:8], [out[0][:, :9], *out[1:]], [g["x"], *out[1:]], [g["dy"], *out[1:]],
+                [out[0], out[0], *out[2:]], [*out[:3], out[0][..., :16], *out[4:]],
+                [*out[:2], out[2].to(BF16), *out[3:]], [*out[:8], g["ds"]]):
+        with pytest.raises(ValueError):
+            gdn.selective_scan_bwd(*ins, cu_seqlens=dev_cu(cu), out=bad)
+    with pytest.raises(ValueError):
+        run_bwd({**g, "z": None}, cu, out=out)

@@ -297,3 +297,41 @@ def test_outputs_that_overlap_are_refused(gpu_lib):
     for kw in (dict(y=buf[16:80].view(2, 2, 16)), dict(y=state.view(-1)[:64].view(2, 2, 16))):
         with pytest.raises(ValueError):
             gdn.short_conv_step(one, d["taps"], state, **kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cu", [[0, 20, 37], [5, 20, 20, 41], [16, 16, 16]])
+def test_gradients_outside_the_sequences_are_left_alone(gpu_lib, cu, dtype):
+    # in front of the first and behind the last; the workspace holds NaN
+    d = make(1, 60, 2, 16, 4, dtype, cu=cu)
+    lo, hi = cu[0], cu[-1]
+    for k in ("x", "dy"):
+        d[k][:, :lo], d[k][:, hi:] = float("nan"), float("nan")
+    g = {k: t.cuda() for k, t in d.items()}
+    out = [torch.full_like(g[k], 7.0) for k in ("x", "taps", "bias", "s0")]
+    ws = torch.full((1 << 20,), float("nan"), device="cuda")
+    y = torch.full_like(g["x"], 7.0)
+    y, sf = gdn.short_conv_fwd(g["x"], g["taps"], g["bias"], g["s0"], cu_seqlens=dev_cu(cu), y=y)
+    got = gdn.short_conv_bwd(g["x"], g["taps"], g["dy"], g["bias"], g["s0"], g["ds"],
+                             cu_seqlens=dev_cu(cu), workspace=ws, out=out)
+    torch.cuda.synchronize()
+    assert all(a is b for a, b in zip(got, out))
+    for t in (y, got[0]):
+        assert bool((t[:, :lo] == 7.0).all()) and bool((t[:, hi:] == 7.0).all())
+    inside = {k: t[:, lo:hi].contiguous() if k in ("x", "dy") else t for k, t in d.items()}
+    check(inside, [n - lo for n in cu], "silu", dtype, y[:, lo:hi], sf,
+          (got[0][:, lo:hi], *got[1:]))
+
+
+def test_preallocated_gradients_are_checked(gpu_lib):
+    d = {k: t.cuda() for k, t in make(2, 10, 2, 16, 4, F32).items()}
+    out = [torch.empty_like(d[k]) for k in ("x", "taps", "bias", "s0")]
+    ins = (d["x"], d["taps"], d["dy"], d["bias"], d["s0"], d["ds"])
+    for bad in (out[:3], [out[0][:1], *out[1:]], [d["dy"], *out[1:]], [*out[:3], d["ds"]],
+                [out[0], out[1].to(BF16), *out[2:]]):
+        with pytest.raises(ValueError):
+            gdn.short_conv_bwd(*ins, out=bad)
+    with pytest.raises(ValueError):
+        gdn.short_conv_bwd(*ins[:3], None, *ins[4:], out=out)
+    got = gdn.short_conv_bwd(*ins, out=[None, out[1], None, None])
+    assert got[1] is out[1] and got[3] is not None
