@@ -1369,7 +1369,7 @@ void with_plan(const Plan& q, bool gate, F f) {
   };
   auto pads = [&](auto ns, auto ws) {
     if (!q.pad) return all(ns, ws, std::false_type{});
-    if constexpr (ns * ws > 4) all(ns, ws, std::true_type{});
+    if constexpr (ns * ws > 8) all(ns, ws, std::true_type{});  // (4 and 8 states are whole)
   };
   auto waves = [&](auto ns) {
     if (q.ws == 1) return pads(ns, integral_constant<int, 1>{});
