@@ -614,8 +614,9 @@ gdn_status gdn_short_conv_step(const gdn_problem* p, int32_t width, int32_t act,
  * exceeds u[last] sum(r), or the last with r > 0 where rounding leaves none.
  *   p         : B trees of T nodes, T <= 64 (else GDN_ERR_SHAPE), or nseq
  *               trees packed by cu_seqlens (B == 1; of more than 64 nodes the
- *               first 64 are tried, and the answer is unspecified); io_dtype
- *               is that of the probabilities; the rest is ignored.
+ *               first 64 are tried, and the answer is unspecified); at most
+ *               2^20 trees (else GDN_ERR_SHAPE); io_dtype is that of the
+ *               probabilities; the rest is ignored.
  *   vocab     : 1 .. 2^28.
  *   parent    : device int32 as in gdn_tree_verify, or NULL for chains (node
  *               i continues node i - 1).
@@ -626,6 +627,8 @@ gdn_status gdn_short_conv_step(const gdn_problem* p, int32_t width, int32_t act,
  *               i + 1 those behind node i.  Values that are NaN count as 0.
  *   draft     : the draft's, laid out the same (rows of nodes without
  *               children are not read), or NULL: q is 1 at the drafted token.
+ *               A token whose value is NaN is not accepted, and nothing of it
+ *               is left behind a rejection.
  *   uniform   : [B, T + 1] or [nodes + nseq] fp32 in [0, 1): one for each
  *               node, then the last for the next token.
  *   accepted  : int32 [trees], the last accepted node or -1 (what

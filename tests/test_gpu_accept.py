@@ -343,3 +343,18 @@ def test_outputs_that_overlap_are_refused(gpu_lib):
         with pytest.raises(ValueError):
             gdn.draft_accept(g["tokens"], g["target"], g["draft"], g["uniform"], cu_seqlens=cu,
                              out=out)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [512, 5001, 40000])
+def test_nan_in_a_draft_row(gpu_lib, V, dtype, tree):
+    # such a token is not accepted, and nothing of it is left behind a
+    # rejection: what a draft's infinity comes to, which the oracle has
+    sizes = [6] * 8
+    d = make(sizes, V, dtype, tree, far=2.0, seed=V)
+    bad = torch.rand(V, generator=torch.Generator().manual_seed(2)) < 0.2
+    want = dict(d, draft=torch.where(bad, float("inf"), d["draft"].float()).to(dtype))
+    got = dict(d, draft=torch.where(bad, float("nan"), d["draft"].float()).to(dtype))
+    assert np.array_equal(run(got, sizes, True), reference(want, sizes))
+    assert np.array_equal(run(want, sizes, True), reference(want, sizes))
