@@ -18,12 +18,14 @@
 // leaves.  What bounds a call is a chain of waits, not their bytes: the nodes,
 // the values of their tokens, a row, its sum, and again for every row.  One
 // workgroup walks a sequence, with its row in the CU where it fits (256 trees
-// of 16 nodes over 32000 fp32 values: 40 us, of which 65 MB at the rate of a
-// copy are 13; a chain of 8: 13 us).  Longer rows, and odd ones, are read anew
-// for every sum; of a chain of such only one node is ever tried at a place, so
-// its end is known from gathered values alone: every workgroup finds it by
-// itself and takes a slab of the row, a second launch finds the token in the
-// slabs' sums.
+// of 16 nodes over 32000 fp32 values: 36 to 42 us by the slowest of them, where
+// 65 MB at the rate of a copy are 13; a chain of 8: 12 us).  Longer rows, and
+// odd ones, are read anew for every sum (256 such trees over 32001 fp32 values:
+// 145 us, over 50257: 195; over 128256 values in bf16: 324).  Of a chain of such
+// only one node is ever tried at a place, so its end is known from gathered
+// values alone: every workgroup finds it by itself and takes a slab of the row,
+// a second launch finds the token in the slabs' sums (256 chains of 16 over
+// 50257 fp32 values 51 us, one of them 15).
 
 #include <algorithm>
 
@@ -215,8 +217,7 @@ __device__ inline int draw(const Row<IO>& r, int lo, int hi, double target, int 
   }
   double w[kLastPer];
   const int at = lo + threadIdx.x * kLastPer;
-#pragma unroll
-  for (int e = 0; e < kLastPer; ++e) w[e] = at + e < hi ? r.at(at + e) : 0.0;
+  r.take(at, hi, w);
   return find(w, at, target, none, meet);
 }
 

@@ -26,8 +26,16 @@ struct AcceptRow {
     }
     return w;
   }
-  __device__ inline double at(int x) const {
-    return less(IO::load(p, x), two() ? IO::load(q, x) : 0.f, x);
+  // The values of tokens x on, zeros from hi on; all loads in front of their
+  // use, so that one wait is for all of a row's.
+  template <int N>
+  __device__ inline void take(int x, int hi, double (&w)[N]) const {
+    float pv[N], qv[N];
+    for (int e = 0; e < N; ++e) pv[e] = x + e < hi ? IO::load(p, x + e) : 0.f;
+    for (int e = 0; e < N; ++e) qv[e] = 0.f;
+    if (two())
+      for (int e = 0; e < N; ++e) qv[e] = x + e < hi ? IO::load(q, x + e) : 0.f;
+    for (int e = 0; e < N; ++e) w[e] = x + e < hi ? less(pv[e], qv[e], x + e) : 0.0;
   }
 };
 

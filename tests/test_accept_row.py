@@ -32,7 +32,9 @@ int main() {
       const gdn::AcceptRow<watched> r{target, with ? draft : nullptr, m, scale, tried};
       reads = 0;
       printf("%d %d:", with, m);
-      for (int x = 0; x < 3; ++x) printf(" %.17g", r.at(x));
+      double w[4];
+      r.take(0, 3, w);
+      for (int x = 0; x < 4; ++x) printf(" %.17g", w[x]);
       printf(" reads %d two %d\n", reads, static_cast<int>(r.two()));
     }
 }
@@ -50,10 +52,10 @@ def test_a_draft_row_is_read_behind_a_rejection_only(tmp_path):
     # the target's row; less the draft's (or a one at the token), then that
     # times 4 less it again
     assert out[:6] == [
-        "0 0: 0.5 0.25 0.25 reads 0 two 0",
-        "0 1: 0.5 0 0.25 reads 0 two 0",
-        "0 2: 1 0 1 reads 0 two 0",
-        "1 0: 0.5 0.25 0.25 reads 0 two 0",
-        "1 1: 0.25 0 0 reads 3 two 1",
-        "1 2: 0.75 0 0 reads 3 two 1"]
+        "0 0: 0.5 0.25 0.25 0 reads 0 two 0",
+        "0 1: 0.5 0 0.25 0 reads 0 two 0",
+        "0 2: 1 0 1 0 reads 0 two 0",
+        "1 0: 0.5 0.25 0.25 0 reads 0 two 0",
+        "1 1: 0.25 0 0 0 reads 3 two 1",
+        "1 2: 0.75 0 0 0 reads 3 two 1"]
 
