@@ -12,9 +12,11 @@
 // A thread owns V adjacent channels (one 16-byte piece where the row allows
 // it) and walks a run of tokens with the last W - 1 inputs in registers, so
 // every row is read once and memory bounds the pass: the forward of 16384
-// tokens of 4096 channels in bf16, width 4, 53 us or 5.1 TB/s.  The backward
-// (16384 tokens of 1024 channels: 33 us, 3.1 TB/s) has fewer, shorter rows and
-// 45 instructions for a token and channel beside them.  Runs lie on the grid of
+// tokens of 4096 channels in bf16, width 4, 53 us with its inputs in cache, 60
+// without (5.1, 4.5 TB/s).  The backward (16384 tokens of 1024 channels: 33 and
+// 39 us, 3.1 and 2.6 TB/s) fills neither: its 512 workgroups are two waves a
+// SIMD, with which the vector unit is 52 % busy, and more of them leave more
+// shares of dtaps and dbias to add (kBwdBlocks).  Runs lie on the grid of
 // all tokens; a walk that meets a sequence's end takes up the next one's
 // history.
 
@@ -82,10 +84,12 @@ __device__ inline void store_v(void* p, int64_t i, const float* x) {
   }
 }
 
-// The hardware's exponential and reciprocal for bf16 rows (their errors, a few
-// 2^-24 times |p|, are far below the rows' rounding; a division in full takes
-// ten instructions more, and the forward of 16384 tokens of 4096 channels 57 us
-// instead of 53), the library's exponential and a division for fp32 ones.
+// The hardware's exponential and reciprocal for bf16 rows, the library's
+// exponential and a division for fp32 ones.  What the former are off by, a few
+// 2^-24 (1 + |p|) of the value, is far below the rounding of rows in bf16; in
+// the fp32 sums dtaps and dbias it is the size of a term's own rounding (a
+// division in full takes ten instructions more, and the forward of 16384
+// tokens of 4096 channels 57 us instead of 53).
 template <typename IO>
 __device__ inline float sigmoid(float x) {
   if constexpr (io<IO>::bytes == 2) return __builtin_amdgcn_rcpf(1.0f + __expf(-x));
@@ -432,7 +436,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Channels of a thread: a 16-byte piece of a row, 8 bytes where wide windows
 // of it would not fit the registers, one channel where rows are not whole
-// pieces.
+// pieces.  The backward keeps twice the window: 16384 tokens of 1024 channels
+// in bf16 take 33 us with four channels a thread, 45 with eight (of 4096
+// channels 121 and 102; widths from 5 on have four either way).
 int vec_of(const ShortConv& p, bool bwd) {
   int v = p.io == GDN_BF16 ? 8 : 4;
   if (p.width > 4 || bwd) v = 4;
@@ -454,9 +460,11 @@ Args make_args(const ShortConv& p, int V, int64_t most) {
   return A;
 }
 
-// (backward, 16384 tokens of 1024 channels in bf16, with the division above: 47
-// us with 256, 40 with 512, 43 with 1024: shorter runs form more of their neighbours' e and leave more
-// shares)
+// (backward of 16384 tokens, inputs in cache / not, us with 256, 512 and 1024
+// workgroups: 1024 channels in bf16 42/52, 33/39, 35/38, of width 8 56/64,
+// 48/53, 60/68, in fp32 53/63, 44/50, 49/56; 4096 channels in bf16 185/186,
+// 121/122, 102/104: shorter runs form more of their neighbours' e and leave
+// more shares)
 constexpr int64_t kFwdBlocks = 4096, kBwdBlocks = 512;
 
 template <typename F>

@@ -15,7 +15,9 @@
 // in LDS.  There is no product of two shared matrices here (the decay differs
 // in every channel and state), so nothing for the matrix cores: the vector
 // unit's exponential, two multiplications and two multiply-adds for every
-// token, channel and state bound the walks.
+// token, channel and state bound the walks.  A group of fewer than 64 channels
+// leaves lanes idle: 4096 tokens of 128 heads of 16 channels take 207 us with
+// rows of b and c for each head, 74 with one for all.
 //
 // Few or long sequences are cut into segments walked by workgroups of their
 // own: one launch walks every segment from zero and leaves its last state and
@@ -64,9 +66,11 @@ __device__ inline float softplus(float v) {
   return __builtin_elementwise_maximum(v, 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), u - (w - 1.f));
 }
 
-// bf16 rows take the exponential as it is (its error, |v| 2^-24, is far below
-// their rounding).  Zero from about -89 down, so that v times it is none of
-// the type's lowest value; of a NaN it is anything, its users keep the NaN.
+// bf16 rows take the exponential as it is: its error, |v| 2^-24, is far below
+// the rounding of rows in bf16, and in the fp32 sums da, dd and dt_bias's
+// gradient the size of a term's own rounding.  Zero from about -89 down, so
+// that v times it is none of the type's lowest value; of a NaN it is anything,
+// its users keep the NaN.
 template <typename IO>
 __device__ inline float sigmoid(float v) {
   const float e = io<IO>::bytes == 2 ? __builtin_amdgcn_exp2f(-v * kLog2e)
@@ -1236,10 +1240,17 @@ Plan plan_scan(const Scan& p) {
   };
   split();
   // Segments: eight waves a SIMD to choose from hide the loads (forward of
-  // 16384 packed tokens of 4096 channels: 440 us with four, 429 with six, 409),
-  // but not below half the square root of the tokens, where the chaining takes
-  // over (4096 tokens of 2048 channels: 86 us from a quarter, 75 from half, 80
-  // from the whole root); no cut where one walk takes less than three launches.
+  // 16384 packed tokens of 4096 channels: 428 us with four, 419 with six, 402;
+  // of 65536 tokens of 2048: 825, 814, 780; backward of 16384 of 4096: 1267,
+  // 1289, 1260, but of 8 x 2048 of 1024 376, 411, 388), but not below half the
+  // square root of the tokens, where the chaining takes over (4096 tokens of
+  // 2048 channels: 86 us from a quarter, 74 from half, 77 from the whole root).
+  // Up to 96 tokens stay whole: batches fill the machine by themselves (64
+  // sequences of 96 tokens of 128 channels: 26.5 us, in segments of 16 39.2;
+  // backward 86 and 89), and a short sequence takes less than three launches
+  // (64 tokens of 32 channels 17.3 us, cut 18.3).  One sequence alone would gain
+  // from about 80 tokens on (96: 24.4 and 18.5), its backward from 32 on (64:
+  // 58 and 31, 96: 82 and 31).
   int64_t L;
   if (p.seg_req < 0) {
     L = q.len;
