@@ -63,7 +63,8 @@ __device__ inline float exp_full(float x) {
 // the least step times the lowest finite rate is a decay of zero (rate_of).
 __device__ inline float softplus(float v) {
   const float u = exp_full(fmaxf(-fabsf(v), -83.f)), w = 1.f + u;
-  return __builtin_elementwise_maximum(v, 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), u - (w - 1.f));
+  return __builtin_elementwise_maximum(v, 0.f) +
+         fmaf(kLn2, __builtin_amdgcn_logf(w), u - (w - 1.f));
 }
 
 // bf16 rows take the exponential as it is: its error, |v| 2^-24, is far below

@@ -528,9 +528,9 @@ gdn_status gdn_group_norm_bwd(const gdn_problem* p, int32_t d, int32_t act, int3
  *   ws        : at least gdn_selective_scan_fwd_workspace bytes; calls that
  *               overlap in time (streams, captured graphs) need one each.
  * All arithmetic is fp32, the state too.  Rows of packed tensors in front of
- * cu_seqlens[0] and behind cu_seqlens[nseq] are neither read nor written.  A NaN or infinity in a
- * token stays in its sequence.  Deterministic.  Errors as gdn_chunk_fwd;
- * GDN_ERR_SHAPE where a launch would take 2^32 threads. */
+ * cu_seqlens[0] and behind cu_seqlens[nseq] are neither read nor written.  A
+ * NaN or infinity in a token stays in its sequence.  Deterministic.  Errors as
+ * gdn_chunk_fwd; GDN_ERR_SHAPE where a launch would take 2^32 threads. */
 gdn_status gdn_selective_scan_fwd_workspace(const gdn_problem* p, int32_t hb, size_t* bytes);
 gdn_status gdn_selective_scan_fwd(const gdn_problem* p, int32_t hb, int32_t softplus,
                                   const void* x, const void* dt, const float* a, const void* b,
@@ -579,7 +579,8 @@ gdn_status gdn_selective_scan_step(const gdn_problem* p, int32_t hb, int32_t sof
  *               width - 1 inputs, oldest first; s0 NULL = zeros, s_final NULL
  *               to skip it.
  * No output may overlap an input or the other output: y not x, s_final not s0.
- * Rows behind cu_seqlens[nseq] are neither read nor written. */
+ * Rows in front of cu_seqlens[0] and behind cu_seqlens[nseq] are neither read
+ * nor written. */
 gdn_status gdn_short_conv_fwd(const gdn_problem* p, int32_t width, int32_t act, const void* x,
                               const float* taps, const float* bias, const void* s0, void* y,
                               void* s_final, void* stream);

@@ -47,7 +47,8 @@ def test_a_draft_row_is_read_behind_a_rejection_only(tmp_path):
         pytest.skip("g++ not found")
     src, exe = tmp_path / "row.cpp", tmp_path / "row"
     src.write_text(SOURCE)
-    subprocess.run([cxx, "-O1", "-std=c++17", "-I", build.CSRC, str(src), "-o", str(exe)], check=True)
+    subprocess.run([cxx, "-O1", "-std=c++17", "-I", build.CSRC, str(src), "-o", str(exe)],
+                   check=True)
     out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split("\n")
     # the target's row; less the draft's (or a one at the token), then that
     # times 4 less it again
